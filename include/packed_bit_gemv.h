@@ -71,6 +71,7 @@ extern "C" {
 #define PBG_ERR_CODE (-4)    /* pack input held a value outside {-1, 0, +1} */
 #define PBG_ERR_HIP (-5)     /* a HIP launch or copy failed */
 #define PBG_ERR_WORKSPACE (-6) /* a workspace is smaller than the call needs */
+#define PBG_ERR_VALUE (-7)   /* a scalar argument is out of range */
 
 /* Limits: 1 <= n <= PBG_MAX_N, 1 <= k <= PBG_MAX_K, 1 <= m <= PBG_MAX_M. */
 #define PBG_MAX_N 16777216LL
@@ -395,6 +396,127 @@ int ternary3_ffn_swiglu_small(const uint32_t* gate_packed, const float* gate_sca
                               const float* up_scale, const uint32_t* down_packed, const float* down_scale,
                               int64_t d_model, int64_t d_ff, const uint16_t* x, int64_t m, uint16_t* h, float* y,
                               hipStream_t stream);
+
+/*
+ * The 8-bit activation path: rows of int8 codes with an fp32 scale per row,
+ * standing for q_scale[i] * q[i][j]. Products of such rows with a packed
+ * ternary matrix are sums of whole numbers, exact in int32, and run for any
+ * number of rows: one decoded token, a verify step, a batch of sequences, a
+ * prompt. A row of k codes takes pbg_q8_row_bytes(k) = 64 * ceil(k / 64)
+ * bytes (the columns of whole 16-byte weight chunks); add_rmsnorm and
+ * quantize_rows write the bytes past k as 0, and readers ignore them.
+ * Limits of the entry points below: 1 <= m <= PBG_MAX_ROWS rows,
+ * 1 <= k <= PBG_I8_MAX_K columns (128 * 64 * k stays below 2^31), and
+ * m * n <= PBG_MAX_OUTPUTS outputs.
+ * Source: Neutrino-1 8B model page, "Where the bytes live" (ternary codes with
+ * per-row scales; fp32 norm weights) and geometry table (norm epsilon 1e-6,
+ * widths).
+ */
+#define PBG_MAX_ROWS 1048576LL
+#define PBG_I8_MAX_K 131072LL
+#define PBG_MAX_OUTPUTS (1LL << 36)
+
+/* Bytes of an 8-bit row of k codes: 64 * ceil(k / 64); 0 if k <= 0. */
+int64_t pbg_q8_row_bytes(int64_t k);
+
+/*
+ * add_rmsnorm - the step between two linears: adds a linear's output to the
+ * residual stream and norms the sum, for the fp16 linears, the 8-bit ones, or
+ * both:
+ *   r[i][j] = x[i][j] + residual[i][j]
+ *   g_i     = 1 / sqrt(sum_j r[i][j]^2 / k + eps)
+ *   h[i][j] = fp16(r[i][j] * weight[j] * g_i)       (overflow to +-inf)
+ *   q[i][j] = rint(p * (127 * (1 / A))), p = r[i][j] * weight[j], A = max_j |p|
+ *   q_scale[i] = A * g_i / 127
+ * Each code is the result of single fp32 operations (g_i cancels in it), so
+ * codes are the same bits whatever the order of the sum. A row with A < 2^-100
+ * has codes 0 and scale 0. A row that holds NaN or an infinity, or whose sum
+ * of squares overflows fp32, has codes 0 and scale NaN.
+ *
+ *   x         [m][k] fp32, 4-byte aligned
+ *   residual  [m][k] fp32, or NULL: r = x
+ *   weight    [k] fp32
+ *   eps       > 0, finite (else PBG_ERR_VALUE)
+ *   residual_out  [m][k] fp32 out: r; NULL if not wanted; may be x or residual
+ *             itself (in place), and must not overlap them otherwise
+ *   h         [m][k] fp16 bits out, 2-byte aligned, or NULL
+ *   q         [m][pbg_q8_row_bytes(k)] int8 out, 16-byte aligned, or NULL
+ *   q_scale   [m] fp32 out; NULL exactly if q is
+ * At least one of h and q is required.
+ */
+int add_rmsnorm(const float* x, const float* residual, const float* weight, float eps, int64_t m, int64_t k,
+                float* residual_out, uint16_t* h, int8_t* q, float* q_scale, hipStream_t stream);
+
+/*
+ * quantize_rows - 8-bit form of fp16 rows that no norm precedes (the attention
+ * output, the SwiGLU activations): A = max_j |x[i][j]|, q = rint(x * (127 *
+ * (1 / A))), q_scale[i] = A / 127, in fp32; rows of zeros and non-finite rows
+ * as add_rmsnorm.
+ *   x  [m][k] fp16 bits, 2-byte aligned; q, q_scale as add_rmsnorm
+ */
+int quantize_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* q, float* q_scale, hipStream_t stream);
+
+/*
+ * ternary_gemm_i8 - Y[i][r] = q_scale[i] * scale[r] * sum_j c[r][j] * q[i][j]
+ * for any number of 8-bit activation rows. The sum is exact; the two scales
+ * are applied in fp32 afterwards, so the result does not depend on the split
+ * of the work and is the same bits on every call.
+ *   packed, scale, n  as ternary_gemv
+ *   q        [m][pbg_q8_row_bytes(k)] int8, 16-byte aligned; the full range
+ *            -128..127 is taken; bytes past column k - 1 may hold anything
+ *   q_scale  [m] fp32, 4-byte aligned
+ *   y        [m][n] fp32 out, 4-byte aligned
+ */
+int ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
+                    const float* q_scale, int64_t m, float* y, hipStream_t stream);
+
+/*
+ * ternary_swiglu_gate_up_i8 - ternary_swiglu_gate_up_small on 8-bit rows, any
+ * number of them: h[i][j] = fp16(silu(g) * u) with g and u the ternary_gemm_i8
+ * outputs of the gate and up rows j; g and u never reach memory.
+ *   gate_packed, gate_scale, up_packed, up_scale  as ternary_ffn_swiglu
+ *   q, q_scale  as ternary_gemm_i8 with k = d_model <= PBG_I8_MAX_K
+ *   h        [m][d_ff] fp16 bits out, 2-byte aligned
+ */
+int ternary_swiglu_gate_up_i8(const uint32_t* gate_packed, const float* gate_scale, const uint32_t* up_packed,
+                              const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
+                              const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream);
+
+/*
+ * lora_add - low-rank adapters of many requests at once beside a shared
+ * projection: with t = ids[i],
+ *   out[i][r] = y[i][r] + scale[t] * sum_l b[t][r][l] * (sum_j a[t][l][j] * x[i][j])
+ * y being the shared projection's output (of a 2-bit or a 3-bit linear). Rows
+ * whose id is outside [0, adapters) have no adapter: out[i] = y[i]. Rows may
+ * come in any order and mix; an adapter's weights are read for its own rows
+ * only, so what another request's adapter holds (NaN included) does not reach
+ * them. The inner sums of length `rank` keep 22 bits or more of each value;
+ * accumulation is fp32.
+ *   y      [m][n] fp32, 4-byte aligned
+ *   x      [m][k] fp16 bits, 2-byte aligned, finite
+ *   ids    [m] int32, 4-byte aligned
+ *   a      [adapters][rank][k] fp16 bits, 2-byte aligned
+ *   b      [adapters][n][rank] fp16 bits, 2-byte aligned
+ *   scale  [adapters] fp32, 4-byte aligned (commonly alpha / rank)
+ *   adapters  1 .. PBG_LORA_MAX_ADAPTERS
+ *   rank   1 .. PBG_LORA_MAX_RANK; adapters of a lower rank are stored with
+ *          zero rows in a or zero columns in b
+ *   out    [m][n] fp32 out; may be y itself, and must not overlap it otherwise
+ *   workspace  device, 16-byte aligned, pbg_lora_workspace_bytes(m, rank)
+ *          bytes, of any content; calls that overlap in time need separate
+ *          workspaces
+ * k a multiple of 8, rank a multiple of 8 and 16-byte aligned x, a and b take
+ * the fast loads.
+ */
+#define PBG_LORA_MAX_RANK 128
+#define PBG_LORA_MAX_ADAPTERS 65536
+
+/* Workspace of lora_add for m rows; 0 for m or rank out of range. */
+int64_t pbg_lora_workspace_bytes(int64_t m, int64_t rank);
+
+int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
+             const float* scale, int64_t m, int64_t n, int64_t k, int64_t adapters, int64_t rank, float* out,
+             void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
  * pbg_stream_read - measurement helper, not a step of the decode path: reads

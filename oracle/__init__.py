@@ -428,3 +428,60 @@ def ffn3_swiglu(gate_packed: np.ndarray, gate_scale: np.ndarray, up_packed: np.n
     h = (silu(g) * u).astype(np.float16)
     y = ternary3_gemm_small(down_packed, down_scale, d_ff, h)
     return h, y
+
+
+# ---- 8-bit activation rows and adapters -----------------------------------
+
+TINY_ROW = np.float32(2.0 ** -100)
+
+
+def row_codes(p: np.ndarray):
+    """8-bit codes of fp32 rows p [m, k]: (q int8 [m, k], A fp32 [m]), A = max_j |p_j| and
+    q = rint(p * (127 * (1 / A))) in fp32; rows with A < 2^-100 have codes 0 and A 0, rows
+    with NaN or an infinity codes 0 and A NaN."""
+    p = np.asarray(p)
+    if p.dtype != np.float32 or p.ndim != 2:
+        raise ValueError("rows must be fp32 [m, k]")
+    bad = ~np.isfinite(p).all(axis=1)
+    top = np.abs(np.where(bad[:, None], np.float32(0), p)).max(axis=1)
+    some = top >= TINY_ROW
+    f = np.float32(127) * (np.float32(1) / np.where(some, top, np.float32(1)))
+    q = np.rint(np.where(some[:, None], p, np.float32(0)) * f[:, None]).astype(np.int8)
+    return q, np.where(bad, np.float32(np.nan), np.where(some, top, np.float32(0)))
+
+
+def quantize_rows(x: np.ndarray):
+    """8-bit form of fp16 rows: (q int8 [m, k], q_scale fp64 [m])."""
+    if x.dtype != np.float16:
+        raise ValueError("x must be fp16")
+    q, top = row_codes(x.astype(np.float32))
+    return q, top.astype(np.float64) / 127.0
+
+
+def add_rmsnorm(x: np.ndarray, weight: np.ndarray, eps: float, residual: np.ndarray | None = None):
+    """(r fp32, h fp64, q int8, q_scale fp64) of r = x + residual, h = r w / sqrt(mean r^2 + eps); the
+    codes are those of the fp32 products r w."""
+    r = x if residual is None else x + residual
+    with np.errstate(over="ignore", invalid="ignore"):
+        p = r * weight
+        g = 1.0 / np.sqrt(np.square(r.astype(np.float64)).mean(axis=1) + eps)
+        q, top = row_codes(p)
+        h = r.astype(np.float64) * weight.astype(np.float64) * g[:, None]
+    return r, h, q, top.astype(np.float64) * g / 127.0
+
+
+def ternary_gemm_i8(packed: np.ndarray, scale: np.ndarray, k: int, q: np.ndarray, q_scale: np.ndarray) -> np.ndarray:
+    """Y[i, r] = q_scale_i * s_r * sum_j c_rj q_ij in fp64 (the sum is a whole number below 2^24)."""
+    c = unpack(packed, k).astype(np.float64)
+    return (q[:, :k].astype(np.float64) @ c.T) * q_scale.astype(np.float64)[:, None] * scale.astype(np.float64)[None, :]
+
+
+def lora_add(y: np.ndarray, x: np.ndarray, ids: np.ndarray, a: np.ndarray, b: np.ndarray,
+             scale: np.ndarray) -> np.ndarray:
+    """out_i = y_i + s_t b_t (a_t x_i) in fp64 with t = ids_i; y_i where t is not an adapter."""
+    out = y.astype(np.float64)
+    for i, t in enumerate(ids):
+        if 0 <= t < a.shape[0]:
+            v = a[t].astype(np.float64) @ x[i].astype(np.float64)
+            out[i] += float(scale[t]) * (b[t].astype(np.float64) @ v)
+    return out

@@ -52,6 +52,14 @@ _SIGNATURES = {
     "ternary3_swiglu_gate_up": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _c_i64, _vp, _vp, _vp]),
     "ternary3_ffn_swiglu": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _vp, _vp, _vp, _vp]),
     "ternary3_swiglu_gate_up_small": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp]),
+    "pbg_q8_row_bytes": (_c_i64, [_c_i64]),
+    "add_rmsnorm": (_c_int, [_vp, _vp, _vp, ctypes.c_float, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp]),
+    "quantize_rows": (_c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _vp]),
+    "ternary_gemm_i8": (_c_int, [_vp, _vp, _c_i64, _c_i64, _vp, _vp, _c_i64, _vp, _vp]),
+    "ternary_swiglu_gate_up_i8": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _c_i64, _vp, _vp, _c_i64, _vp, _vp]),
+    "pbg_lora_workspace_bytes": (_c_i64, [_c_i64, _c_i64]),
+    "lora_add": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i64,
+                          _vp]),
     "pbg_stream_read": (_c_int, [_vp, _c_i64, _vp, _vp]),
 }
 
@@ -513,6 +521,161 @@ def ternary3_ffn_swiglu(gate: torch.Tensor, gate_scale: torch.Tensor, up: torch.
                         h: torch.Tensor | None = None, y: torch.Tensor | None = None):
     """ternary_ffn_swiglu with the three linears in the 3-bit layout (rows of words_per_row3 words)."""
     return _ffn_swiglu("ternary3", words_per_row3, gate, gate_scale, up, up_scale, down, down_scale, x, h, y)
+
+
+def q8_row_bytes(k: int) -> int:
+    """Bytes of an 8-bit activation row of k codes (64 * ceil(k / 64))."""
+    return 0 if k <= 0 else 64 * ((int(k) + 63) // 64)
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """Call a C entry point on dev's current stream, whatever the current device is."""
+    if dev.index == torch.cuda.current_device():
+        rc = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != 0:
+        _check(name, rc)
+
+
+def _on(dev: torch.device, t, name: str, dtype: torch.dtype, shape: tuple) -> int:
+    """Address of t after checking that it is a contiguous dtype tensor of that shape on dev."""
+    _dev(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    return t.data_ptr()
+
+
+def _matrix(t, name: str, dtype: torch.dtype) -> tuple[int, int]:
+    _dev(t, name, dtype)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return t.shape
+
+
+def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                residual_out: torch.Tensor | None = None, h: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                q_scale: torch.Tensor | None = None, want: str | None = None):
+    """Residual addition and root-mean-square norm of fp32 rows x [m, k]: (residual_out, h, q, q_scale).
+
+    r = x + residual goes to residual_out, which may be x or residual for an update in place; without
+    a residual r is x, which is returned itself unless residual_out is given. h is the normed row in fp16 [m, k]; q int8 [m, q8_row_bytes(k)] and q_scale fp32
+    [m] are the same row in 8 bits. Outputs are the tensors given; `want` ("h", "q" or "hq") allocates
+    those of its letters that are not. With neither, h is allocated. Outputs not asked for are None.
+    """
+    m, k = _matrix(x, "x", torch.float32)
+    dev = x.device
+    if want is None:
+        want = "h" if h is None and q is None and q_scale is None else ""
+    elif want not in ("h", "q", "hq"):
+        raise ValueError('want must be "h", "q" or "hq"')
+    if residual_out is None and residual is not None:
+        residual_out = torch.empty_like(x)
+    if h is None and "h" in want:
+        h = torch.empty((m, k), dtype=torch.float16, device=dev)
+    if "q" in want or q is not None or q_scale is not None:
+        if q is None:
+            q = torch.empty((m, q8_row_bytes(k)), dtype=torch.int8, device=dev)
+        if q_scale is None:
+            q_scale = torch.empty((m,), dtype=torch.float32, device=dev)
+    _call("add_rmsnorm", dev, x.data_ptr(),
+          None if residual is None else _on(dev, residual, "residual", torch.float32, (m, k)),
+          _on(dev, weight, "weight", torch.float32, (k,)), eps, m, k,
+          None if residual_out is None else _on(dev, residual_out, "residual_out", torch.float32, (m, k)),
+          None if h is None else _on(dev, h, "h", torch.float16, (m, k)),
+          None if q is None else _on(dev, q, "q", torch.int8, (m, q8_row_bytes(k))),
+          None if q is None else _on(dev, q_scale, "q_scale", torch.float32, (m,)))
+    return x if residual_out is None else residual_out, h, q, q_scale
+
+
+def quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None, q_scale: torch.Tensor | None = None):
+    """8-bit form of fp16 rows x [m, k]: (q int8 [m, q8_row_bytes(k)], q_scale fp32 [m]), x ~ q_scale * q."""
+    m, k = _matrix(x, "x", torch.float16)
+    dev = x.device
+    if q is None:
+        q = torch.empty((m, q8_row_bytes(k)), dtype=torch.int8, device=dev)
+    if q_scale is None:
+        q_scale = torch.empty((m,), dtype=torch.float32, device=dev)
+    _call("quantize_rows", dev, x.data_ptr(), m, k, _on(dev, q, "q", torch.int8, (m, q8_row_bytes(k))),
+          _on(dev, q_scale, "q_scale", torch.float32, (m,)))
+    return q, q_scale
+
+
+def ternary_gemm_i8(packed: torch.Tensor, scale: torch.Tensor, k: int, q: torch.Tensor, q_scale: torch.Tensor,
+                    y: torch.Tensor | None = None) -> torch.Tensor:
+    """Y[i, r] = q_scale[i] * scale[r] * sum_j c[r, j] * q[i, j], exact sums, any number of rows.
+
+    q int8 [m, q8_row_bytes(k)] and q_scale fp32 [m] as add_rmsnorm and quantize_rows leave them; Y fp32 [m, n].
+    """
+    n, words = _matrix(packed, "packed", torch.int32)
+    m, _ = _matrix(q, "q", torch.int8)
+    dev = packed.device
+    kp = q8_row_bytes(k)
+    if words != kp // 16:
+        raise ValueError(f"packed must be [n, {kp // 16}] for k={k}")
+    if y is None:
+        y = torch.empty((m, n), dtype=torch.float32, device=dev)
+    _call("ternary_gemm_i8", dev, packed.data_ptr(), _on(dev, scale, "scale", torch.float32, (n,)), n, k,
+          _on(dev, q, "q", torch.int8, (m, kp)), _on(dev, q_scale, "q_scale", torch.float32, (m,)), m,
+          _on(dev, y, "y", torch.float32, (m, n)))
+    return y
+
+
+def ternary_swiglu_gate_up_i8(gate: torch.Tensor, gate_scale: torch.Tensor, up: torch.Tensor, up_scale: torch.Tensor,
+                              d_model: int, q: torch.Tensor, q_scale: torch.Tensor,
+                              h: torch.Tensor | None = None) -> torch.Tensor:
+    """h = fp16(silu(gate q) * up q) for 8-bit rows q [m, q8_row_bytes(d_model)]; h fp16 [m, d_ff]."""
+    d_ff, words = _matrix(gate, "gate", torch.int32)
+    m, _ = _matrix(q, "q", torch.int8)
+    dev = gate.device
+    kp = q8_row_bytes(d_model)
+    if words != kp // 16:
+        raise ValueError(f"gate and up must be [d_ff, {kp // 16}]")
+    if h is None:
+        h = torch.empty((m, d_ff), dtype=torch.float16, device=dev)
+    _call("ternary_swiglu_gate_up_i8", dev, gate.data_ptr(), _on(dev, gate_scale, "gate_scale", torch.float32, (d_ff,)),
+          _on(dev, up, "up", torch.int32, (d_ff, words)), _on(dev, up_scale, "up_scale", torch.float32, (d_ff,)),
+          d_model, d_ff, _on(dev, q, "q", torch.int8, (m, kp)), _on(dev, q_scale, "q_scale", torch.float32, (m,)), m,
+          _on(dev, h, "h", torch.float16, (m, d_ff)))
+    return h
+
+
+def lora_workspace(m: int, rank: int, device) -> torch.Tensor:
+    """A workspace for lora_add on m rows (its contents do not matter)."""
+    return torch.empty((int(lib().pbg_lora_workspace_bytes(int(m), int(rank))),), dtype=torch.uint8, device=device)
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, ids: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+             scale: torch.Tensor, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """out[i] = y[i] + scale[t] * b[t] @ (a[t] @ x[i]) with t = ids[i]; rows with t outside [0, adapters) are copied.
+
+    y, out fp32 [m, n] (out may be y); x fp16 [m, k]; ids int32 [m]; a fp16 [adapters, rank, k];
+    b fp16 [adapters, n, rank]; scale fp32 [adapters]; workspace from lora_workspace(m, rank) or any
+    larger tensor (a new one is allocated if not given).
+    """
+    m, n = _matrix(y, "y", torch.float32)
+    _, k = _matrix(x, "x", torch.float16)
+    dev = y.device
+    _dev(a, "a", torch.float16)
+    if a.dim() != 3:
+        raise ValueError("a must be [adapters, rank, k]")
+    adapters, rank, _ = a.shape
+    if out is None:
+        out = torch.empty_like(y)
+    if workspace is None:
+        workspace = lora_workspace(m, rank, dev)
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    _call("lora_add", dev, y.data_ptr(), _on(dev, x, "x", torch.float16, (m, k)),
+          _on(dev, ids, "ids", torch.int32, (m,)), _on(dev, a, "a", torch.float16, (adapters, rank, k)),
+          _on(dev, b, "b", torch.float16, (adapters, n, rank)), _on(dev, scale, "scale", torch.float32, (adapters,)),
+          m, n, k, adapters, rank, _on(dev, out, "out", torch.float32, (m, n)), workspace.data_ptr(),
+          workspace.nbytes)
+    return out
 
 
 def stream_read(src: torch.Tensor, sink: torch.Tensor | None = None) -> torch.Tensor:

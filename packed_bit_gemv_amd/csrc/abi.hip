@@ -15,6 +15,11 @@ bool bad_ffn(int64_t d_model, int64_t d_ff) {
   return d_model < 8 || d_model > PBG_FFN_MAX_MODEL || d_model % 8 != 0 || bad_nk(d_ff, d_model);
 }
 
+// Rows of the 8-bit path: m x k within the limits of one launch and of an exact int32 sum.
+bool bad_rows(int64_t m, int64_t k) { return m < 1 || m > PBG_MAX_ROWS || k < 1 || k > PBG_I8_MAX_K; }
+
+bool bad_outputs(int64_t m, int64_t n) { return n < 1 || n > PBG_MAX_N || m * n > PBG_MAX_OUTPUTS; }
+
 // True when earlier work on this thread left a HIP error pending. Such an
 // error is the caller's: it is left in place (not cleared) and the call
 // enqueues nothing. hipErrorNotReady from a completion query is a status,
@@ -49,6 +54,7 @@ const char* pbg_strerror(int code) {
     case PBG_ERR_ALIGN: return "a pointer lacks its required alignment";
     case PBG_ERR_CODE: return "pack input held a value outside {-1, 0, +1}";
     case PBG_ERR_HIP: return "a HIP launch or copy failed";
+    case PBG_ERR_VALUE: return "a scalar argument is out of range";
     case PBG_ERR_WORKSPACE: return "workspace smaller than the call needs";
     default: return "unknown error code";
   }
@@ -178,6 +184,73 @@ int int8_embedding_gather(const int8_t* table, const float* scale, int64_t n, in
   if (misaligned(scale, 4) || misaligned(tokens, 4) || misaligned(out, 4)) return PBG_ERR_ALIGN;
   if (pending_error()) return PBG_ERR_HIP;
   return finish(pbg::launch_embedding_gather(table, scale, n, k, tokens, m, out, stream));
+}
+
+int64_t pbg_q8_row_bytes(int64_t k) { return pbg::q8_row_bytes(k); }
+
+int add_rmsnorm(const float* x, const float* residual, const float* weight, float eps, int64_t m, int64_t k,
+                float* residual_out, uint16_t* h, int8_t* q, float* q_scale, hipStream_t stream) {
+  if (!x || !weight || (!h && !q) || (q == nullptr) != (q_scale == nullptr)) return PBG_ERR_NULL;
+  if (bad_rows(m, k)) return PBG_ERR_SHAPE;
+  if (misaligned(x, 4) || misaligned(residual, 4) || misaligned(weight, 4) || misaligned(residual_out, 4) ||
+      misaligned(h, 2) || misaligned(q, 16) || misaligned(q_scale, 4))
+    return PBG_ERR_ALIGN;
+  if (!(eps > 0.0f && eps < __builtin_inff())) return PBG_ERR_VALUE;
+  if (pending_error()) return PBG_ERR_HIP;
+  return finish(pbg::launch_add_rmsnorm(x, residual, weight, eps, m, k, residual_out, h, q, q_scale, stream));
+}
+
+int quantize_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* q, float* q_scale, hipStream_t stream) {
+  if (!x || !q || !q_scale) return PBG_ERR_NULL;
+  if (bad_rows(m, k)) return PBG_ERR_SHAPE;
+  if (misaligned(x, 2) || misaligned(q, 16) || misaligned(q_scale, 4)) return PBG_ERR_ALIGN;
+  if (pending_error()) return PBG_ERR_HIP;
+  return finish(pbg::launch_quantize_rows(x, m, k, q, q_scale, stream));
+}
+
+int ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
+                    const float* q_scale, int64_t m, float* y, hipStream_t stream) {
+  if (!packed || !scale || !q || !q_scale || !y) return PBG_ERR_NULL;
+  if (bad_rows(m, k) || bad_outputs(m, n)) return PBG_ERR_SHAPE;
+  if (misaligned(packed, 16) || misaligned(scale, 4) || misaligned(q, 16) || misaligned(q_scale, 4) ||
+      misaligned(y, 4))
+    return PBG_ERR_ALIGN;
+  if (pending_error()) return PBG_ERR_HIP;
+  return finish(pbg::launch_ternary_gemm_i8(packed, scale, n, k, q, q_scale, m, y, stream));
+}
+
+int ternary_swiglu_gate_up_i8(const uint32_t* gate_packed, const float* gate_scale, const uint32_t* up_packed,
+                              const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
+                              const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream) {
+  if (!gate_packed || !gate_scale || !up_packed || !up_scale || !q || !q_scale || !h) return PBG_ERR_NULL;
+  if (bad_rows(m, d_model) || bad_outputs(m, d_ff)) return PBG_ERR_SHAPE;
+  if (misaligned(gate_packed, 16) || misaligned(up_packed, 16) || misaligned(gate_scale, 4) ||
+      misaligned(up_scale, 4) || misaligned(q, 16) || misaligned(q_scale, 4) || misaligned(h, 2))
+    return PBG_ERR_ALIGN;
+  if (pending_error()) return PBG_ERR_HIP;
+  return finish(pbg::launch_swiglu_gate_up_i8(gate_packed, gate_scale, up_packed, up_scale, d_model, d_ff, q, q_scale,
+                                              m, h, stream));
+}
+
+int64_t pbg_lora_workspace_bytes(int64_t m, int64_t rank) {
+  if (m < 1 || m > PBG_MAX_ROWS || rank < 1 || rank > PBG_LORA_MAX_RANK) return 0;
+  return 4 * m * rank * pbg::lora_slices(m);
+}
+
+int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
+             const float* scale, int64_t m, int64_t n, int64_t k, int64_t adapters, int64_t rank, float* out,
+             void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (!y || !x || !ids || !a || !b || !scale || !out || !workspace) return PBG_ERR_NULL;
+  if (bad_rows(m, k) || bad_outputs(m, n) || adapters < 1 || adapters > PBG_LORA_MAX_ADAPTERS || rank < 1 ||
+      rank > PBG_LORA_MAX_RANK)
+    return PBG_ERR_SHAPE;
+  if (misaligned(y, 4) || misaligned(x, 2) || misaligned(ids, 4) || misaligned(a, 2) || misaligned(b, 2) ||
+      misaligned(scale, 4) || misaligned(out, 4) || misaligned(workspace, 16))
+    return PBG_ERR_ALIGN;
+  if (workspace_bytes < pbg_lora_workspace_bytes(m, rank)) return PBG_ERR_WORKSPACE;
+  if (pending_error()) return PBG_ERR_HIP;
+  return finish(pbg::launch_lora_add(y, x, ids, a, b, scale, m, n, k, static_cast<int>(adapters),
+                                     static_cast<int>(rank), out, static_cast<float*>(workspace), stream));
 }
 
 int pbg_stream_read(const void* src, int64_t bytes, uint32_t* sink, hipStream_t stream) {

@@ -1,0 +1,232 @@
+// lora_add: out_i = y_i + s_a B_a (A_a x_i) with a = ids[i], the adapters of
+// many requests at once beside a shared projection; rows without an adapter
+// are passed through.
+//
+// Two launches. The first forms v_i = A_a x_i on the f16 matrix cores (fp16
+// products are exact in its fp32 sums), K split over the waves of a workgroup
+// and, for few rows, over workgroups; the slices' sums go to the workspace.
+// The second adds the slices in order and multiplies by B_a: v stays fp32 in
+// effect, split into two fp16 parts (see split_row), so that B_a can stay
+// fp16 on the matrix cores.
+//
+// Both take 16 rows at a time and run once for each different adapter among
+// them; a row takes the result of its own adapter by a select, so infinities
+// or NaN in another request's adapter never reach it.
+#include "pbg_device.hpp"
+#include "pbg_internal.hpp"
+
+namespace pbg {
+namespace {
+
+constexpr int kRows = 16;
+constexpr int kWaves = 4;
+
+// ids of a 16-row tile, -1 for rows past m and rows without an adapter (lane
+// l of every wave holds row l % 16).
+__device__ __forceinline__ int tile_id(const int32_t* __restrict__ ids, int64_t row, int64_t m, int adapters) {
+  const int id = row < m ? ids[row] : -1;
+  return id >= 0 && id < adapters ? id : -1;
+}
+
+// Bit i (0..15): row i is the tile's first one with its adapter.
+__device__ __forceinline__ uint32_t first_rows(int id) {
+  const int li = threadIdx.x & 15;
+  bool first = id >= 0;
+#pragma unroll
+  for (int j = 0; j < 15; ++j) first &= !(j < li && __builtin_amdgcn_readlane(id, j) == id);
+  return static_cast<uint32_t>(__ballot(first)) & 0xFFFFu;
+}
+
+// Eight fp16 elements p[c .. c + 7], zero from column k on.
+template <bool FAST>
+__device__ __forceinline__ mfma_half8_t load8(const uint16_t* __restrict__ p, int64_t c, int64_t k) {
+  if constexpr (FAST) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c < k) v = *reinterpret_cast<const uint4*>(p + c);
+    return __builtin_bit_cast(mfma_half8_t, v);
+  } else {
+    mfma_half8_t v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < k ? __builtin_bit_cast(_Float16, p[c + e]) : static_cast<_Float16>(0.0f);
+    return v;
+  }
+}
+
+// v[slice][row][rank]: blockIdx.x is the row tile, blockIdx.y the slice of
+// K, blockIdx.z the first of the tile's adapters (stepping by gridDim.z).
+template <int RT, bool FAST>
+__global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t* __restrict__ x,
+                                                                  const int32_t* __restrict__ ids,
+                                                                  const uint16_t* __restrict__ a, int64_t m, int64_t k,
+                                                                  int adapters, int rank, int64_t k_slice,
+                                                                  float* __restrict__ v) {
+  __shared__ mfma_float4_t part[kWaves - 1][RT][kWave];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int li = lane & 15, lg = lane >> 4;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  const int id = tile_id(ids, m0 + li, m, adapters);
+  const int64_t k0 = blockIdx.y * k_slice;
+  const int64_t k1 = k0 + k_slice < k ? k0 + k_slice : k;
+  const int64_t xr = m0 + li < m ? m0 + li : m - 1;
+  uint32_t todo = first_rows(id);
+  for (int d = 0; todo; ++d) {
+    const int f = __builtin_ctz(todo);
+    todo &= todo - 1;
+    if (d % gridDim.z != blockIdx.z) continue;
+    const int ad = __builtin_amdgcn_readlane(id, f);
+    mfma_float4_t acc[RT] = {};
+    for (int64_t c = k0 + 32 * wave + 8 * lg; c - 8 * lg < k1; c += 32 * kWaves) {
+      const mfma_half8_t xv = load8<FAST>(x + xr * k, c, k1);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int j = 16 * t + li;
+        const mfma_half8_t av = load8<FAST>(a + (static_cast<int64_t>(ad) * rank + (j < rank ? j : rank - 1)) * k, c, k1);
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv, av, acc[t], 0, 0, 0);
+      }
+    }
+    __syncthreads();
+    if (wave > 0) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) part[wave - 1][t][lane] = acc[t];
+    }
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+#pragma unroll
+        for (int w = 0; w < kWaves - 1; ++w) acc[t] += part[w][t][lane];
+        const int j = 16 * t + li;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * lg + e;  // row of the tile
+          const int idi = __shfl(id, i);
+          if (j < rank && idi == ad) v[(blockIdx.y * m + m0 + i) * rank + j] = acc[t][e];
+        }
+      }
+    }
+  }
+}
+
+// out = y + (s_a 2^-e) B_a (hi + lo): v 2^e = hi + lo in two fp16 parts.
+template <int RT, bool FAST>
+__global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, const int32_t* __restrict__ ids,
+                                                                const uint16_t* __restrict__ b,
+                                                                const float* __restrict__ scale, int64_t m, int64_t n,
+                                                                int adapters, int rank, int slices, int64_t n_blocks,
+                                                                const float* __restrict__ v, float* out) {
+  constexpr int RP = 16 * RT;
+  __shared__ float vs[kRows][RP + 1];
+  __shared__ float back[kRows];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int li = lane & 15, lg = lane >> 4;
+  const int64_t m0 = blockIdx.x / n_blocks * kRows;
+  const int id = tile_id(ids, m0 + li, m, adapters);
+  for (int e = threadIdx.x; e < kRows * RP; e += kWaves * kWave) {
+    const int i = e / RP, j = e % RP;
+    const int idi = __shfl(id, i);
+    float s = 0.0f;
+    if (idi >= 0 && j < rank)
+      for (int p = 0; p < slices; ++p) s += v[(p * m + m0 + i) * rank + j];
+    vs[i][j] = s;
+  }
+  __syncthreads();
+  // The row's largest |v| is brought to [2^13, 2^14) by a power of two: both
+  // fp16 parts then hold v to 2^-22 of itself, or 2^-38 of the row's largest.
+  if (threadIdx.x < kRows) {
+    float top = 0.0f;
+    for (int j = 0; j < RP; ++j) top = fmaxf(top, fabsf(vs[threadIdx.x][j]));
+    int e = 0;
+    if (top > 0.0f && top < __builtin_inff()) e = 13 - ilogbf(top);
+    const float f = ldexpf(1.0f, e);
+    for (int j = 0; j < RP; ++j) vs[threadIdx.x][j] *= f;
+    back[threadIdx.x] = id >= 0 ? ldexpf(scale[id], -e) : 0.0f;
+  }
+  __syncthreads();
+  // Matrix-core operand of the rows: element e of lane (li, lg), step t, is
+  // part lg / 2 (hi, lo) of v[li][16 t + 8 (lg % 2) + e].
+  mfma_half8_t vf[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float s = vs[li][16 * t + 8 * (lg & 1) + e];
+      const _Float16 hi = static_cast<_Float16>(s);
+      vf[t][e] = lg < 2 ? hi : static_cast<_Float16>(s - static_cast<float>(hi));
+    }
+  const float bk = back[li];
+  const int64_t n0 = (blockIdx.x % n_blocks * kWaves + wave) * 16;
+  if (n0 >= n) return;
+  mfma_float4_t acc = {};
+  const int64_t br = n0 + li < n ? n0 + li : n - 1;
+  for (uint32_t todo = first_rows(id); todo; todo &= todo - 1) {
+    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+    mfma_float4_t d = {};
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const mfma_half8_t bv = load8<FAST>(b + (static_cast<int64_t>(ad) * n + br) * rank, 16 * t + 8 * (lg & 1), rank);
+      d = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv, vf[t], d, 0, 0, 0);
+    }
+    if (id == ad) acc = d;
+  }
+  // lane: row m0 + li, columns n0 + 4 lg ..
+  if (m0 + li < m) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t r = n0 + 4 * lg + e;
+      if (r >= n) continue;
+      const float base = y[(m0 + li) * n + r];
+      out[(m0 + li) * n + r] = id >= 0 ? base + bk * acc[e] : base;
+    }
+  }
+}
+
+// Columns of one slice: whole steps of the down kernel's four waves.
+int64_t slice_columns(int64_t k, int slices) {
+  const int64_t step = 32 * kWaves;
+  return ((k + slices - 1) / slices + step - 1) / step * step;
+}
+
+template <int RT, bool FAST>
+void launch(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
+            const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out, float* ws,
+            hipStream_t stream) {
+  const int64_t tiles = (m + kRows - 1) / kRows;
+  const int64_t ks = slice_columns(k, lora_slices(m));
+  const int slices = static_cast<int>((k + ks - 1) / ks);
+  const unsigned dz = tiles <= 32 ? 16 : 1;
+  hipLaunchKernelGGL((lora_down_kernel<RT, FAST>), dim3(static_cast<unsigned>(tiles), slices, dz),
+                     dim3(kWaves * kWave), 0, stream, x, ids, a, m, k, adapters, rank, ks, ws);
+  const int64_t nb = (n + 16 * kWaves - 1) / (16 * kWaves);
+  hipLaunchKernelGGL((lora_up_kernel<RT, FAST>), dim3(static_cast<unsigned>(nb * tiles)), dim3(kWaves * kWave), 0, stream,
+                     y, ids, b, scale, m, n, adapters, rank, slices, nb, ws, out);
+}
+
+template <bool FAST>
+void launch_rank(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
+                 const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out, float* ws,
+                 hipStream_t stream) {
+  if (rank <= 16) launch<1, FAST>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
+  else if (rank <= 32) launch<2, FAST>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
+  else if (rank <= 64) launch<4, FAST>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
+  else launch<8, FAST>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
+}
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+}  // namespace
+
+int lora_slices(int64_t m) { return m <= 64 ? 16 : m <= 256 ? 4 : 1; }
+
+hipError_t launch_lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
+                           const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out,
+                           float* ws, hipStream_t stream) {
+  if (k % 8 == 0 && rank % 8 == 0 && !off16(x) && !off16(a) && !off16(b))
+    launch_rank<true>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
+  else
+    launch_rank<false>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
+  return hipGetLastError();
+}
+
+}  // namespace pbg

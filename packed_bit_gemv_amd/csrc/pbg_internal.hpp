@@ -64,6 +64,29 @@ hipError_t launch_ffn_swiglu_small(const uint32_t* gate, const float* gate_scale
                                    int64_t d_model, int64_t d_ff, const uint16_t* x, int m, uint16_t* h, float* y,
                                    hipStream_t stream);
 
+// 8-bit activation rows: k codes, padded to whole 64-byte groups.
+inline int64_t q8_row_bytes(int64_t k) { return k <= 0 ? 0 : 64 * ((k + 63) / 64); }
+
+// Any of residual, residual_out, h and (q, q_scale) may be null; residual_out may be x or residual.
+hipError_t launch_add_rmsnorm(const float* x, const float* residual, const float* weight, float eps, int64_t m,
+                              int64_t k, float* residual_out, uint16_t* h, int8_t* q, float* q_scale,
+                              hipStream_t stream);
+hipError_t launch_quantize_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* q, float* q_scale,
+                                hipStream_t stream);
+
+// Ternary products on 8-bit rows [m][q8_row_bytes(k)], any m.
+hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
+                                  const float* q_scale, int64_t m, float* y, hipStream_t stream);
+hipError_t launch_swiglu_gate_up_i8(const uint32_t* gate, const float* gate_scale, const uint32_t* up,
+                                    const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
+                                    const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream);
+
+// Adapters; ws holds lora_slices(m) * m * rank floats. out may be y.
+int lora_slices(int64_t m);
+hipError_t launch_lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
+                           const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out,
+                           float* ws, hipStream_t stream);
+
 // One read of `bytes` (a multiple of 16) from 16-byte aligned src, folded into sink.
 hipError_t launch_stream_read(const void* src, int64_t bytes, uint32_t* sink, hipStream_t stream);
 

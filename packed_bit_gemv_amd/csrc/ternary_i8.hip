@@ -1,0 +1,162 @@
+// ternary_gemm_i8 and ternary_swiglu_gate_up_i8: packed ternary matrices times
+// 8-bit activation rows, any number of rows.
+//
+// y[i][r] = q_scale_i * s_r * sum_j c_rj q_ij. Codes are decoded in registers
+// to bytes 64 * c and multiplied on the i8 matrix cores; the int32 sums are
+// exact (64 * 128 * 2^17 = 2^30), so any split of K gives the same bits.
+#include "pbg_device.hpp"
+#include "pbg_internal.hpp"
+
+namespace pbg {
+namespace {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kByteMask = 0xC0C0C0C0u;
+constexpr int kCodeShift = 6;  // decoded bytes are 64 * c
+
+// The 16 codes of a word as bytes 64 * c in column order. Code 2t + h is the
+// field at bits 16h + 14 - 2t: bytes 1 and 3 of the word hold codes 0..7
+// (even and odd ones), bytes 0 and 2 codes 8..15, highest field first. One
+// permute per half pairs the two bytes with themselves shifted by one field;
+// a shift by two fields then gives the next four codes, and the mask drops
+// what was carried across bytes (it stays below each byte's top field).
+__device__ __forceinline__ i32x4_t word_bytes(uint32_t w) {
+  const uint32_t s = w << 2;
+  const uint32_t lo = __builtin_amdgcn_perm(s, w, 0x07050301u);
+  const uint32_t hi = __builtin_amdgcn_perm(s, w, 0x06040200u);
+  const uint64_t next = shl64<4>(static_cast<uint64_t>(hi) << 32 | lo);
+  i32x4_t o;
+  o[0] = static_cast<int>(lo & kByteMask);
+  o[1] = static_cast<int>(static_cast<uint32_t>(next) & kByteMask);
+  o[2] = static_cast<int>(hi & kByteMask);
+  o[3] = static_cast<int>(static_cast<uint32_t>(next >> 32) & kByteMask);
+  return o;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& c, int w) {
+  return w == 0 ? c.x : w == 1 ? c.y : w == 2 ? c.z : c.w;
+}
+
+// Matrix product of one workgroup: T tiles of 16 weight rows (of gate and of
+// up each with SWIGLU) against MT tiles of 16 activation rows. Its SK waves
+// share K in units of 256 columns: lane (i, g) = (l % 16, l / 16) holds the
+// 16-byte chunk 4u + g (64 codes) of weight row i and the same 64 bytes of
+// activation row i, so step w of a unit multiplies word w of the chunk with
+// bytes 16w .. 16w + 15. The waves' int32 sums meet in LDS.
+template <int MT, int T, int SK, bool SWIGLU>
+__global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
+    const uint4* __restrict__ packed, const float* __restrict__ scale, const uint4* __restrict__ packed2,
+    const float* __restrict__ scale2, int64_t n, int64_t chunks, const int8_t* __restrict__ q,
+    const float* __restrict__ q_scale, int64_t m, int64_t n_blocks, float* __restrict__ y, uint16_t* __restrict__ h) {
+  constexpr int TT = SWIGLU ? 2 * T : T;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int li = lane & 15, lg = lane >> 4;
+  const int64_t n0 = (blockIdx.x % n_blocks) * (16 * T);
+  const int64_t m0 = (blockIdx.x / n_blocks) * (16 * MT);
+  const int64_t kp = chunks * 64;
+  const int64_t units = (chunks + 3) / 4;
+
+  const uint4* wp[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int64_t r = n0 + 16 * (t % T) + li;
+    wp[t] = (t < T ? packed : packed2) + (r < n ? r : n - 1) * chunks;
+  }
+  const int8_t* xp[MT];
+#pragma unroll
+  for (int a = 0; a < MT; ++a) {
+    const int64_t r = m0 + 16 * a + li;
+    xp[a] = q + (r < m ? r : m - 1) * kp;
+  }
+  i32x4_t acc[MT][TT] = {};
+  for (int64_t u = wave; u < units; u += SK) {
+    const int64_t c = 4 * u + lg;
+    const bool in = c < chunks;  // chunks past the row: codes 0
+    const int64_t cc = in ? c : chunks - 1;
+    uint4 w[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) w[t] = masked(wp[t][cc], in);
+    i32x4_t x[MT][4];
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) x[a][s] = *reinterpret_cast<const i32x4_t*>(xp[a] + cc * 64 + 16 * s);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const i32x4_t b = word_bytes(word_of(w[t], s));
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+          acc[a][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[a][s], b, acc[a][t], 0, 0, 0);
+      }
+  }
+
+  if constexpr (SK > 1) {
+    __shared__ i32x4_t part[SK - 1][MT * TT][kWave];
+    if (wave > 0) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) part[wave - 1][a * TT + t][lane] = acc[a][t];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+    for (int s = 0; s < SK - 1; ++s)
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[a][t] += part[s][a * TT + t][lane];
+  }
+  // column r = li of a tile, activation row 4 lg + e
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int64_t r = n0 + 16 * t + li;
+    if (r >= n) continue;
+    const float s1 = scale[r];
+    const float s2 = SWIGLU ? scale2[r] : 0.0f;
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t i = m0 + 16 * a + 4 * lg + e;
+        if (i >= m) continue;
+        const float qs = q_scale[i];
+        const float v = static_cast<float>(acc[a][t][e] >> kCodeShift) * qs * s1;
+        if constexpr (SWIGLU) {
+          const float v2 = static_cast<float>(acc[a][T + t][e] >> kCodeShift) * qs * s2;
+          h[i * n + r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(silu(v) * v2));
+        } else {
+          y[i * n + r] = v;
+        }
+      }
+  }
+}
+
+template <int MT, int T, int SK, bool SWIGLU>
+void launch_stream(const uint32_t* p1, const float* s1, const uint32_t* p2, const float* s2, int64_t n, int64_t k,
+                   const int8_t* q, const float* q_scale, int64_t m, float* y, uint16_t* h, hipStream_t stream) {
+  const int64_t nb = (n + 16 * T - 1) / (16 * T), mb = (m + 16 * MT - 1) / (16 * MT);
+  hipLaunchKernelGGL((gemm_i8_stream_kernel<MT, T, SK, SWIGLU>), dim3(static_cast<unsigned>(nb * mb)),
+                     dim3(SK * kWave), 0, stream, reinterpret_cast<const uint4*>(p1), s1,
+                     reinterpret_cast<const uint4*>(p2), s2, n, words_per_row(k) / 4, q, q_scale, m, nb, y, h);
+}
+
+}  // namespace
+
+hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
+                                  const float* q_scale, int64_t m, float* y, hipStream_t stream) {
+  launch_stream<1, 1, 4, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_gate_up_i8(const uint32_t* gate, const float* gate_scale, const uint32_t* up,
+                                    const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
+                                    const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream) {
+  launch_stream<1, 1, 4, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream);
+  return hipGetLastError();
+}
+
+}  // namespace pbg

@@ -1,0 +1,438 @@
+"""GPU parity of the 8-bit activation path (add_rmsnorm, quantize_rows,
+ternary_gemm_i8, ternary_swiglu_gate_up_i8) and of lora_add against the CPU
+oracle in 64 bits.
+
+Codes and integer probes must match bit for bit. Tolerances, with u = 2^-24:
+* q_scale and the norm's factor: an fp32 sum of k squares in any order is
+  within k u relative, its root within half of that, and the mean, the added
+  epsilon, the root, the reciprocal and two products add one u each.
+* h: that plus one fp16 rounding (2^-11 relative, 2^-25 below the normals).
+* ternary_gemm_i8: the sum is exact and two products follow: 2 u (2.01 u with
+  their cross term).
+* lora_add: fp32 sums of k products for the inner values, 2^-22 of each for
+  their two fp16 parts, an fp32 sum of 2 rank products, then three roundings.
+"""
+from __future__ import annotations
+
+import sys
+
+import numpy as np
+import pytest
+
+import oracle
+import synth
+from helpers import assert_within, swiglu_h_bound
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+NAN = float("nan")
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module")
+def pbg(gpu):
+    import packed_bit_gemv_amd as m
+
+    m.lib()
+    return m
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda:0")
+
+
+def host(t):
+    return t.cpu().numpy()
+
+
+def norm_case(seed, m, k):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((m, k)).astype(np.float32)
+    res = (rng.standard_normal((m, k)) * 4).astype(np.float32)
+    res[:, :: max(1, k // 3)] *= 12
+    return x, res, rng.uniform(0.5, 1.5, k).astype(np.float32)
+
+
+def check_norm(got, ref, k, res_in=True):
+    r, h, q, qs = got
+    rr, hh, qq, ss = ref
+    g = (k / 2 + 8) * U
+    if r is not None:
+        assert np.array_equal(host(r), rr)
+    if h is not None:
+        assert_within(host(h).astype(np.float64), hh, np.abs(hh) * (2.0 ** -11 + g) * 1.001 + 2.0 ** -25, "h")
+    if q is not None:
+        qn = host(q)
+        assert qn.shape[1] == oracle.words_per_row(k) * 16
+        assert np.array_equal(qn[:, :k], qq) and not qn[:, k:].any()
+        assert_within(host(qs), ss, np.abs(ss) * g * 1.001, "q_scale")
+
+
+NORM_SHAPES = [(1, 1), (1, 63), (3, 64), (1, 4096), (2, 4100), (5, 4097), (7, 12288), (700, 260), (1030, 1024), (2, 16384),
+               (3, 16388), (2, 20001), (1, 131072), (2500, 8), (600, 4096)]
+
+
+@pytest.mark.parametrize("m,k", NORM_SHAPES)
+def test_add_rmsnorm(pbg, m, k):
+    say(f"add_rmsnorm m={m} k={k}")
+    x, res, w = norm_case(10 + m + k, m, k)
+    ref = oracle.add_rmsnorm(x, w, 1e-6, res)
+    xd, rd, wd = dev(x), dev(res), dev(w)
+    check_norm(pbg.add_rmsnorm(xd, wd, 1e-6, residual=rd, want="hq"), ref, k)
+    r, h, q, qs = pbg.add_rmsnorm(xd, wd, 1e-6, residual=rd)
+    assert q is None and qs is None
+    check_norm((r, h, None, None), ref, k)
+    r, h, q, qs = pbg.add_rmsnorm(xd, wd, 1e-6, residual=rd, want="q")
+    assert h is None
+    check_norm((r, None, q, qs), ref, k)
+    # without a residual
+    ref0 = oracle.add_rmsnorm(x, w, 1e-5)
+    r, h, q, qs = pbg.add_rmsnorm(xd, wd, 1e-5, want="hq")
+    assert r is xd
+    check_norm((None, h, q, qs), ref0, k)
+    # in place, into the residual's buffer and into x's
+    r1 = rd.clone()
+    got = pbg.add_rmsnorm(xd, wd, 1e-6, residual=r1, residual_out=r1, want="hq")
+    assert got[0] is r1
+    check_norm(got, ref, k)
+    x1 = xd.clone()
+    check_norm(pbg.add_rmsnorm(x1, wd, 1e-6, residual=rd, residual_out=x1, want="hq"), ref, k)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_add_rmsnorm_offsets(pbg, off):
+    """Buffers that are only element-aligned, rows behind the last one left as they were."""
+    m, k = 3, 4096
+    x, res, w = norm_case(5, m, k)
+
+    def at(a):
+        t = torch.zeros(a.size + 8, dtype=torch.float32, device="cuda:0")
+        t[off:off + a.size] = dev(a.reshape(-1))
+        return t[off:off + a.size].view(a.shape)
+
+    h = torch.full((m * k + 16,), 7.0, dtype=torch.float16, device="cuda:0")
+    q = torch.full(((m + 1), k), 9, dtype=torch.int8, device="cuda:0")
+    qs = torch.full((m + 1,), 5.0, device="cuda:0")
+    ro = torch.full((m * k + 8,), 3.0, device="cuda:0")
+    got = pbg.add_rmsnorm(at(x), at(w), 1e-6, residual=at(res), residual_out=ro[off:off + m * k].view(m, k),
+                          h=h[off:off + m * k].view(m, k), q=q[:m], q_scale=qs[:m])
+    check_norm(got, oracle.add_rmsnorm(x, w, 1e-6, res), k)
+    assert (h[:off] == 7).all() and (h[off + m * k:] == 7).all() and (q[m] == 9).all() and qs[m] == 5
+    assert (ro[:off] == 3).all() and (ro[off + m * k:] == 3).all()
+
+
+@pytest.mark.parametrize("k", [4096, 4100, 37])
+def test_add_rmsnorm_odd_rows(pbg, k):
+    """Rows of zeros, NaN, infinities, sums of squares past fp32, magnitudes near both ends."""
+    x = np.random.default_rng(1).standard_normal((8, k)).astype(np.float32)
+    x[0] = 0
+    x[1, 5] = np.nan
+    x[2, 7] = np.inf
+    x[3] *= np.float32(1e25)
+    x[4] *= np.float32(1e-36)
+    x[5] *= np.float32(1e-25)
+    x[6, 3] = 3e4
+    w = np.ones(k, np.float32)
+    _, h, q, qs = pbg.add_rmsnorm(dev(x), dev(w), 1e-6, want="hq")
+    h, q, qs = host(h).astype(np.float64), host(q), host(qs)
+    assert not q[:4].any() and qs[0] == 0 and np.isnan(qs[1:4]).all() and not q[4].any() and qs[4] == 0
+    assert np.isnan(h[1]).all() and np.isnan(h[2]).all() and np.isnan(h[3]).all() and not h[0].any()
+    ref = oracle.add_rmsnorm(x[5:], w, 1e-6)
+    check_norm((None, torch.from_numpy(h[5:]), torch.from_numpy(q[5:]), torch.from_numpy(qs[5:])), ref, k)
+
+
+@pytest.mark.parametrize("m,k", [(1, 1), (1, 31), (2, 4096), (33, 4100), (5, 4104), (2, 12288), (900, 520), (3, 16392), (1, 131072),
+                                 (2, 40008), (2048, 8), (513, 12288)])
+def test_quantize_rows(pbg, m, k):
+    say(f"quantize_rows m={m} k={k}")
+    x = (np.random.default_rng(m + k).standard_normal((m, k)) * 0.7).astype(np.float16)
+    if m > 4:
+        x[1] = 0
+        x[2, k // 2] = np.nan
+        x[3, 0] = -np.inf
+        x[4] = np.float16(6e-8)
+    qq, ss = oracle.quantize_rows(x)
+    q, qs = pbg.quantize_rows(dev(x))
+    qn = host(q)
+    assert np.array_equal(qn[:, :k], qq) and not qn[:, k:].any()
+    assert np.array_equal(host(qs), ss.astype(np.float32), equal_nan=True)
+    # an element-aligned input
+    t = torch.zeros(m * k + 3, dtype=torch.float16, device="cuda:0")
+    t[3:] = dev(x).view(-1)
+    q2, qs2 = pbg.quantize_rows(t[3:].view(m, k))
+    assert torch.equal(q2, q) and np.array_equal(host(qs2), host(qs), equal_nan=True)
+
+
+def pad(q):
+    out = np.full((q.shape[0], 64 * ((q.shape[1] + 63) // 64)), 77, np.int8)  # readers ignore the padding
+    out[:, :q.shape[1]] = q
+    return out
+
+
+GEMM_SHAPES = [(1, 1, 1), (1, 17, 64), (2, 5, 65), (16, 16, 256), (17, 33, 320), (1, 6144, 4096), (7, 4096, 12288), (8, 1024, 4096),
+               (33, 100, 4100), (64, 48, 1000), (100, 1024, 4096), (129, 130, 192), (257, 300, 640), (300, 1000, 1096),
+               (512, 512, 512), (1000, 257, 64), (2, 70000, 64), (70000, 3, 130), (130, 640, 12288), (513, 2050, 4096)]
+
+
+@pytest.mark.parametrize("m,n,k", GEMM_SHAPES)
+def test_gemm_i8(pbg, m, n, k):
+    say(f"gemm_i8 m={m} n={n} k={k}")
+    rng = np.random.default_rng(m * 3 + n * 5 + k)
+    q = rng.integers(-128, 128, (m, k)).astype(np.int8)
+    codes = synth.ternary_codes(n + k, n, k)
+    total = (torch.from_numpy(q).double() @ torch.from_numpy(codes).double().t()).numpy()
+    packed = pbg.pack_ternary(dev(codes))[0]
+    # powers of two as scales: exact
+    s, qs = synth.pow2_scales(n, n), synth.pow2_scales(m + 1, m)
+    buf = torch.full((m + 1, n), 5.0, device="cuda:0")
+    y = pbg.ternary_gemm_i8(packed, dev(s), k, dev(pad(q)), dev(qs), buf[:m])
+    assert np.array_equal(host(y).astype(np.float64), total * qs.astype(np.float64)[:, None] * s.astype(np.float64))
+    assert (buf[m] == 5).all()
+    # any scales: two roundings, NaN of a row without an 8-bit form stays in its row
+    s, qs = synth.row_scales(n, n), synth.row_scales(m + 1, m)
+    ref = total * qs.astype(np.float64)[:, None] * s.astype(np.float64)
+    if m > 2:
+        qs[1] = NAN
+    y = host(pbg.ternary_gemm_i8(packed, dev(s), k, dev(pad(q)), dev(qs)))
+    if m > 2:
+        assert np.isnan(y[1]).all()
+        y, ref = np.delete(y, 1, 0), np.delete(ref, 1, 0)
+    assert_within(y, ref, np.abs(ref) * 2.01 * U, "gemm_i8")
+
+
+def test_gemm_i8_largest_sum(pbg):
+    """k at its limit, every product of the same sign: the int32 sums reach 2^30."""
+    k = 131072
+    codes = np.ones((3, k), np.int8)
+    codes[1] = -1
+    q = np.full((2, k), -128, np.int8)
+    q[1] = 127
+    one = np.ones(3, np.float32)
+    y = host(pbg.ternary_gemm_i8(pbg.pack_ternary(dev(codes))[0], dev(one), k, dev(q), dev(one[:2])))
+    assert np.array_equal(y, np.array([[-1, 1, -1], [0, 0, 0]]) * 128.0 * k + np.array([[0, 0, 0], [1, -1, 1]]) * 127.0 * k)
+
+
+def test_gemm_i8_reads_every_code(pbg):
+    """One nonzero activation at a time reads the packed codes back."""
+    k, n = 200, 37
+    codes = synth.ternary_codes(4, n, k)
+    q = np.zeros((k, k), np.int8)
+    np.fill_diagonal(q, 1)
+    y = host(pbg.ternary_gemm_i8(pbg.pack_ternary(dev(codes))[0], dev(np.ones(n, np.float32)), k, dev(pad(q)),
+                                 dev(np.ones(k, np.float32))))
+    assert np.array_equal(y.T, codes)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 12288, 4096), (8, 333, 4096), (16, 40, 72), (65, 100, 200), (130, 257, 1000),
+                                   (300, 520, 4096), (40, 2048, 4096), (600, 130, 640)])
+def test_swiglu_gate_up_i8(pbg, m, n, k):
+    say(f"swiglu_gate_up_i8 m={m} n={n} k={k}")
+    rng = np.random.default_rng(m + n + k)
+    q = rng.integers(-128, 128, (m, k)).astype(np.int8)
+    cg, cu = synth.ternary_codes(n + 1, n, k), synth.ternary_codes(n + 2, n, k)
+    sg, su = synth.row_scales(3, n), synth.row_scales(4, n)
+    qs = synth.row_scales(5, m) * np.float32(2 / np.sqrt(k))
+    qd = torch.from_numpy(q).double()
+    g = (qd @ torch.from_numpy(cg).double().t()).numpy() * qs.astype(np.float64)[:, None] * sg.astype(np.float64)
+    u = (qd @ torch.from_numpy(cu).double().t()).numpy() * qs.astype(np.float64)[:, None] * su.astype(np.float64)
+    buf = torch.full((m * n + 8,), 3.0, dtype=torch.float16, device="cuda:0")
+    h = pbg.ternary_swiglu_gate_up_i8(pbg.pack_ternary(dev(cg))[0], dev(sg), pbg.pack_ternary(dev(cu))[0], dev(su), k,
+                                      dev(pad(q)), dev(qs), buf[:m * n].view(m, n))
+    sil = oracle.silu(g)
+    assert_within(host(h).astype(np.float64), sil * u, swiglu_h_bound(sil, u, np.abs(g) * 2.01 * U, np.abs(u) * 2.01 * U), "h")
+    assert (buf[m * n:] == 3).all()
+
+
+def lora_case(seed, m, n, k, na, r, runs=False):
+    rng = np.random.default_rng(seed)
+    ids = rng.integers(-1, na + 1, m).astype(np.int32)  # -1 and na: no adapter
+    if runs:
+        ids.sort()
+    return dict(y=rng.standard_normal((m, n)).astype(np.float32), x=rng.standard_normal((m, k)).astype(np.float16), ids=ids,
+                a=(rng.standard_normal((na, r, k)) / np.sqrt(k)).astype(np.float16),
+                b=(rng.standard_normal((na, n, r)) / np.sqrt(r)).astype(np.float16),
+                scale=rng.uniform(0.5, 2, na).astype(np.float32))
+
+
+def lora_bound(c):
+    """Derived bound per element (see the module's docstring)."""
+    na, r, k = c["a"].shape
+    x, a, b, s = (np.abs(c[i].astype(np.float64)) for i in ("x", "a", "b", "scale"))
+    out = np.abs(c["y"].astype(np.float64)) * U * 1.01
+    for i, t in enumerate(c["ids"]):
+        if 0 <= t < na:
+            va = a[t] @ x[i]
+            out[i] += s[t] * (b[t] @ va) * ((k + 16) * U + 2.0 ** -22 + 2 * r * U + 4 * U) * 1.01
+    return out
+
+
+LORA_SHAPES = [(1, 1, 1, 1, 1), (1, 4096, 4096, 4, 16), (5, 70, 64, 3, 8), (16, 33, 40, 20, 4), (64, 512, 4096, 24, 16),
+               (40, 100, 100, 7, 12), (37, 260, 520, 2, 64), (100, 64, 264, 5, 128), (70, 200, 72, 70, 24), (300, 129, 640, 3, 32),
+               (1000, 77, 130, 6, 16), (3, 50, 12288, 2, 16), (17, 6, 3, 2, 127), (600, 1100, 512, 4, 64)]
+
+
+@pytest.mark.parametrize("runs", [False, True])
+@pytest.mark.parametrize("m,n,k,na,r", LORA_SHAPES)
+def test_lora_add(pbg, m, n, k, na, r, runs):
+    say(f"lora m={m} n={n} k={k} adapters={na} rank={r} runs={runs}")
+    c = lora_case(m + n + k, m, n, k, na, r, runs)
+    d = {i: dev(v) for i, v in c.items()}
+    ref = oracle.lora_add(**c)
+    buf = torch.full((m + 1, n), 5.0, device="cuda:0")
+    ws = torch.full((pbg.lora_workspace(m, r, "cuda:0").numel() + 64,), 255, dtype=torch.uint8, device="cuda:0")  # any content
+    out = pbg.lora_add(**d, out=buf[:m], workspace=ws)
+    assert_within(host(out), ref, lora_bound(c), "lora")
+    without = (c["ids"] < 0) | (c["ids"] >= na)
+    assert np.array_equal(host(out)[without], c["y"][without]) and (buf[m] == 5).all()
+    assert (ws[-64:] == 255).all()
+    y = d["y"].clone()
+    assert torch.equal(pbg.lora_add(**{**d, "y": y}, out=y), out)  # in place, the same bits
+
+
+@pytest.mark.parametrize("m,k,r", [(3, 64, 8), (40, 192, 16), (300, 64, 64), (9, 60, 5)])
+def test_lora_exact_probe(pbg, m, k, r):
+    """Whole numbers and scales of powers of two: every sum is exact in fp32."""
+    rng = np.random.default_rng(m)
+    n, na = 50, 3
+    c = dict(y=rng.integers(-99, 99, (m, n)).astype(np.float32), x=rng.integers(-8, 9, (m, k)).astype(np.float16),
+             ids=rng.integers(-1, na, m).astype(np.int32), a=rng.integers(-3, 4, (na, r, k)).astype(np.float16),
+             b=rng.integers(-3, 4, (na, n, r)).astype(np.float16), scale=np.array([0.5, 1, 2], np.float32))
+    out = host(pbg.lora_add(**{i: dev(v) for i, v in c.items()}))
+    assert np.array_equal(out.astype(np.float64), oracle.lora_add(**c))
+
+
+def test_lora_other_adapters_stay_out(pbg):
+    """NaN and infinities in one adapter reach only its own rows."""
+    c = lora_case(2, 50, 96, 128, 4, 16)
+    c["ids"][:] = np.arange(50) % 5 - 1
+    ref = oracle.lora_add(**c)
+    bound = lora_bound(c)
+    c["a"][2], c["b"][2, 3:9] = np.nan, np.inf
+    out = host(pbg.lora_add(**{i: dev(v) for i, v in c.items()}))
+    ok = c["ids"] != 2
+    assert_within(out[ok], ref[ok], bound[ok], "rows of other adapters")
+    assert np.isnan(out[~ok]).any()
+
+
+def test_lora_odd_offsets(pbg):
+    """Element-aligned fp16 inputs take the guarded loads and give the same sums."""
+    c = lora_case(8, 20, 64, 256, 3, 16)
+
+    def at(v):
+        if v.dtype != np.float16:
+            return dev(v)
+        t = torch.zeros(v.size + 1, dtype=torch.float16, device="cuda:0")
+        t[1:] = dev(v).view(-1)
+        return t[1:].view(v.shape)
+
+    assert_within(host(pbg.lora_add(**{i: at(v) for i, v in c.items()})), oracle.lora_add(**c), lora_bound(c), "offsets")
+
+
+def block(pbg, w, x, res, ids):
+    """The feed-forward half of a layer on 8-bit rows with an adapter beside down, and the norm that follows."""
+    r, _, q, qs = pbg.add_rmsnorm(x, w["norm"], 1e-6, residual=res, want="q")
+    h = pbg.ternary_swiglu_gate_up_i8(w["gate"], w["sg"], w["up"], w["su"], w["d"], q, qs)
+    hq, hs = pbg.quantize_rows(h)
+    y = pbg.ternary_gemm_i8(w["down"], w["sd"], w["f"], hq, hs)
+    pbg.lora_add(y, h, ids, w["a"], w["b"], w["s"], out=y)
+    r2, h2, _, _ = pbg.add_rmsnorm(y, w["norm"], 1e-6, residual=r)
+    return q, qs, h, hq, hs, y, r2, h2
+
+
+def block_weights(pbg, d, f):
+    rng = np.random.default_rng(d)
+    cg, cu, cd = (synth.ternary_codes(i, f, d) for i in (1, 2)), None, synth.ternary_codes(3, d, f)
+    cg, cu = cg
+    np_w = dict(cg=cg, cu=cu, cd=cd, sg=synth.row_scales(4, f), su=synth.row_scales(5, f), sd=synth.row_scales(6, d),
+                norm=rng.uniform(0.5, 1.5, d).astype(np.float32),
+                a=(rng.standard_normal((3, 16, f)) / np.sqrt(f)).astype(np.float16),
+                b=(rng.standard_normal((3, d, 16)) / 4).astype(np.float16), s=np.array([0.5, 1, 2], np.float32))
+    w = {i: dev(v) for i, v in np_w.items() if not i.startswith("c")}
+    w.update(gate=pbg.pack_ternary(dev(cg))[0], up=pbg.pack_ternary(dev(cu))[0], down=pbg.pack_ternary(dev(cd))[0], d=d, f=f)
+    return np_w, w
+
+
+@pytest.mark.parametrize("m", [1, 6, 200])
+def test_block(pbg, m):
+    """The operators together: each step against the oracle on the step's own inputs."""
+    d, f = 256, 712
+    nw, w = block_weights(pbg, d, f)
+    x, res, _ = norm_case(m, m, d)
+    ids = (np.arange(m) % 4 - 1).astype(np.int32)
+    q, qs, h, hq, hs, y, r2, h2 = [host(t) for t in block(pbg, w, dev(x), dev(res), dev(ids))]
+    r_ref, _, q_ref, qs_ref = oracle.add_rmsnorm(x, nw["norm"], 1e-6, res)
+    assert np.array_equal(q[:, :d], q_ref)
+    assert_within(qs, qs_ref, qs_ref * (d / 2 + 8) * U * 1.001, "q_scale")
+    g = oracle.ternary_gemm_i8(oracle.pack(nw["cg"])[0], nw["sg"], d, q, qs)
+    u = oracle.ternary_gemm_i8(oracle.pack(nw["cu"])[0], nw["su"], d, q, qs)
+    sil = oracle.silu(g)
+    assert_within(h.astype(np.float64), sil * u, swiglu_h_bound(sil, u, np.abs(g) * 2.01 * U, np.abs(u) * 2.01 * U), "h")
+    assert np.array_equal(hq[:, :f], oracle.quantize_rows(h)[0])
+    base = oracle.ternary_gemm_i8(oracle.pack(nw["cd"])[0], nw["sd"], f, hq, hs)
+    c = dict(y=base, x=h, ids=ids, a=nw["a"], b=nw["b"], scale=nw["s"])
+    assert_within(y, oracle.lora_add(**c), lora_bound(c) + np.abs(base) * 2.01 * U, "y")
+    r_ref2, h_ref2, _, _ = oracle.add_rmsnorm(y, nw["norm"], 1e-6, r_ref)
+    check_norm((torch.from_numpy(r2), torch.from_numpy(h2), None, None), (r_ref2, h_ref2, None, None), d)
+
+
+def test_block_in_a_graph_and_on_a_stream(pbg):
+    """Captured once and replayed on new inputs, with eager work between the replays; and on a side stream."""
+    m, d, f = 5, 256, 712
+    _, w = block_weights(pbg, d, f)
+    x, res, ids = (torch.zeros((m, d), device="cuda:0"), torch.zeros((m, d), device="cuda:0"),
+                   torch.zeros(m, dtype=torch.int32, device="cuda:0"))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block(pbg, w, x, res, ids)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = block(pbg, w, x, res, ids)
+    for seed in range(4):
+        xn, rn, _ = norm_case(seed, m, d)
+        x.copy_(dev(xn))
+        res.copy_(dev(rn))
+        ids.copy_(dev((np.arange(m) + seed).astype(np.int32) % 4 - 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = block(pbg, w, x, res, ids)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other = block(pbg, w, x, res, ids)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        for a, b, c in zip(outs, eager, other):
+            assert torch.equal(a, b) and torch.equal(c, b)
+
+
+def test_refusals(pbg):
+    x = torch.zeros((2, 64), device="cuda:0")
+    w = torch.ones(64, device="cuda:0")
+    h = x.half()
+    with pytest.raises(pbg.PbgError):
+        pbg.add_rmsnorm(x, w, 0.0)
+    with pytest.raises(pbg.PbgError):
+        pbg.add_rmsnorm(x[:0], w)
+    for bad in (lambda: pbg.add_rmsnorm(h, w), lambda: pbg.add_rmsnorm(x, w[:63]), lambda: pbg.add_rmsnorm(x.t(), w),
+                lambda: pbg.add_rmsnorm(x, w, residual=x[:1]), lambda: pbg.add_rmsnorm(x, w, want="x"),
+                lambda: pbg.quantize_rows(x), lambda: pbg.quantize_rows(h, torch.zeros((2, 63), dtype=torch.int8, device="cuda:0")),
+                lambda: pbg.ternary_gemm_i8(torch.zeros((4, 4), dtype=torch.int32, device="cuda:0"), torch.ones(4, device="cuda:0"),
+                                            65, torch.zeros((2, 128), dtype=torch.int8, device="cuda:0"),
+                                            torch.ones(2, device="cuda:0")),
+                lambda: pbg.lora_add(x, h, torch.zeros(2, dtype=torch.int64, device="cuda:0"),
+                                     torch.zeros((1, 8, 64), dtype=torch.float16, device="cuda:0"),
+                                     torch.zeros((1, 64, 8), dtype=torch.float16, device="cuda:0"), torch.ones(1, device="cuda:0"))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(pbg.PbgError):
+        pbg.lora_add(x, h, torch.zeros(2, dtype=torch.int32, device="cuda:0"),
+                     torch.zeros((1, 8, 64), dtype=torch.float16, device="cuda:0"),
+                     torch.zeros((1, 64, 8), dtype=torch.float16, device="cuda:0"), torch.ones(1, device="cuda:0"),
+                     workspace=torch.zeros(16, dtype=torch.uint8, device="cuda:0"))
