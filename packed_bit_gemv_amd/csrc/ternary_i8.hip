@@ -11,6 +11,7 @@ namespace pbg {
 namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kByteMask = 0xC0C0C0C0u;
 constexpr int kCodeShift = 6;  // decoded bytes are 64 * c
@@ -144,10 +145,175 @@ void launch_stream(const uint32_t* p1, const float* s1, const uint32_t* p2, cons
                      reinterpret_cast<const uint4*>(p2), s2, n, words_per_row(k) / 4, q, q_scale, m, nb, y, h);
 }
 
+// Chunk c of a row, codes 0 from the end of the row on.
+__device__ __forceinline__ i32x4_t load_chunk(const uint4* __restrict__ row, int64_t c, int64_t chunks) {
+  const i32x4_t v = *reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1));
+  const int keep = c < chunks ? -1 : 0;
+  return v & keep;
+}
+
+// Tile of a workgroup. Workgroups go round the 8 XCDs, each with its own L2:
+// an XCD gets a run of consecutive tiles, ordered by groups of kGroupM row
+// blocks under one column block, so that the tiles in flight on an XCD share
+// both operands.
+constexpr int kXcds = 8;
+constexpr int kGroupM = 4;
+
+__device__ __forceinline__ void tile_of_block(int m_blocks, int n_blocks, int& mb, int& nb) {
+  const int total = m_blocks * n_blocks;
+  const int xcd = blockIdx.x % kXcds, at = blockIdx.x / kXcds;
+  const int each = total / kXcds, over = total % kXcds;
+  const int id = xcd * each + (xcd < over ? xcd : over) + at;
+  const int group = id / (kGroupM * n_blocks);
+  const int rows = m_blocks - group * kGroupM < kGroupM ? m_blocks - group * kGroupM : kGroupM;
+  const int in = id - group * kGroupM * n_blocks;
+  mb = group * kGroupM + in % rows;
+  nb = in / rows;
+}
+
+// Matrix product of many activation rows: a workgroup of WM x WN waves owns
+// 32 TM WM rows by 32 TN WN columns, a wave TM x TN tiles of the 32x32x32 i8
+// matrix instruction, whose A operand is activations and B operand decoded
+// codes. K goes in steps of two chunks (128 columns). The activations of a
+// step go through LDS, double-buffered, one barrier a step: the next step's
+// loads are issued before the step's products and stored after them. 16-byte
+// piece c of row i sits at place c ^ (i % 8) of its 128 bytes, so that both
+// the stores and the operand reads touch every bank once in eight lanes. The
+// packed words come straight to registers (lane (i, g) = (l % 32, l / 32) the
+// chunk 2u + g of column i) and are decoded once for all TM row tiles, which
+// is what pays for the decode: 8 vector instructions a word against TM matrix
+// instructions of 32 cycles.
+template <int WM, int WN, int TM, int TN, bool SWIGLU>
+__global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
+    const uint4* __restrict__ packed, const float* __restrict__ scale, const uint4* __restrict__ packed2,
+    const float* __restrict__ scale2, int64_t n, int64_t chunks, const int8_t* __restrict__ q,
+    const float* __restrict__ q_scale, int64_t m, int m_blocks, int n_blocks, float* __restrict__ y,
+    uint16_t* __restrict__ h) {
+  static_assert(!SWIGLU || TN % 2 == 0, "a wave holds as many gate tiles as up tiles");
+  constexpr int kThreads = WM * WN * kWave;
+  constexpr int BM = 32 * TM * WM;
+  constexpr int TC = SWIGLU ? TN / 2 : TN;  // column tiles of a wave
+  constexpr int BN = 32 * TC * WN;
+  constexpr int kLoads = BM * 8 / kThreads;
+  static_assert(BM * 8 % kThreads == 0, "whole loads");
+  __shared__ i32x4_t xs[2][BM * 8];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int li = lane & 31, lg = lane >> 5;
+  const int wm = wave / WN, wn = wave % WN;
+  int mb, nb;
+  tile_of_block(m_blocks, n_blocks, mb, nb);
+  const int64_t m0 = static_cast<int64_t>(mb) * BM;
+  const int64_t n0 = static_cast<int64_t>(nb) * BN + wn * (32 * TC);
+  const int64_t kp = chunks * 64;
+  const int64_t steps = (chunks + 1) / 2;
+
+  const uint4* wp[TN];
+#pragma unroll
+  for (int t = 0; t < TN; ++t) {
+    const int64_t r = n0 + 32 * (t % TC) + li;
+    wp[t] = (t < TC ? packed : packed2) + (r < n ? r : n - 1) * chunks;
+  }
+  const int8_t* xp[kLoads];  // this thread's pieces: row (threadIdx.x + i kThreads) / 8, piece threadIdx.x % 8
+  int xo[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int row = (threadIdx.x + i * kThreads) >> 3, c = threadIdx.x & 7;
+    const int64_t r = m0 + row;
+    xp[i] = q + (r < m ? r : m - 1) * kp + 16 * c;
+    xo[i] = row * 8 + (c ^ (row & 7));
+  }
+  const int half = (threadIdx.x & 7) >> 2;  // chunk of the step that this thread's pieces belong to
+  i32x4_t xv[kLoads], wv[TN];
+  i32x16_t acc[TM][TN] = {};
+  // Chunks past the row (the last step of an odd count) read the last one: activations as they are, codes 0.
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+    xv[i] = *reinterpret_cast<const i32x4_t*>(xp[i] - (half < chunks ? 0 : 64));
+#pragma unroll
+  for (int t = 0; t < TN; ++t) wv[t] = load_chunk(wp[t], lg, chunks);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) xs[0][xo[i]] = xv[i];
+  __syncthreads();
+  for (int64_t u = 0; u < steps; ++u) {
+    i32x4_t w[TN];
+#pragma unroll
+    for (int t = 0; t < TN; ++t) w[t] = wv[t];
+    const bool more = u + 1 < steps;
+    if (more) {
+      const int64_t at = (u + 1) * 128 - (2 * (u + 1) + half < chunks ? 0 : 64);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) xv[i] = *reinterpret_cast<const i32x4_t*>(xp[i] + at);
+#pragma unroll
+      for (int t = 0; t < TN; ++t) wv[t] = load_chunk(wp[t], 2 * (u + 1) + lg, chunks);
+    }
+    const i32x4_t* xb = xs[u & 1];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      i32x4_t a[TM];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int row = (wm * TM + i) * 32 + li;
+        a[i] = xb[row * 8 + ((4 * lg + s) ^ (row & 7))];
+      }
+#pragma unroll
+      for (int t = 0; t < TN; ++t) {
+        const i32x4_t b = word_bytes(static_cast<uint32_t>(w[t][s]));
+#pragma unroll
+        for (int i = 0; i < TM; ++i) acc[i][t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b, acc[i][t], 0, 0, 0);
+      }
+    }
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) xs[(u + 1) & 1][xo[i]] = xv[i];
+    }
+    __syncthreads();
+  }
+
+  // lane: column li of a tile, rows 8 (e / 4) + 4 lg + e % 4
+#pragma unroll
+  for (int t = 0; t < TC; ++t) {
+    const int64_t r = n0 + 32 * t + li;
+    if (r >= n) continue;
+    const float s1 = scale[r];
+    const float s2 = SWIGLU ? scale2[r] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t ri = m0 + (wm * TM + i) * 32 + 8 * (e / 4) + 4 * lg + e % 4;
+        if (ri >= m) continue;
+        const float qs = q_scale[ri];
+        const float v = static_cast<float>(acc[i][t][e] >> kCodeShift) * qs * s1;
+        if constexpr (SWIGLU) {
+          const float v2 = static_cast<float>(acc[i][TC + t][e] >> kCodeShift) * qs * s2;
+          h[ri * n + r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(silu(v) * v2));
+        } else {
+          y[ri * n + r] = v;
+        }
+      }
+  }
+}
+
+template <int WM, int WN, int TM, int TN, bool SWIGLU>
+void launch_tile(const uint32_t* p1, const float* s1, const uint32_t* p2, const float* s2, int64_t n, int64_t k,
+                 const int8_t* q, const float* q_scale, int64_t m, float* y, uint16_t* h, hipStream_t stream) {
+  constexpr int BM = 32 * TM * WM, BN = 32 * (SWIGLU ? TN / 2 : TN) * WN;
+  const int64_t nb = (n + BN - 1) / BN, mb = (m + BM - 1) / BM;
+  hipLaunchKernelGGL((gemm_i8_tile_kernel<WM, WN, TM, TN, SWIGLU>), dim3(static_cast<unsigned>(nb * mb)),
+                     dim3(WM * WN * kWave), 0, stream, reinterpret_cast<const uint4*>(p1), s1,
+                     reinterpret_cast<const uint4*>(p2), s2, n, words_per_row(k) / 4, q, q_scale, m,
+                     static_cast<int>(mb), static_cast<int>(nb), y, h);
+}
+
 }  // namespace
 
 hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
                                   const float* q_scale, int64_t m, float* y, hipStream_t stream) {
+  if (m > 128) {
+    launch_tile<2, 4, 4, 2, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream);
+    return hipGetLastError();
+  }
   launch_stream<1, 1, 4, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream);
   return hipGetLastError();
 }
@@ -155,6 +321,10 @@ hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, in
 hipError_t launch_swiglu_gate_up_i8(const uint32_t* gate, const float* gate_scale, const uint32_t* up,
                                     const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
                                     const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream) {
+  if (m > 128) {
+    launch_tile<2, 4, 4, 2, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream);
+    return hipGetLastError();
+  }
   launch_stream<1, 1, 4, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream);
   return hipGetLastError();
 }
