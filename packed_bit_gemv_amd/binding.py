@@ -530,23 +530,25 @@ def q8_row_bytes(k: int) -> int:
 
 def _call(name: str, dev: torch.device, *args) -> None:
     """Call a C entry point on dev's current stream, whatever the current device is."""
-    if dev.index == torch.cuda.current_device():
-        rc = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    # The raw handles: the Stream objects of torch.cuda.current_stream cost as much as a small kernel.
+    index = dev.index
+    if index == torch._C._cuda_getDevice():
+        rc = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            rc = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         _check(name, rc)
 
 
 def _on(dev: torch.device, t, name: str, dtype: torch.dtype, shape: tuple) -> int:
     """Address of t after checking that it is a contiguous dtype tensor of that shape on dev."""
+    if isinstance(t, torch.Tensor) and t.device == dev and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     _dev(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, not on {dev}")
 
 
 def _matrix(t, name: str, dtype: torch.dtype) -> tuple[int, int]:

@@ -35,22 +35,34 @@ __device__ __forceinline__ i32x4_t word_bytes(uint32_t w) {
   return o;
 }
 
-__device__ __forceinline__ uint32_t word_of(const uint4& c, int w) {
-  return w == 0 ? c.x : w == 1 ? c.y : w == 2 ? c.z : c.w;
+// Chunk c of a row, codes 0 from the end of the row on. The streaming form
+// marks the load non-temporal (each weight byte is read once per call).
+__device__ __forceinline__ i32x4_t load_chunk(const uint4* __restrict__ row, int64_t c, int64_t chunks) {
+  const i32x4_t v = *reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1));
+  return v & (c < chunks ? -1 : 0);
+}
+__device__ __forceinline__ i32x4_t load_chunk_nt(const uint4* __restrict__ row, int64_t c, int64_t chunks) {
+  const i32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1)));
+  return v & (c < chunks ? -1 : 0);
 }
 
-// Matrix product of one workgroup: T tiles of 16 weight rows (of gate and of
-// up each with SWIGLU) against MT tiles of 16 activation rows. Its SK waves
-// share K in units of 256 columns: lane (i, g) = (l % 16, l / 16) holds the
-// 16-byte chunk 4u + g (64 codes) of weight row i and the same 64 bytes of
-// activation row i, so step w of a unit multiplies word w of the chunk with
-// bytes 16w .. 16w + 15. The waves' int32 sums meet in LDS.
-template <int MT, int T, int SK, bool SWIGLU>
+// Matrix product of few activation rows: a workgroup owns T tiles of 16
+// weight rows (of gate and of up each with SWIGLU) against MT tiles of 16
+// activation rows and streams the weights. Its SK waves share K in units of
+// 256 columns, UPW units a wave at a time with all their loads in flight
+// before the first product: lane (i, g) = (l % 16, l / 16) holds the 16-byte
+// chunk 4u + g (64 codes) of weight row i and the same 64 bytes of activation
+// row i, so step w of a unit multiplies word w of the chunk with bytes
+// 16w .. 16w + 15. The waves add their int32 sums in LDS (exact in any order).
+template <int MT, int T, int SK, int UPW, bool SWIGLU>
 __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
     const uint4* __restrict__ packed, const float* __restrict__ scale, const uint4* __restrict__ packed2,
     const float* __restrict__ scale2, int64_t n, int64_t chunks, const int8_t* __restrict__ q,
     const float* __restrict__ q_scale, int64_t m, int64_t n_blocks, float* __restrict__ y, uint16_t* __restrict__ h) {
   constexpr int TT = SWIGLU ? 2 * T : T;
+  constexpr int kThreads = SK * kWave;
+  constexpr int kStride = 16 * TT + 4;
+  __shared__ int sums[MT * 16][kStride];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int li = lane & 15, lg = lane >> 4;
@@ -58,6 +70,10 @@ __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
   const int64_t m0 = (blockIdx.x / n_blocks) * (16 * MT);
   const int64_t kp = chunks * 64;
   const int64_t units = (chunks + 3) / 4;
+  if constexpr (SK > 1) {
+    for (int i = threadIdx.x; i < MT * 16 * kStride; i += kThreads) (&sums[0][0])[i] = 0;
+    __syncthreads();
+  }
 
   const uint4* wp[TT];
 #pragma unroll
@@ -66,90 +82,80 @@ __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
     wp[t] = (t < T ? packed : packed2) + (r < n ? r : n - 1) * chunks;
   }
   const int8_t* xp[MT];
+  bool xin[MT];  // rows past m load nothing and count as 0
 #pragma unroll
   for (int a = 0; a < MT; ++a) {
     const int64_t r = m0 + 16 * a + li;
+    xin[a] = r < m;
     xp[a] = q + (r < m ? r : m - 1) * kp;
   }
   i32x4_t acc[MT][TT] = {};
-  for (int64_t u = wave; u < units; u += SK) {
-    const int64_t c = 4 * u + lg;
-    const bool in = c < chunks;  // chunks past the row: codes 0
-    const int64_t cc = in ? c : chunks - 1;
-    uint4 w[TT];
+  for (int64_t u0 = wave * UPW; u0 < units; u0 += SK * UPW) {
+    i32x4_t w[UPW][TT], x[UPW][MT][4];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) w[t] = masked(wp[t][cc], in);
-    i32x4_t x[MT][4];
+    for (int j = 0; j < UPW; ++j)
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
+      for (int t = 0; t < TT; ++t) w[j][t] = load_chunk_nt(wp[t], 4 * (u0 + j) + lg, chunks);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) x[a][s] = *reinterpret_cast<const i32x4_t*>(xp[a] + cc * 64 + 16 * s);
+    for (int j = 0; j < UPW; ++j) {
+      const int64_t c = 4 * (u0 + j) + lg;
+      const int64_t at = (c < chunks ? c : chunks - 1) * 64;
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+      for (int a = 0; a < MT; ++a)
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const i32x4_t b = word_bytes(word_of(w[t], s));
+        for (int s = 0; s < 4; ++s) {
+          x[j][a][s] = i32x4_t{};
+          if (xin[a]) x[j][a][s] = *reinterpret_cast<const i32x4_t*>(xp[a] + at + 16 * s);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
-          acc[a][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[a][s], b, acc[a][t], 0, 0, 0);
-      }
+    for (int j = 0; j < UPW; ++j)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const i32x4_t b = word_bytes(static_cast<uint32_t>(w[j][t][s]));
+#pragma unroll
+          for (int a = 0; a < MT; ++a)
+            acc[a][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[j][a][s], b, acc[a][t], 0, 0, 0);
+        }
   }
 
-  if constexpr (SK > 1) {
-    __shared__ i32x4_t part[SK - 1][MT * TT][kWave];
-    if (wave > 0) {
+  // column li of a tile, activation row 4 lg + e
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
+  for (int a = 0; a < MT; ++a)
 #pragma unroll
-        for (int t = 0; t < TT; ++t) part[wave - 1][a * TT + t][lane] = acc[a][t];
-    }
-    __syncthreads();
-    if (wave > 0) return;
-    for (int s = 0; s < SK - 1; ++s)
-#pragma unroll
-      for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int t = 0; t < TT; ++t) acc[a][t] += part[s][a * TT + t][lane];
-  }
-  // column r = li of a tile, activation row 4 lg + e
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
-    const int64_t r = n0 + 16 * t + li;
-    if (r >= n) continue;
-    const float s1 = scale[r];
-    const float s2 = SWIGLU ? scale2[r] : 0.0f;
-#pragma unroll
-    for (int a = 0; a < MT; ++a)
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int64_t i = m0 + 16 * a + 4 * lg + e;
-        if (i >= m) continue;
-        const float qs = q_scale[i];
-        const float v = static_cast<float>(acc[a][t][e] >> kCodeShift) * qs * s1;
-        if constexpr (SWIGLU) {
-          const float v2 = static_cast<float>(acc[a][T + t][e] >> kCodeShift) * qs * s2;
-          h[i * n + r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(silu(v) * v2));
-        } else {
-          y[i * n + r] = v;
-        }
+        int* at = &sums[16 * a + 4 * lg + e][16 * t + li];
+        if constexpr (SK > 1) __hip_atomic_fetch_add(at, acc[a][t][e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        else *at = acc[a][t][e];
       }
+  __syncthreads();
+  for (int o = threadIdx.x; o < MT * 16 * 16 * T; o += kThreads) {
+    const int row = o / (16 * T), col = o % (16 * T);
+    const int64_t i = m0 + row, r = n0 + col;
+    if (i >= m || r >= n) continue;
+    const float qs = q_scale[i];
+    const float v = static_cast<float>(sums[row][col] >> kCodeShift) * qs * scale[r];
+    if constexpr (SWIGLU) {
+      const float v2 = static_cast<float>(sums[row][16 * T + col] >> kCodeShift) * qs * scale2[r];
+      h[i * n + r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(silu(v) * v2));
+    } else {
+      y[i * n + r] = v;
+    }
   }
 }
 
-template <int MT, int T, int SK, bool SWIGLU>
+template <int MT, int T, int SK, int UPW, bool SWIGLU>
 void launch_stream(const uint32_t* p1, const float* s1, const uint32_t* p2, const float* s2, int64_t n, int64_t k,
                    const int8_t* q, const float* q_scale, int64_t m, float* y, uint16_t* h, hipStream_t stream) {
   const int64_t nb = (n + 16 * T - 1) / (16 * T), mb = (m + 16 * MT - 1) / (16 * MT);
-  hipLaunchKernelGGL((gemm_i8_stream_kernel<MT, T, SK, SWIGLU>), dim3(static_cast<unsigned>(nb * mb)),
+  hipLaunchKernelGGL((gemm_i8_stream_kernel<MT, T, SK, UPW, SWIGLU>), dim3(static_cast<unsigned>(nb * mb)),
                      dim3(SK * kWave), 0, stream, reinterpret_cast<const uint4*>(p1), s1,
                      reinterpret_cast<const uint4*>(p2), s2, n, words_per_row(k) / 4, q, q_scale, m, nb, y, h);
-}
-
-// Chunk c of a row, codes 0 from the end of the row on.
-__device__ __forceinline__ i32x4_t load_chunk(const uint4* __restrict__ row, int64_t c, int64_t chunks) {
-  const i32x4_t v = *reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1));
-  const int keep = c < chunks ? -1 : 0;
-  return v & keep;
 }
 
 // Tile of a workgroup. Workgroups go round the 8 XCDs, each with its own L2:
@@ -310,22 +316,18 @@ void launch_tile(const uint32_t* p1, const float* s1, const uint32_t* p2, const 
 
 hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
                                   const float* q_scale, int64_t m, float* y, hipStream_t stream) {
-  if (m > 128) {
-    launch_tile<2, 4, 4, 2, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream);
-    return hipGetLastError();
-  }
-  launch_stream<1, 1, 4, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream);
+  if (m > 128) launch_tile<2, 4, 4, 2, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream);
+  else launch_stream<1, 1, 8, 2, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_gate_up_i8(const uint32_t* gate, const float* gate_scale, const uint32_t* up,
                                     const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
                                     const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream) {
-  if (m > 128) {
+  if (m > 128)
     launch_tile<2, 4, 4, 2, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream);
-    return hipGetLastError();
-  }
-  launch_stream<1, 1, 4, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream);
+  else
+    launch_stream<1, 1, 8, 2, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream);
   return hipGetLastError();
 }
 
