@@ -234,7 +234,7 @@ int ternary_swiglu_gate_up_i8(const uint32_t* gate_packed, const float* gate_sca
 
 int64_t pbg_lora_workspace_bytes(int64_t m, int64_t rank) {
   if (m < 1 || m > PBG_MAX_ROWS || rank < 1 || rank > PBG_LORA_MAX_RANK) return 0;
-  return 4 * m * rank * pbg::lora_slices(m);
+  return pbg::lora_workspace_bytes(m, static_cast<int>(rank));
 }
 
 int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
@@ -250,7 +250,7 @@ int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16
   if (workspace_bytes < pbg_lora_workspace_bytes(m, rank)) return PBG_ERR_WORKSPACE;
   if (pending_error()) return PBG_ERR_HIP;
   return finish(pbg::launch_lora_add(y, x, ids, a, b, scale, m, n, k, static_cast<int>(adapters),
-                                     static_cast<int>(rank), out, static_cast<float*>(workspace), stream));
+                                     static_cast<int>(rank), out, workspace, stream));
 }
 
 int pbg_stream_read(const void* src, int64_t bytes, uint32_t* sink, hipStream_t stream) {

@@ -2,40 +2,89 @@
 // many requests at once beside a shared projection; rows without an adapter
 // are passed through.
 //
-// Two launches. The first forms v_i = A_a x_i on the f16 matrix cores (fp16
-// products are exact in its fp32 sums), K split over the waves of a workgroup
-// and, for few rows, over workgroups; the slices' sums go to the workspace.
-// The second adds the slices in order and multiplies by B_a: v stays fp32 in
-// effect, split into two fp16 parts, so that B_a can stay fp16 on the matrix
+// v_i = A_a x_i on the f16 matrix cores (fp16 products are exact in its fp32
+// sums), then the product with B_a added to y. Between the two v is fp32 in
+// effect: it is split into two fp16 parts after a power of two has
+// brought the row's largest |v| to [2^13, 2^14), which hold v to 2^-22 of
+// itself (2^-38 of the row's largest) and let B_a stay fp16 on the matrix
 // cores.
 //
-// Both take 16 rows at a time and run once for each different adapter among
-// them; a row takes the result of its own adapter by a select, so infinities
-// or NaN in another request's adapter never reach it.
+// Rows come in any order. A workgroup takes a block of R rows, sorts them by
+// adapter in LDS and cuts the sorted list into groups of at most 16 rows of
+// one adapter, which is what a matrix instruction takes: an adapter's weights
+// are read once per group, not once per row, and only for its own rows, so
+// that NaN in one adapter cannot reach another's rows.
 #include "pbg_device.hpp"
 #include "pbg_internal.hpp"
 
 namespace pbg {
 namespace {
 
-constexpr int kRows = 16;
+constexpr int kRows = 16;       // rows of a group
 constexpr int kWaves = 4;
+constexpr int kMaxSlices = 16;  // slices of K
 
-// ids of a 16-row tile, -1 for rows past m and rows without an adapter (lane
-// l of every wave holds row l % 16).
-__device__ __forceinline__ int tile_id(const int32_t* __restrict__ ids, int64_t row, int64_t m, int adapters) {
-  const int id = row < m ? ids[row] : -1;
-  return id >= 0 && id < adapters ? id : -1;
+// Up to 16 rows are one block whose second launch adds the slices itself.
+bool lora_one_block(int64_t m) { return m <= kRows; }
+
+// Slices of K that give the chip about 1,024 workgroups of the first launch.
+int lora_slices(int64_t m) {
+  if (lora_one_block(m)) return kMaxSlices;
+  const int64_t s = 1024 * kRows / m;
+  return static_cast<int>(s < 2 ? 2 : s > 8 ? 8 : s);
 }
 
-// Bit i (0..15): row i is the tile's first one with its adapter.
-__device__ __forceinline__ uint32_t first_rows(int id) {
-  const int li = threadIdx.x & 15;
-  bool first = id >= 0;
+int rank_padded(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+// The groups of R rows from m0 on. Built by the first R threads (R <= 64: one
+// wave); group g is order[start[g]] .. order[start[g + 1] - 1]. Rows without
+// an adapter come last, in groups with id -1; rows past m are left out.
+template <int R>
+struct Groups {
+  int key[R];         // adapter of a row, `adapters` for none, INT_MAX past m
+  int16_t order[R];   // rows by key
+  int16_t start[R + 1];
+  int id[R];          // adapter of a group
+  int count;
+
+  __device__ void build(const int32_t* __restrict__ ids, int64_t m0, int64_t m, int adapters) {
+    static_assert(R <= kWave, "one wave sorts");
+    const int i = threadIdx.x;
+    if (i < kWave) {
+      int k = 0x7FFFFFFF;
+      if (i < R && m0 + i < m) {
+        const int t = ids[m0 + i];
+        k = t >= 0 && t < adapters ? t : adapters;
+      }
+      int place = 0;
 #pragma unroll
-  for (int j = 0; j < 15; ++j) first &= !(j < li && __builtin_amdgcn_readlane(id, j) == id);
-  return static_cast<uint32_t>(__ballot(first)) & 0xFFFFu;
-}
+      for (int j = 0; j < R; ++j) {
+        const int o = __builtin_amdgcn_readlane(k, j);
+        place += o < k || (o == k && j < i);
+      }
+      if (i < R) {
+        key[place] = k;
+        order[place] = static_cast<int16_t>(i);
+      }
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const int mine = i < R ? key[i] : 0x7FFFFFFF;
+      const bool live = mine != 0x7FFFFFFF;
+      const bool first = live && (i % kRows == 0 || key[i - 1] != mine);
+      const uint64_t firsts = __ballot(first), lives = __ballot(live);
+      if (first) {
+        const int g = __popcll(firsts & ((1ull << i) - 1));
+        start[g] = static_cast<int16_t>(i);
+        id[g] = mine < adapters ? mine : -1;
+      }
+      if (i == 0) {
+        count = __popcll(firsts);
+        start[count] = static_cast<int16_t>(__popcll(lives));
+      }
+    }
+    __syncthreads();
+  }
+};
 
 // Eight fp16 elements p[c .. c + 7], zero from column k on; FAST: 16-byte
 // aligned and k a multiple of 8.
@@ -53,33 +102,44 @@ __device__ __forceinline__ mfma_half8_t load8(const uint16_t* __restrict__ p, in
   }
 }
 
-// v[slice][row][rank] for one 16-row tile (blockIdx.x) and one slice of K
-// (blockIdx.y); blockIdx.z is the first of the tile's adapters (stepping by
-// gridDim.z). The waves take 32-column steps in turn, U steps of loads in
-// flight; K is cut into slices until the launch fills the chip, since a tile
-// alone is bound by the latency of its loads.
-template <int RT, bool FAST>
+// Power of two (as its exponent) that brings a row's largest |v| to [2^13, 2^14).
+__device__ __forceinline__ int exponent_of(float top) {
+  return top > 0.0f && top < __builtin_inff() ? 13 - ilogbf(top) : 0;
+}
+
+__device__ __forceinline__ float row_max16(float v) {
+  v = fmaxf(v, row_ror<8>(v));
+  v = fmaxf(v, row_ror<4>(v));
+  v = fmaxf(v, row_ror<2>(v));
+  return fmaxf(v, row_ror<1>(v));
+}
+
+// First product: v[slice][row][rank] for the row block blockIdx.x, the slice
+// of K blockIdx.y and the groups blockIdx.z, + gridDim.z, ... The waves take
+// 32-column steps in turn, U steps of loads in flight. A group alone is bound
+// by the latency of its loads, so K is sliced until the launch fills the chip.
+template <int R, int RT, bool FAST>
 __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t* __restrict__ x,
                                                                   const int32_t* __restrict__ ids,
                                                                   const uint16_t* __restrict__ a, int64_t m, int64_t k,
                                                                   int adapters, int rank, int64_t k_slice,
                                                                   float* __restrict__ v) {
-  constexpr int U = RT >= 8 ? 2 : RT >= 4 ? 4 : 8;
+  constexpr int U = RT >= 8 ? 2 : 4;
+  __shared__ Groups<R> groups;
   __shared__ mfma_float4_t part[kWaves - 1][RT][kWave];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int li = lane & 15, lg = lane >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  const int id = tile_id(ids, m0 + li, m, adapters);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * R;
+  groups.build(ids, m0, m, adapters);
   const int64_t k0 = blockIdx.y * k_slice;
   const int64_t k1 = k0 + k_slice < k ? k0 + k_slice : k;
-  const uint16_t* xr = x + (m0 + li < m ? m0 + li : m - 1) * k;
-  uint32_t todo = first_rows(id);
-  for (int d = 0; todo; ++d) {
-    const int f = __builtin_ctz(todo);
-    todo &= todo - 1;
-    if (d % gridDim.z != blockIdx.z) continue;
-    const int ad = __builtin_amdgcn_readlane(id, f);
+  const int count = __builtin_amdgcn_readfirstlane(groups.count);
+  for (int g = blockIdx.z; g < count; g += gridDim.z) {
+    const int ad = __builtin_amdgcn_readfirstlane(groups.id[g]);
+    if (ad < 0) break;  // the groups without an adapter are the last ones
+    const int p0 = groups.start[g], p1 = groups.start[g + 1];
+    const uint16_t* xr = x + (m0 + groups.order[p0 + li < p1 ? p0 + li : p0]) * k;
     const uint16_t* ar[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -87,6 +147,7 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t
       ar[t] = a + (static_cast<int64_t>(ad) * rank + (j < rank ? j : rank - 1)) * k;
     }
     mfma_float4_t acc[RT] = {};
+#pragma unroll 1
     for (int64_t c0 = k0 + 32 * wave; c0 < k1; c0 += 32 * kWaves * U) {
       mfma_half8_t xv[U], av[U][RT];
 #pragma unroll
@@ -108,188 +169,276 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t
       for (int t = 0; t < RT; ++t) part[wave - 1][t][lane] = acc[t];
     }
     __syncthreads();
-    if (wave == 0) {
+    if (wave > 0) continue;
+    // lane: v[4 lg + e][16 t + li] of the group's rows
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
+    for (int t = 0; t < RT; ++t) {
 #pragma unroll
-        for (int w = 0; w < kWaves - 1; ++w) acc[t] += part[w][t][lane];
-        const int j = 16 * t + li;
+      for (int w = 0; w < kWaves - 1; ++w) acc[t] += part[w][t][lane];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * lg + e;  // row of the tile
-          const int idi = __shfl(id, i);
-          if (j < rank && idi == ad) v[(blockIdx.y * m + m0 + i) * rank + j] = acc[t][e];
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int at = p0 + 4 * lg + e;
+        if (at < p1 && 16 * t + li < rank)
+          v[(blockIdx.y * m + m0 + groups.order[at]) * rank + 16 * t + li] = acc[t][e];
       }
     }
   }
 }
 
+// v of one row on the 16 lanes of a DPP row, the slices added in order: its
+// two fp16 parts to hi and lo [16 RT], and the factor that undoes the power of
+// two, times the adapter's scale.
+template <int RT>
+__device__ __forceinline__ void join_row(const float* __restrict__ v, int64_t slice_stride, int slices, int rank,
+                                         float scale, _Float16* hi, _Float16* lo, float* factor) {
+  const int li = threadIdx.x & 15;
+  float s[RT], top = 0.0f;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int j = 16 * t + li;
+    float p[kMaxSlices];
+#pragma unroll
+    for (int q = 0; q < kMaxSlices; ++q) p[q] = q < slices ? v[q * slice_stride + (j < rank ? j : 0)] : 0.0f;
+    s[t] = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kMaxSlices; ++q) s[t] += p[q];
+    if (j >= rank) s[t] = 0.0f;
+    top = fmaxf(top, fabsf(s[t]));
+  }
+  const int ex = exponent_of(row_max16(top));
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const float w = ldexpf(s[t], ex);
+    const _Float16 h = static_cast<_Float16>(w);
+    hi[16 * t + li] = h;
+    lo[16 * t + li] = static_cast<_Float16>(w - static_cast<float>(h));
+  }
+  if (li == 0) *factor = ldexpf(scale, -ex);
+}
+
+// The same for every row with an adapter, parts [m][2][16 RT] and factors [m]
+// to memory; 16 rows a workgroup.
+template <int RT>
+__global__ __launch_bounds__(256) void lora_join_kernel(const int32_t* __restrict__ ids, const float* __restrict__ scale,
+                                                        int64_t m, int adapters, int rank, int slices,
+                                                        const float* __restrict__ v, _Float16* __restrict__ parts,
+                                                        float* __restrict__ factors) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
+  if (row >= m) return;
+  const int id = ids[row];
+  if (id < 0 || id >= adapters) return;
+  _Float16* hi = parts + row * (32 * RT);
+  join_row<RT>(v + row * rank, m * rank, slices, rank, scale[id], hi, hi + 16 * RT, factors + row);
+}
+
 typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
 
-// out = y + (s_a 2^-e) B_a (hi + lo) for one 16-row tile and 16 C kWaves
-// columns. First the tile's v: the slices' sums in order, then a power of two
-// that brings the row's largest |v| to [2^13, 2^14), then two fp16 parts,
-// which hold v to 2^-22 of itself (2^-38 of the row's largest). One matrix
-// instruction takes 16 of the rank with both parts: its 32 columns are
-// [hi | lo] against [B_a | B_a]. With B_a as the row operand a lane ends up
-// with four consecutive outputs of one row. Bound by y and out; the C column
-// tiles of a wave are loaded together.
-template <int RT, int C, bool FAST>
+// out = y + (s_a 2^-e) B_a (hi + lo) for a row block and 16 C columns of each
+// wave, the groups blockIdx.y, + gridDim.y, ... of the block. B_a is the row
+// operand of the matrix instruction, so a lane gets four consecutive outputs
+// of one row. Ranks over 16 take 32 of the rank at a time, first hi, then lo,
+// on one load of B_a; up to 16 one instruction takes both, [hi | lo] against
+// [B_a | B_a]. Bound by y and out, which a wave reads and writes in pieces of
+// 64 C bytes a row: the product goes through LDS to that order. JOIN: the
+// block's only group adds the slices of v itself.
+template <int R, int RT, int C, bool JOIN, bool FAST>
 __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, const int32_t* __restrict__ ids,
                                                                 const uint16_t* __restrict__ b,
                                                                 const float* __restrict__ scale, int64_t m, int64_t n,
                                                                 int adapters, int rank, int slices, int64_t n_blocks,
-                                                                const float* __restrict__ v, float* out) {
+                                                                const float* __restrict__ v,
+                                                                const _Float16* __restrict__ parts,
+                                                                const float* __restrict__ factors, float* out) {
+  constexpr int KT = RT > 1 ? RT / 2 : 1;  // loads of B_a per column tile
   constexpr int RP = 16 * RT;
-  __shared__ _Float16 parts[2][kRows][RP + 8];
-  __shared__ float back[kRows];
+  constexpr int kTile = 16 * C;            // columns of a wave
+  constexpr int kGroup = kTile / 4;        // lanes on one row of y
+  constexpr int kPieces = 16 * kGroup / kWave;
+  __shared__ Groups<R> groups;
+  __shared__ _Float16 own[JOIN ? kRows : 1][2][RP + 8];
+  __shared__ float own_factor[kRows];
+  __shared__ float turn[kWaves][kRows][kTile + 4];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int li = lane & 15, lg = lane >> 4;
-  const int64_t m0 = blockIdx.x / n_blocks * kRows;
-  const int id = tile_id(ids, m0 + li, m, adapters);
-  {
-    const int i = threadIdx.x >> 4;  // row of the tile, on the 16 lanes of a DPP row
-    const int idi = __shfl(id, i);
-    float s[RT], top = 0.0f;
+  const int64_t m0 = blockIdx.x / n_blocks * R;
+  groups.build(ids, m0, m, adapters);
+  const int64_t n0 = (blockIdx.x % n_blocks * kWaves + wave) * kTile;
+  const int count = __builtin_amdgcn_readfirstlane(groups.count);
+  const int pc = 4 * (lane % kGroup);  // this lane's columns of y and out, rows lane / kGroup + i (64 / kGroup)
+  const int64_t r0 = n0 + pc;
+  for (int g = blockIdx.y; g < count; g += gridDim.y) {
+    const int ad = __builtin_amdgcn_readfirstlane(groups.id[g]);
+    if (ad < 0 && y == out) break;  // nothing left to copy
+    const int p0 = groups.start[g], p1 = groups.start[g + 1];
+    // y and B first, so that they are in flight while v is made
+    mfma_float4_t base[kPieces];
+    int64_t row[kPieces];
+    bool in[kPieces];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int j = 16 * t + li;
-      s[t] = 0.0f;
-      if (idi >= 0 && j < rank)
-        for (int p = 0; p < slices; ++p) s[t] += v[(p * m + m0 + i) * rank + j];
-      top = fmaxf(top, fabsf(s[t]));
+    for (int i = 0; i < kPieces; ++i) {
+      const int at = p0 + lane / kGroup + i * (kWave / kGroup);
+      in[i] = at < p1;
+      row[i] = (m0 + groups.order[in[i] ? at : p0]) * n;
+      base[i] = mfma_float4_t{};
+      if (in[i] && r0 + 4 <= n) {
+        base[i] = *reinterpret_cast<const f32x4_any_t*>(y + row[i] + r0);
+      } else if (in[i]) {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (r0 + e < n) base[i][e] = y[row[i] + r0 + e];
+      }
     }
-    top = fmaxf(top, row_ror<8>(top));
-    top = fmaxf(top, row_ror<4>(top));
-    top = fmaxf(top, row_ror<2>(top));
-    top = fmaxf(top, row_ror<1>(top));
-    const int e = top > 0.0f && top < __builtin_inff() ? 13 - ilogbf(top) : 0;
+    if (ad >= 0) {
+      mfma_half8_t bv[C][KT];
+      const uint16_t* ba = b + static_cast<int64_t>(ad) * n * rank;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const float w = ldexpf(s[t], e);
-      const _Float16 hi = static_cast<_Float16>(w);
-      parts[0][i][16 * t + li] = hi;
-      parts[1][i][16 * t + li] = static_cast<_Float16>(w - static_cast<float>(hi));
+      for (int c = 0; c < C; ++c) {
+        const int64_t r = n0 + 16 * c + li;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+          bv[c][t] = load8<FAST>(ba + (r < n ? r : n - 1) * rank, RT > 1 ? 32 * t + 8 * lg : 8 * (lg & 1), rank);
+      }
+      // operand of the rows: lane (li, lg) holds 8 values of part `half` of row li
+      mfma_half8_t vf[2][KT];
+      float bk;
+      const _Float16* src;
+      if constexpr (JOIN) {
+        const int i = threadIdx.x >> 4;
+        __syncthreads();
+        join_row<RT>(v + (m0 + groups.order[p0 + i < p1 ? p0 + i : p0]) * rank, m * rank, slices, rank, scale[ad],
+                     own[i][0], own[i][1], own_factor + i);
+        __syncthreads();
+        src = own[li][0];
+        bk = own_factor[li];
+      } else {
+        const int64_t at = m0 + groups.order[p0 + li < p1 ? p0 + li : p0];
+        src = parts + at * (2 * RP);
+        bk = factors[at];
+      }
+      constexpr int kLo = JOIN ? RP + 8 : RP;  // from hi to lo
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        if constexpr (RT > 1) {
+          vf[0][t] = *reinterpret_cast<const mfma_half8_t*>(src + 32 * t + 8 * lg);
+          vf[1][t] = *reinterpret_cast<const mfma_half8_t*>(src + kLo + 32 * t + 8 * lg);
+        } else {
+          vf[0][t] = *reinterpret_cast<const mfma_half8_t*>(src + (lg >> 1) * kLo + 8 * (lg & 1));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        mfma_float4_t d = {};
+#pragma unroll
+        for (int h = 0; h < (RT > 1 ? 2 : 1); ++h)
+#pragma unroll
+          for (int t = 0; t < KT; ++t) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv[c][t], vf[h][t], d, 0, 0, 0);
+        *reinterpret_cast<mfma_float4_t*>(&turn[wave][li][16 * c + 4 * lg]) = bk * d;
+      }
+      // one wave writes and reads its own part: LDS is in order within a wave
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        base[i] += *reinterpret_cast<const mfma_float4_t*>(&turn[wave][lane / kGroup + i * (kWave / kGroup)][pc]);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    if (li == 0) back[i] = idi >= 0 ? ldexpf(scale[idi], -e) : 0.0f;
-  }
-  __syncthreads();
-  mfma_half8_t vf[RT];
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
-    vf[t] = *reinterpret_cast<const mfma_half8_t*>(&parts[lg >> 1][li][16 * t + 8 * (lg & 1)]);
-  const float bk = back[li];
-  const int64_t n0 = (blockIdx.x % n_blocks * kWaves + wave) * (16 * C);
-  if (n0 >= n) return;
-  const bool in = m0 + li < m;
-  const float* yr = y + (m0 + li) * n;
-  float* o = out + (m0 + li) * n;
-  mfma_float4_t base[C], acc[C];
+    for (int i = 0; i < kPieces; ++i) {
+      if (in[i] && r0 + 4 <= n) {
+        *reinterpret_cast<f32x4_any_t*>(out + row[i] + r0) = base[i];
+      } else if (in[i]) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int64_t r = n0 + 16 * c + 4 * lg;
-    acc[c] = mfma_float4_t{};
-    base[c] = mfma_float4_t{};
-    if (in && r + 4 <= n) {
-      base[c] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any_t*>(yr + r));
-    } else if (in) {
-#pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (r + e < n) base[c][e] = yr[r + e];
-    }
-  }
-  for (uint32_t todo = first_rows(id); todo; todo &= todo - 1) {
-    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-    const uint16_t* ba = b + static_cast<int64_t>(ad) * n * rank;
-    mfma_half8_t bv[C][RT];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int64_t r = n0 + 16 * c + li;
-#pragma unroll
-      for (int t = 0; t < RT; ++t) bv[c][t] = load8<FAST>(ba + (r < n ? r : n - 1) * rank, 16 * t + 8 * (lg & 1), rank);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      mfma_float4_t d = {};
-#pragma unroll
-      for (int t = 0; t < RT; ++t) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv[c][t], vf[t], d, 0, 0, 0);
-      if (id == ad) acc[c] = d;
-    }
-  }
-  if (!in) return;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int64_t r = n0 + 16 * c + 4 * lg;
-    if (id >= 0) base[c] += bk * acc[c];
-    if (r + 4 <= n) {
-      *reinterpret_cast<f32x4_any_t*>(o + r) = base[c];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (r + e < n) o[r + e] = base[c][e];
+        for (int e = 0; e < 3; ++e)
+          if (r0 + e < n) out[row[i] + r0 + e] = base[i][e];
+      }
     }
   }
 }
 
-// Columns of one slice: whole steps of the down kernel's four waves.
+// Columns of one slice: whole steps of four waves.
 int64_t slice_columns(int64_t k, int slices) {
-  const int64_t step = 32 * kWaves;
-  return ((k + slices - 1) / slices + step - 1) / step * step;
+  return ((k + slices - 1) / slices + 127) / 128 * 128;
+}
+
+struct Args {
+  const float* y;
+  const uint16_t* x;
+  const int32_t* ids;
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* scale;
+  int64_t m, n, k;
+  int adapters, rank;
+  float* out;
+  void* ws;
+  hipStream_t stream;
+};
+
+// Workspace: the slices' sums [slices][m][rank], then, 16-byte aligned, the
+// parts [m][2][padded rank] and the factors [m].
+int64_t sums_bytes(int64_t m, int rank) { return (4 * m * rank * lora_slices(m) + 15) / 16 * 16; }
+
+template <int R, int RT, bool FAST>
+void launch_down(const Args& g, int slices, int64_t k_slice, int64_t z) {
+  hipLaunchKernelGGL((lora_down_kernel<R, RT, FAST>),
+                     dim3(static_cast<unsigned>((g.m + R - 1) / R), slices, static_cast<unsigned>(z)),
+                     dim3(kWaves * kWave), 0, g.stream, g.x, g.ids, g.a, g.m, g.k, g.adapters, g.rank, k_slice,
+                     static_cast<float*>(g.ws));
+}
+
+template <int R, int RT, int C, bool JOIN, bool FAST>
+void launch_up(const Args& g, int slices, int64_t z) {
+  const int64_t blocks = (g.m + R - 1) / R, nb = (g.n + 16 * C * kWaves - 1) / (16 * C * kWaves);
+  const _Float16* parts = reinterpret_cast<const _Float16*>(static_cast<char*>(g.ws) + sums_bytes(g.m, g.rank));
+  hipLaunchKernelGGL((lora_up_kernel<R, RT, C, JOIN, FAST>),
+                     dim3(static_cast<unsigned>(blocks * nb), static_cast<unsigned>(z)), dim3(kWaves * kWave), 0,
+                     g.stream, g.y, g.ids, g.b, g.scale, g.m, g.n, g.adapters, g.rank, slices, nb,
+                     static_cast<const float*>(g.ws), parts, reinterpret_cast<const float*>(parts + g.m * 32 * RT),
+                     g.out);
 }
 
 template <int RT, bool FAST>
-void launch(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
-            const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out, float* ws,
-            hipStream_t stream) {
-  const int64_t tiles = (m + kRows - 1) / kRows;
-  const int64_t ks = slice_columns(k, lora_slices(m));
-  const int slices = static_cast<int>((k + ks - 1) / ks);
-  // few tiles: their adapters go to workgroups of their own
-  const unsigned dz = tiles <= 32 ? (m < 16 ? static_cast<unsigned>(m) : 16) : 1;
-  hipLaunchKernelGGL((lora_down_kernel<RT, FAST>), dim3(static_cast<unsigned>(tiles), slices, dz),
-                     dim3(kWaves * kWave), 0, stream, x, ids, a, m, k, adapters, rank, ks, ws);
-  constexpr int C = RT >= 8 ? 2 : 4;
-  if (tiles * n >= 16 * 4096) {
-    const int64_t nb = (n + 16 * C * kWaves - 1) / (16 * C * kWaves);
-    hipLaunchKernelGGL((lora_up_kernel<RT, C, FAST>), dim3(static_cast<unsigned>(nb * tiles)), dim3(kWaves * kWave), 0,
-                       stream, y, ids, b, scale, m, n, adapters, rank, slices, nb, ws, out);
-  } else {
-    const int64_t nb = (n + 16 * kWaves - 1) / (16 * kWaves);
-    hipLaunchKernelGGL((lora_up_kernel<RT, 1, FAST>), dim3(static_cast<unsigned>(nb * tiles)), dim3(kWaves * kWave), 0,
-                       stream, y, ids, b, scale, m, n, adapters, rank, slices, nb, ws, out);
+void launch(const Args& g) {
+  const int64_t ks = slice_columns(g.k, lora_slices(g.m));
+  const int slices = static_cast<int>((g.k + ks - 1) / ks);
+  if (lora_one_block(g.m)) {
+    launch_down<16, RT, FAST>(g, slices, ks, g.m);
+    launch_up<16, RT, 1, true, FAST>(g, slices, g.m);
+    return;
   }
+  launch_down<64, RT, FAST>(g, slices, ks, 16);
+  _Float16* parts = reinterpret_cast<_Float16*>(static_cast<char*>(g.ws) + sums_bytes(g.m, g.rank));
+  hipLaunchKernelGGL((lora_join_kernel<RT>), dim3(static_cast<unsigned>((g.m + 15) / 16)), dim3(256), 0, g.stream,
+                     g.ids, g.scale, g.m, g.adapters, g.rank, slices, static_cast<const float*>(g.ws), parts,
+                     reinterpret_cast<float*>(parts + g.m * 32 * RT));
+  if (g.m <= 256) launch_up<64, RT, 2, false, FAST>(g, slices, 16);
+  else launch_up<64, RT, 4, false, FAST>(g, slices, 4);
 }
 
 template <bool FAST>
-void launch_rank(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
-                 const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out, float* ws,
-                 hipStream_t stream) {
-  if (rank <= 16) launch<1, FAST>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
-  else if (rank <= 32) launch<2, FAST>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
-  else if (rank <= 64) launch<4, FAST>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
-  else launch<8, FAST>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
+void launch_rank(const Args& g) {
+  switch (rank_padded(g.rank)) {
+    case 16: return launch<1, FAST>(g);
+    case 32: return launch<2, FAST>(g);
+    case 64: return launch<4, FAST>(g);
+    default: return launch<8, FAST>(g);
+  }
 }
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 }  // namespace
 
-// Enough slices of K to fill the chip with 16-row tiles.
-int lora_slices(int64_t m) {
-  const int64_t tiles = (m + kRows - 1) / kRows;
-  const int64_t s = 1024 / tiles;
-  return static_cast<int>(s < 2 ? 2 : s > 16 ? 16 : s);
+int64_t lora_workspace_bytes(int64_t m, int rank) {
+  return sums_bytes(m, rank) + (lora_one_block(m) ? 0 : 4 * m * (rank_padded(rank) + 1));
 }
 
 hipError_t launch_lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
                            const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out,
-                           float* ws, hipStream_t stream) {
-  if (k % 8 == 0 && rank % 8 == 0 && !off16(x) && !off16(a) && !off16(b))
-    launch_rank<true>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
-  else
-    launch_rank<false>(y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream);
+                           void* ws, hipStream_t stream) {
+  const Args g{y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream};
+  if (k % 8 == 0 && rank % 8 == 0 && !off16(x) && !off16(a) && !off16(b)) launch_rank<true>(g);
+  else launch_rank<false>(g);
   return hipGetLastError();
 }
 

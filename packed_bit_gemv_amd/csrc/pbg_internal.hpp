@@ -81,11 +81,11 @@ hipError_t launch_swiglu_gate_up_i8(const uint32_t* gate, const float* gate_scal
                                     const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
                                     const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream);
 
-// Adapters; ws holds lora_slices(m) * m * rank floats. out may be y.
-int lora_slices(int64_t m);
+// Adapters; ws holds lora_workspace_bytes(m, rank). out may be y.
+int64_t lora_workspace_bytes(int64_t m, int rank);
 hipError_t launch_lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
                            const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out,
-                           float* ws, hipStream_t stream);
+                           void* ws, hipStream_t stream);
 
 // One read of `bytes` (a multiple of 16) from 16-byte aligned src, folded into sink.
 hipError_t launch_stream_read(const void* src, int64_t bytes, uint32_t* sink, hipStream_t stream);
