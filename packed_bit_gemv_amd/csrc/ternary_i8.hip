@@ -35,15 +35,14 @@ __device__ __forceinline__ i32x4_t word_bytes(uint32_t w) {
   return o;
 }
 
-// Chunk c of a row, codes 0 from the end of the row on. The streaming form
-// marks the load non-temporal (each weight byte is read once per call).
+// Chunk c of a row (the last one past its end, for the caller to mask). The
+// streaming form marks the load non-temporal (each weight byte is read once
+// per call).
 __device__ __forceinline__ i32x4_t load_chunk(const uint4* __restrict__ row, int64_t c, int64_t chunks) {
-  const i32x4_t v = *reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1));
-  return v & (c < chunks ? -1 : 0);
+  return *reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1));
 }
 __device__ __forceinline__ i32x4_t load_chunk_nt(const uint4* __restrict__ row, int64_t c, int64_t chunks) {
-  const i32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1)));
-  return v & (c < chunks ? -1 : 0);
+  return __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1)));
 }
 
 // Matrix product of few activation rows: a workgroup owns T tiles of 16
@@ -115,7 +114,7 @@ __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const i32x4_t b = word_bytes(static_cast<uint32_t>(w[j][t][s]));
+          const i32x4_t b = word_bytes(static_cast<uint32_t>(w[j][t][s] & (4 * (u0 + j) + lg < chunks ? -1 : 0)));
 #pragma unroll
           for (int a = 0; a < MT; ++a)
             acc[a][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[j][a][s], b, acc[a][t], 0, 0, 0);
@@ -177,13 +176,29 @@ __device__ __forceinline__ void tile_of_block(int m_blocks, int n_blocks, int& m
   nb = in / rows;
 }
 
+// Order of one word's work: each matrix instruction is followed by a share of
+// the next word's operand reads and decode, which run under it.
+template <int TM, int TN>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < TM * TN; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                // one matrix instruction
+    if (i < TM) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // one LDS read
+    __builtin_amdgcn_sched_group_barrier(0x002, 12 / TM, 0);          // vector instructions
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Matrix product of many activation rows: a workgroup of WM x WN waves owns
 // 32 TM WM rows by 32 TN WN columns, a wave TM x TN tiles of the 32x32x32 i8
 // matrix instruction, whose A operand is activations and B operand decoded
-// codes. K goes in steps of two chunks (128 columns). The activations of a
-// step go through LDS, double-buffered, one barrier a step: the next step's
-// loads are issued before the step's products and stored after them. 16-byte
-// piece c of row i sits at place c ^ (i % 8) of its 128 bytes, so that both
+// codes. K goes in steps of two chunks (128 columns), four words a lane. The
+// activations go through LDS, double-buffered with one barrier a step: a step
+// starts by storing the next step's activations, which were loaded during the
+// step before, into the buffer that every wave has read by then, and reaches
+// the barrier with only its last word's products left, whose operands are in
+// registers; they run while the first operands of the next step are read.
+// 16-byte piece c of row i sits at place c ^ (i % 8) of its 128 bytes, so that both
 // the stores and the operand reads touch every bank once in eight lanes. The
 // packed words come straight to registers (lane (i, g) = (l % 32, l / 32) the
 // chunk 2u + g of column i) and are decoded once for all TM row tiles, which
@@ -230,50 +245,70 @@ __global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
     xo[i] = row * 8 + (c ^ (row & 7));
   }
   const int half = (threadIdx.x & 7) >> 2;  // chunk of the step that this thread's pieces belong to
-  i32x4_t xv[kLoads], wv[TN];
+  i32x4_t xv[kLoads], wv[TN], w[TN], a[2][TM], b[2][TN];
+  // Steps past the last one read it again, chunks past the row (the last step of an odd count) the row's last one:
+  // activations as they are, codes 0 (masked when used, so that nothing waits for the load before its step).
+  auto load_x = [&](int64_t u) {
+    const int64_t v = u < steps ? u : steps - 1;
+    const int64_t at = v * 128 - (2 * v + half < chunks ? 0 : 64);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) xv[i] = *reinterpret_cast<const i32x4_t*>(xp[i] + at);
+  };
+  auto load_w = [&](int64_t u) {
+#pragma unroll
+    for (int t = 0; t < TN; ++t) wv[t] = load_chunk(wp[t], 2 * u + lg, chunks);
+  };
+  auto store_x = [&](int buffer) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) xs[buffer][xo[i]] = xv[i];
+  };
+  auto take_w = [&](int64_t u) {
+#pragma unroll
+    for (int t = 0; t < TN; ++t) w[t] = wv[t] & (2 * u + lg < chunks ? -1 : 0);
+  };
+  const int row8 = (wm * TM * 32 + li) * 8;
+  auto operands = [&](int buffer, int s) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) a[s & 1][i] = xs[buffer][row8 + i * 256 + ((4 * lg + s) ^ (li & 7))];
+#pragma unroll
+    for (int t = 0; t < TN; ++t) b[s & 1][t] = word_bytes(static_cast<uint32_t>(w[t][s]));
+  };
   i32x16_t acc[TM][TN] = {};
-  // Chunks past the row (the last step of an odd count) read the last one: activations as they are, codes 0.
+  auto multiply = [&](int s) {
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i)
-    xv[i] = *reinterpret_cast<const i32x4_t*>(xp[i] - (half < chunks ? 0 : 64));
+    for (int t = 0; t < TN; ++t)
 #pragma unroll
-  for (int t = 0; t < TN; ++t) wv[t] = load_chunk(wp[t], lg, chunks);
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) xs[0][xo[i]] = xv[i];
+      for (int i = 0; i < TM; ++i)
+        acc[i][t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[s & 1][i], b[s & 1][t], acc[i][t], 0, 0, 0);
+  };
+
+  load_x(0);
+  load_w(0);
+  store_x(0);
+  load_x(1);
+  take_w(0);
   __syncthreads();
+  operands(0, 0);
   for (int64_t u = 0; u < steps; ++u) {
-    i32x4_t w[TN];
-#pragma unroll
-    for (int t = 0; t < TN; ++t) w[t] = wv[t];
-    const bool more = u + 1 < steps;
-    if (more) {
-      const int64_t at = (u + 1) * 128 - (2 * (u + 1) + half < chunks ? 0 : 64);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) xv[i] = *reinterpret_cast<const i32x4_t*>(xp[i] + at);
-#pragma unroll
-      for (int t = 0; t < TN; ++t) wv[t] = load_chunk(wp[t], 2 * (u + 1) + lg, chunks);
-    }
-    const i32x4_t* xb = xs[u & 1];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      i32x4_t a[TM];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int row = (wm * TM + i) * 32 + li;
-        a[i] = xb[row * 8 + ((4 * lg + s) ^ (row & 7))];
-      }
-#pragma unroll
-      for (int t = 0; t < TN; ++t) {
-        const i32x4_t b = word_bytes(static_cast<uint32_t>(w[t][s]));
-#pragma unroll
-        for (int i = 0; i < TM; ++i) acc[i][t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b, acc[i][t], 0, 0, 0);
-      }
-    }
-    if (more) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) xs[(u + 1) & 1][xo[i]] = xv[i];
-    }
+    const int here = static_cast<int>(u & 1), next = here ^ 1;
+    store_x(next);
+    load_w(u + 1);
+    load_x(u + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    operands(here, 1);
+    multiply(0);
+    interleave<TM, TN>();
+    operands(here, 2);
+    multiply(1);
+    interleave<TM, TN>();
+    operands(here, 3);
+    multiply(2);
+    interleave<TM, TN>();
     __syncthreads();
+    take_w(u + 1);
+    operands(next, 0);
+    multiply(3);
+    interleave<TM, TN>();
   }
 
   // lane: column li of a tile, rows 8 (e / 4) + 4 lg + e % 4
