@@ -48,11 +48,14 @@ __device__ __forceinline__ i32x4_t load_chunk_nt(const uint4* __restrict__ row, 
 // Matrix product of few activation rows: a workgroup owns T tiles of 16
 // weight rows (of gate and of up each with SWIGLU) against MT tiles of 16
 // activation rows and streams the weights. Its SK waves share K in units of
-// 256 columns, UPW units a wave at a time with all their loads in flight
-// before the first product: lane (i, g) = (l % 16, l / 16) holds the 16-byte
-// chunk 4u + g (64 codes) of weight row i and the same 64 bytes of activation
-// row i, so step w of a unit multiplies word w of the chunk with bytes
-// 16w .. 16w + 15. The waves add their int32 sums in LDS (exact in any order).
+// 256 columns, UPW units a wave at a time, the next units' loads in flight
+// under the products: lane (i, g) = (l % 16, l / 16) holds the 16-byte chunk
+// 4u + g (64 codes) of weight row i, and step w of a unit multiplies word w of
+// the chunk with bytes 16w .. 16w + 15 of chunk 4u + g of the activations.
+// Those are loaded 256 consecutive bytes of a row on 16 lanes and turned
+// through LDS that only this wave uses, without a barrier (piece p of row i at
+// place p ^ i: every bank once in 16 lanes): read directly, 16 lanes would
+// touch 16 lines. The waves add their int32 sums in LDS (exact in any order).
 template <int MT, int T, int SK, int UPW, bool SWIGLU>
 __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
     const uint4* __restrict__ packed, const float* __restrict__ scale, const uint4* __restrict__ packed2,
@@ -62,6 +65,7 @@ __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
   constexpr int kThreads = SK * kWave;
   constexpr int kStride = 16 * TT + 4;
   __shared__ int sums[MT * 16][kStride];
+  __shared__ i32x4_t turn[SK][UPW][MT][256];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int li = lane & 15, lg = lane >> 4;
@@ -80,45 +84,59 @@ __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
     const int64_t r = n0 + 16 * (t % T) + li;
     wp[t] = (t < T ? packed : packed2) + (r < n ? r : n - 1) * chunks;
   }
-  const int8_t* xp[MT];
-  bool xin[MT];  // rows past m load nothing and count as 0
-#pragma unroll
-  for (int a = 0; a < MT; ++a) {
-    const int64_t r = m0 + 16 * a + li;
-    xin[a] = r < m;
-    xp[a] = q + (r < m ? r : m - 1) * kp;
-  }
-  i32x4_t acc[MT][TT] = {};
-  for (int64_t u0 = wave * UPW; u0 < units; u0 += SK * UPW) {
-    i32x4_t w[UPW][TT], x[UPW][MT][4];
+  i32x4_t wv[UPW][TT], xv[UPW][MT][4];
+  auto load = [&](int64_t u0) {
 #pragma unroll
     for (int j = 0; j < UPW; ++j)
 #pragma unroll
-      for (int t = 0; t < TT; ++t) w[j][t] = load_chunk_nt(wp[t], 4 * (u0 + j) + lg, chunks);
+      for (int t = 0; t < TT; ++t) wv[j][t] = load_chunk_nt(wp[t], 4 * (u0 + j) + lg, chunks);
+    // load j of a tile: rows 4j + lg, piece li of the unit; rows past m are left out four at a time
 #pragma unroll
     for (int j = 0; j < UPW; ++j) {
-      const int64_t c = 4 * (u0 + j) + lg;
-      const int64_t at = (c < chunks ? c : chunks - 1) * 64;
+      const int64_t c = 4 * (u0 + j) + (li >> 2);
+      const int64_t at = (c < chunks ? c : chunks - 1) * 64 + (li & 3) * 16;
 #pragma unroll
       for (int a = 0; a < MT; ++a)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          x[j][a][s] = i32x4_t{};
-          if (xin[a]) x[j][a][s] = *reinterpret_cast<const i32x4_t*>(xp[a] + at + 16 * s);
+        for (int e = 0; e < 4; ++e) {
+          const int64_t r = m0 + 16 * a + 4 * e;
+          if (r < m) xv[j][a][e] = *reinterpret_cast<const i32x4_t*>(q + (r + lg < m ? r + lg : m - 1) * kp + at);
         }
     }
-    __builtin_amdgcn_sched_barrier(0);
+  };
+  i32x4_t acc[MT][TT] = {};
+  int64_t u0 = wave * UPW;
+  if (u0 < units) load(u0);
+  while (u0 < units) {
+    i32x4_t w[UPW][TT];
+#pragma unroll
+    for (int j = 0; j < UPW; ++j) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t) w[j][t] = wv[j][t] & (4 * (u0 + j) + lg < chunks ? -1 : 0);
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) turn[wave][j][a][(4 * e + lg) * 16 + (li ^ (4 * e + lg))] = xv[j][a][e];
+    }
+    u0 += SK * UPW;
+    if (u0 < units) load(u0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int j = 0; j < UPW; ++j)
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < 4; ++s) {
+        i32x4_t x[MT];
+#pragma unroll
+        for (int a = 0; a < MT; ++a) x[a] = turn[wave][j][a][li * 16 + ((4 * lg + s) ^ li)];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const i32x4_t b = word_bytes(static_cast<uint32_t>(w[j][t][s] & (4 * (u0 + j) + lg < chunks ? -1 : 0)));
+          const i32x4_t b = word_bytes(static_cast<uint32_t>(w[j][t][s]));
 #pragma unroll
           for (int a = 0; a < MT; ++a)
-            acc[a][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[j][a][s], b, acc[a][t], 0, 0, 0);
+            acc[a][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[a], b, acc[a][t], 0, 0, 0);
         }
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 
   // column li of a tile, activation row 4 lg + e
@@ -198,8 +216,8 @@ __device__ __forceinline__ void interleave() {
 // step before, into the buffer that every wave has read by then, and reaches
 // the barrier with only its last word's products left, whose operands are in
 // registers; they run while the first operands of the next step are read.
-// 16-byte piece c of row i sits at place c ^ (i % 8) of its 128 bytes, so that both
-// the stores and the operand reads touch every bank once in eight lanes. The
+// 16-byte piece c of row i sits at place c ^ (i / 2 % 8) of its 128 bytes, so
+// that 16 lanes of a store or an operand read touch each of the 64 banks once. The
 // packed words come straight to registers (lane (i, g) = (l % 32, l / 32) the
 // chunk 2u + g of column i) and are decoded once for all TM row tiles, which
 // is what pays for the decode: 8 vector instructions a word against TM matrix
@@ -218,6 +236,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
   constexpr int kLoads = BM * 8 / kThreads;
   static_assert(BM * 8 % kThreads == 0, "whole loads");
   __shared__ i32x4_t xs[2][BM * 8];
+  __shared__ __align__(16) float row_scale[BM];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int li = lane & 31, lg = lane >> 5;
@@ -242,8 +261,15 @@ __global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
     const int row = (threadIdx.x + i * kThreads) >> 3, c = threadIdx.x & 7;
     const int64_t r = m0 + row;
     xp[i] = q + (r < m ? r : m - 1) * kp + 16 * c;
-    xo[i] = row * 8 + (c ^ (row & 7));
+    xo[i] = row * 8 + (c ^ (row >> 1 & 7));
   }
+  float s1[TN];
+#pragma unroll
+  for (int t = 0; t < TN; ++t) {
+    const int64_t r = n0 + 32 * (t % TC) + li;
+    s1[t] = (t < TC ? scale : scale2)[r < n ? r : n - 1];
+  }
+  for (int i = threadIdx.x; i < BM; i += kThreads) row_scale[i] = q_scale[m0 + i < m ? m0 + i : m - 1];
   const int half = (threadIdx.x & 7) >> 2;  // chunk of the step that this thread's pieces belong to
   i32x4_t xv[kLoads], wv[TN], w[TN], a[2][TM], b[2][TN];
   // Steps past the last one read it again, chunks past the row (the last step of an odd count) the row's last one:
@@ -269,7 +295,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
   const int row8 = (wm * TM * 32 + li) * 8;
   auto operands = [&](int buffer, int s) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) a[s & 1][i] = xs[buffer][row8 + i * 256 + ((4 * lg + s) ^ (li & 7))];
+    for (int i = 0; i < TM; ++i) a[s & 1][i] = xs[buffer][row8 + i * 256 + ((4 * lg + s) ^ (li >> 1 & 7))];
 #pragma unroll
     for (int t = 0; t < TN; ++t) b[s & 1][t] = word_bytes(static_cast<uint32_t>(w[t][s]));
   };
@@ -311,29 +337,37 @@ __global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
     interleave<TM, TN>();
   }
 
-  // lane: column li of a tile, rows 8 (e / 4) + 4 lg + e % 4
+  // lane: column li of a tile, rows 8 g + 4 lg + e; whole tiles store without a check
+  const bool whole = m0 + BM <= m && n0 + 32 * TC <= n;
+  auto store = [&](int64_t at, int i, int t, int e, float qs) {
+    const float v = static_cast<float>(acc[i][t][e] >> kCodeShift) * qs * s1[t];
+    if constexpr (SWIGLU) {
+      const float v2 = static_cast<float>(acc[i][TC + t][e] >> kCodeShift) * qs * s1[TC + t];
+      h[at] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(silu(v) * v2));
+    } else {
+      y[at] = v;
+    }
+  };
 #pragma unroll
-  for (int t = 0; t < TC; ++t) {
-    const int64_t r = n0 + 32 * t + li;
-    if (r >= n) continue;
-    const float s1 = scale[r];
-    const float s2 = SWIGLU ? scale2[r] : 0.0f;
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int g = 0; g < 4; ++g) {
+      const int row = (wm * TM + i) * 32 + 8 * g + 4 * lg;
+      const mfma_float4_t qs = *reinterpret_cast<const mfma_float4_t*>(row_scale + row);
+      const int64_t at = (m0 + row) * n + n0 + li;
+      if (whole) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int64_t ri = m0 + (wm * TM + i) * 32 + 8 * (e / 4) + 4 * lg + e % 4;
-        if (ri >= m) continue;
-        const float qs = q_scale[ri];
-        const float v = static_cast<float>(acc[i][t][e] >> kCodeShift) * qs * s1;
-        if constexpr (SWIGLU) {
-          const float v2 = static_cast<float>(acc[i][TC + t][e] >> kCodeShift) * qs * s2;
-          h[ri * n + r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(silu(v) * v2));
-        } else {
-          y[ri * n + r] = v;
-        }
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int t = 0; t < TC; ++t) store(at + e * n + 32 * t, i, t, 4 * g + e, qs[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int t = 0; t < TC; ++t)
+            if (m0 + row + e < m && n0 + 32 * t + li < n) store(at + e * n + 32 * t, i, t, 4 * g + e, qs[e]);
       }
-  }
+    }
 }
 
 template <int WM, int WN, int TM, int TN, bool SWIGLU>
