@@ -35,37 +35,33 @@ __device__ __forceinline__ i32x4_t word_bytes(uint32_t w) {
   return o;
 }
 
-// Chunk c of a row (the last one past its end, for the caller to mask). The
-// streaming form marks the load non-temporal (each weight byte is read once
-// per call).
+// Chunk c of a row (the last one past its end, for the caller to mask).
 __device__ __forceinline__ i32x4_t load_chunk(const uint4* __restrict__ row, int64_t c, int64_t chunks) {
   return *reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1));
-}
-__device__ __forceinline__ i32x4_t load_chunk_nt(const uint4* __restrict__ row, int64_t c, int64_t chunks) {
-  return __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(row + (c < chunks ? c : chunks - 1)));
 }
 
 // Matrix product of few activation rows: a workgroup owns T tiles of 16
 // weight rows (of gate and of up each with SWIGLU) against MT tiles of 16
 // activation rows and streams the weights. Its SK waves share K in units of
-// 256 columns, UPW units a wave at a time, the next units' loads in flight
-// under the products: lane (i, g) = (l % 16, l / 16) holds the 16-byte chunk
+// 256 columns, the next unit's loads in flight under a unit's products: lane (i, g) = (l % 16, l / 16) holds the 16-byte chunk
 // 4u + g (64 codes) of weight row i, and step w of a unit multiplies word w of
 // the chunk with bytes 16w .. 16w + 15 of chunk 4u + g of the activations.
 // Those are loaded 256 consecutive bytes of a row on 16 lanes and turned
 // through LDS that only this wave uses, without a barrier (piece p of row i at
 // place p ^ i: every bank once in 16 lanes): read directly, 16 lanes would
 // touch 16 lines. The waves add their int32 sums in LDS (exact in any order).
-template <int MT, int T, int SK, int UPW, bool SWIGLU>
+template <int MT, int T, int SK, bool SWIGLU>
 __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
     const uint4* __restrict__ packed, const float* __restrict__ scale, const uint4* __restrict__ packed2,
     const float* __restrict__ scale2, int64_t n, int64_t chunks, const int8_t* __restrict__ q,
     const float* __restrict__ q_scale, int64_t m, int64_t n_blocks, float* __restrict__ y, uint16_t* __restrict__ h) {
   constexpr int TT = SWIGLU ? 2 * T : T;
   constexpr int kThreads = SK * kWave;
-  constexpr int kStride = 16 * TT + 4;
-  __shared__ int sums[MT * 16][kStride];
-  __shared__ i32x4_t turn[SK][UPW][MT][256];
+  __shared__ int sums[MT * TT][4][kWave];  // element e of a lane's four sums of a tile
+  __shared__ __align__(16) float scales[(MT + TT) * 16];  // of the rows, then of the columns
+  const float* row_scale = scales;
+  const float* col_scale = scales + MT * 16;
+  __shared__ i32x4_t turn[SK][MT][256];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int li = lane & 15, lg = lane >> 4;
@@ -73,104 +69,135 @@ __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
   const int64_t m0 = (blockIdx.x / n_blocks) * (16 * MT);
   const int64_t kp = chunks * 64;
   const int64_t units = (chunks + 3) / 4;
-  if constexpr (SK > 1) {
-    for (int i = threadIdx.x; i < MT * 16 * kStride; i += kThreads) (&sums[0][0])[i] = 0;
-    __syncthreads();
+  // Addresses are a uniform pointer, moved from unit to unit, plus 32-bit offsets that stay (a row holds at most
+  // 131,072 codes, so the rows of a workgroup span less than 2^31 bytes).
+  const int64_t row_bytes = chunks * 16;
+  uint32_t wo[T], xo[MT][4];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int64_t r = n0 + 16 * t + li < n ? 16 * t + li : n - 1 - n0;
+    wo[t] = static_cast<uint32_t>(r * row_bytes + lg * 16);
   }
-
-  const uint4* wp[TT];
+  // load e of a tile: rows 4e + lg, piece li of the unit
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int64_t r = n0 + 16 * (t % T) + li;
-    wp[t] = (t < T ? packed : packed2) + (r < n ? r : n - 1) * chunks;
-  }
-  i32x4_t wv[UPW][TT], xv[UPW][MT][4];
-  auto load = [&](int64_t u0) {
+  for (int a = 0; a < MT; ++a)
 #pragma unroll
-    for (int j = 0; j < UPW; ++j)
-#pragma unroll
-      for (int t = 0; t < TT; ++t) wv[j][t] = load_chunk_nt(wp[t], 4 * (u0 + j) + lg, chunks);
-    // load j of a tile: rows 4j + lg, piece li of the unit; rows past m are left out four at a time
-#pragma unroll
-    for (int j = 0; j < UPW; ++j) {
-      const int64_t c = 4 * (u0 + j) + (li >> 2);
-      const int64_t at = (c < chunks ? c : chunks - 1) * 64 + (li & 3) * 16;
-#pragma unroll
-      for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t r = m0 + 16 * a + 4 * e;
-          if (r < m) xv[j][a][e] = *reinterpret_cast<const i32x4_t*>(q + (r + lg < m ? r + lg : m - 1) * kp + at);
-        }
+    for (int e = 0; e < 4; ++e) {
+      const int64_t r = m0 + 16 * a + 4 * e + lg < m ? 16 * a + 4 * e + lg : m - 1 - m0;
+      xo[a][e] = static_cast<uint32_t>(r * kp + li * 16);
     }
+  const char* wb[2] = {reinterpret_cast<const char*>(packed) + n0 * row_bytes,
+                       SWIGLU ? reinterpret_cast<const char*>(packed2) + n0 * row_bytes : nullptr};
+  const char* xb = reinterpret_cast<const char*>(q) + m0 * kp;
+  const int rows_in = static_cast<int>(m - m0 < 16 * MT ? m - m0 : 16 * MT);  // rows past m are left out four at a time
+  i32x4_t wv[TT], xv[MT][4];
+  auto load = [&](int64_t u) {
+    // the last unit may hold fewer than four chunks: the others read the row's last one, their codes are masked below
+    const int over = 4 * u + 4 > chunks ? static_cast<int>(4 * u + 4 - chunks) : 0;
+    uint32_t wback = 0, xback = 0;
+    if (over > 0) {
+      wback = lg > 3 - over ? 16 * (lg - 3 + over) : 0;
+      xback = (li >> 2) > 3 - over ? 64 * ((li >> 2) - 3 + over) : 0;
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      wv[t] = __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(wb[t / T] + u * 64 + (wo[t % T] - wback)));
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (16 * a + 4 * e < rows_in)
+          xv[a][e] = *reinterpret_cast<const i32x4_t*>(xb + u * 256 + (xo[a][e] - xback));
   };
   i32x4_t acc[MT][TT] = {};
-  int64_t u0 = wave * UPW;
-  if (u0 < units) load(u0);
-  while (u0 < units) {
-    i32x4_t w[UPW][TT];
+  // The scales are loaded ahead of everything else (loads return in order), one a thread, and stored to LDS with the
+  // zero sums while the first units' loads are on their way.
+  static_assert((MT + TT) * 16 <= kThreads, "one scale a thread");
+  float one_scale = 0.0f;
+  {
+    const int i = threadIdx.x, c = i - MT * 16;
+    const int64_t r = n0 + c % (16 * T);
+    if (i < MT * 16) one_scale = q_scale[m0 + i < m ? m0 + i : m - 1];
+    else if (c < TT * 16) one_scale = (c < 16 * T ? scale : scale2)[r < n ? r : n - 1];
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  int64_t u = wave;
+  if (u < units) load(u);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (SK > 1)
+    for (int i = threadIdx.x; i < MT * TT * kWave; i += kThreads) reinterpret_cast<i32x4_t*>(sums)[i] = i32x4_t{};
+  if (threadIdx.x < (MT + TT) * 16) scales[threadIdx.x] = one_scale;
+  __syncthreads();
+  while (u < units) {
+    i32x4_t w[TT];
 #pragma unroll
-    for (int j = 0; j < UPW; ++j) {
+    for (int t = 0; t < TT; ++t) w[t] = wv[t];
+    if (4 * u + 4 > chunks) {
 #pragma unroll
-      for (int t = 0; t < TT; ++t) w[j][t] = wv[j][t] & (4 * (u0 + j) + lg < chunks ? -1 : 0);
-#pragma unroll
-      for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) turn[wave][j][a][(4 * e + lg) * 16 + (li ^ (4 * e + lg))] = xv[j][a][e];
+      for (int t = 0; t < TT; ++t) w[t] &= 4 * u + lg < chunks ? -1 : 0;
     }
-    u0 += SK * UPW;
-    if (u0 < units) load(u0);
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) turn[wave][a][(4 * e + lg) * 16 + (li ^ (4 * e + lg))] = xv[a][e];
+    u += SK;
+    if (u < units) load(u);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int j = 0; j < UPW; ++j)
+    for (int s = 0; s < 4; ++s) {
+      i32x4_t x[MT];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        i32x4_t x[MT];
+      for (int a = 0; a < MT; ++a) x[a] = turn[wave][a][li * 16 + ((4 * lg + s) ^ li)];
 #pragma unroll
-        for (int a = 0; a < MT; ++a) x[a] = turn[wave][j][a][li * 16 + ((4 * lg + s) ^ li)];
+      for (int t = 0; t < TT; ++t) {
+        const i32x4_t b = word_bytes(static_cast<uint32_t>(w[t][s]));
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const i32x4_t b = word_bytes(static_cast<uint32_t>(w[j][t][s]));
-#pragma unroll
-          for (int a = 0; a < MT; ++a)
-            acc[a][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[a], b, acc[a][t], 0, 0, 0);
-        }
+        for (int a = 0; a < MT; ++a) acc[a][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[a], b, acc[a][t], 0, 0, 0);
       }
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 
-  // column li of a tile, activation row 4 lg + e
 #pragma unroll
   for (int a = 0; a < MT; ++a)
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        int* at = &sums[16 * a + 4 * lg + e][16 * t + li];
+        int* at = &sums[a * TT + t][e][lane];
         if constexpr (SK > 1) __hip_atomic_fetch_add(at, acc[a][t][e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         else *at = acc[a][t][e];
       }
   __syncthreads();
-  for (int o = threadIdx.x; o < MT * 16 * 16 * T; o += kThreads) {
-    const int row = o / (16 * T), col = o % (16 * T);
-    const int64_t i = m0 + row, r = n0 + col;
-    if (i >= m || r >= n) continue;
-    const float qs = q_scale[i];
-    const float v = static_cast<float>(sums[row][col] >> kCodeShift) * qs * scale[r];
-    if constexpr (SWIGLU) {
-      const float v2 = static_cast<float>(sums[row][16 * T + col] >> kCodeShift) * qs * scale2[r];
-      h[i * n + r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(silu(v) * v2));
-    } else {
-      y[i * n + r] = v;
+  // the tiles in turn to the waves: column li, activation rows 4 lg + e
+#pragma unroll
+  for (int i = 0; i < (MT * T + SK - 1) / SK; ++i) {
+    const int tile = wave + i * SK;
+    if (tile >= MT * T) break;
+    const int a = tile / T, t = tile % T;
+    const int64_t r = n0 + 16 * t + li;
+    const mfma_float4_t qs = *reinterpret_cast<const mfma_float4_t*>(row_scale + 16 * a + 4 * lg);
+    const float s1 = col_scale[16 * t + li], s2 = SWIGLU ? col_scale[16 * (T + t) + li] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t row = m0 + 16 * a + 4 * lg + e;
+      if (row >= m || r >= n) continue;
+      const float v = static_cast<float>(sums[a * TT + t][e][lane] >> kCodeShift) * qs[e] * s1;
+      if constexpr (SWIGLU) {
+        const float v2 = static_cast<float>(sums[a * TT + T + t][e][lane] >> kCodeShift) * qs[e] * s2;
+        h[row * n + r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(silu(v) * v2));
+      } else {
+        y[row * n + r] = v;
+      }
     }
   }
 }
 
-template <int MT, int T, int SK, int UPW, bool SWIGLU>
+template <int MT, int T, int SK, bool SWIGLU>
 void launch_stream(const uint32_t* p1, const float* s1, const uint32_t* p2, const float* s2, int64_t n, int64_t k,
                    const int8_t* q, const float* q_scale, int64_t m, float* y, uint16_t* h, hipStream_t stream) {
   const int64_t nb = (n + 16 * T - 1) / (16 * T), mb = (m + 16 * MT - 1) / (16 * MT);
-  hipLaunchKernelGGL((gemm_i8_stream_kernel<MT, T, SK, UPW, SWIGLU>), dim3(static_cast<unsigned>(nb * mb)),
+  hipLaunchKernelGGL((gemm_i8_stream_kernel<MT, T, SK, SWIGLU>), dim3(static_cast<unsigned>(nb * mb)),
                      dim3(SK * kWave), 0, stream, reinterpret_cast<const uint4*>(p1), s1,
                      reinterpret_cast<const uint4*>(p2), s2, n, words_per_row(k) / 4, q, q_scale, m, nb, y, h);
 }
@@ -194,15 +221,15 @@ __device__ __forceinline__ void tile_of_block(int m_blocks, int n_blocks, int& m
   nb = in / rows;
 }
 
-// Order of one word's work: each matrix instruction is followed by a share of
-// the next word's operand reads and decode, which run under it.
+// Order of one word's work: the next word's operand reads first, then its
+// decode in shares between the matrix instructions, which cover both.
 template <int TM, int TN>
 __device__ __forceinline__ void interleave() {
+  __builtin_amdgcn_sched_group_barrier(0x100, TM, 0);  // LDS reads
 #pragma unroll
   for (int i = 0; i < TM * TN; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                // one matrix instruction
-    if (i < TM) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // one LDS read
-    __builtin_amdgcn_sched_group_barrier(0x002, 12 / TM, 0);          // vector instructions
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one matrix instruction
+    __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);  // vector instructions
   }
   __builtin_amdgcn_sched_barrier(0);
 }
@@ -217,17 +244,20 @@ __device__ __forceinline__ void interleave() {
 // the barrier with only its last word's products left, whose operands are in
 // registers; they run while the first operands of the next step are read.
 // 16-byte piece c of row i sits at place c ^ (i / 2 % 8) of its 128 bytes, so
-// that 16 lanes of a store or an operand read touch each of the 64 banks once. The
+// that 16 lanes of a store or an operand read touch each of the 64 banks once.
+// Loads are issued D steps ahead (one for the largest tile, whose step is
+// longer than a load; four for small tiles, whose steps are short). The
 // packed words come straight to registers (lane (i, g) = (l % 32, l / 32) the
 // chunk 2u + g of column i) and are decoded once for all TM row tiles, which
 // is what pays for the decode: 8 vector instructions a word against TM matrix
 // instructions of 32 cycles.
-template <int WM, int WN, int TM, int TN, bool SWIGLU>
+template <int WM, int WN, int TM, int TN, int D, bool SWIGLU>
 __global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
     const uint4* __restrict__ packed, const float* __restrict__ scale, const uint4* __restrict__ packed2,
     const float* __restrict__ scale2, int64_t n, int64_t chunks, const int8_t* __restrict__ q,
     const float* __restrict__ q_scale, int64_t m, int m_blocks, int n_blocks, float* __restrict__ y,
     uint16_t* __restrict__ h) {
+  static_assert(D == 1 || D % 2 == 0, "the buffers of a step are known at compile time");
   static_assert(!SWIGLU || TN % 2 == 0, "a wave holds as many gate tiles as up tiles");
   constexpr int kThreads = WM * WN * kWave;
   constexpr int BM = 32 * TM * WM;
@@ -271,26 +301,26 @@ __global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
   }
   for (int i = threadIdx.x; i < BM; i += kThreads) row_scale[i] = q_scale[m0 + i < m ? m0 + i : m - 1];
   const int half = (threadIdx.x & 7) >> 2;  // chunk of the step that this thread's pieces belong to
-  i32x4_t xv[kLoads], wv[TN], w[TN], a[2][TM], b[2][TN];
+  i32x4_t xv[D][kLoads], wv[D][TN], w[TN], a[2][TM], b[2][TN];
   // Steps past the last one read it again, chunks past the row (the last step of an odd count) the row's last one:
   // activations as they are, codes 0 (masked when used, so that nothing waits for the load before its step).
-  auto load_x = [&](int64_t u) {
+  auto load_x = [&](int64_t u, int slot) {
     const int64_t v = u < steps ? u : steps - 1;
     const int64_t at = v * 128 - (2 * v + half < chunks ? 0 : 64);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) xv[i] = *reinterpret_cast<const i32x4_t*>(xp[i] + at);
+    for (int i = 0; i < kLoads; ++i) xv[slot][i] = *reinterpret_cast<const i32x4_t*>(xp[i] + at);
   };
-  auto load_w = [&](int64_t u) {
+  auto load_w = [&](int64_t u, int slot) {
 #pragma unroll
-    for (int t = 0; t < TN; ++t) wv[t] = load_chunk(wp[t], 2 * u + lg, chunks);
+    for (int t = 0; t < TN; ++t) wv[slot][t] = load_chunk(wp[t], 2 * u + lg, chunks);
   };
-  auto store_x = [&](int buffer) {
+  auto store_x = [&](int buffer, int slot) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) xs[buffer][xo[i]] = xv[i];
+    for (int i = 0; i < kLoads; ++i) xs[buffer][xo[i]] = xv[slot][i];
   };
-  auto take_w = [&](int64_t u) {
+  auto take_w = [&](int64_t u, int slot) {
 #pragma unroll
-    for (int t = 0; t < TN; ++t) w[t] = wv[t] & (2 * u + lg < chunks ? -1 : 0);
+    for (int t = 0; t < TN; ++t) w[t] = wv[slot][t] & (2 * u + lg < chunks ? -1 : 0);
   };
   const int row8 = (wm * TM * 32 + li) * 8;
   auto operands = [&](int buffer, int s) {
@@ -308,33 +338,41 @@ __global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
         acc[i][t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[s & 1][i], b[s & 1][t], acc[i][t], 0, 0, 0);
   };
 
-  load_x(0);
-  load_w(0);
-  store_x(0);
-  load_x(1);
-  take_w(0);
+  load_x(0, 0);
+  load_w(0, 0);
+  store_x(0, 0);
+  take_w(0, 0);
+#pragma unroll
+  for (int d = 1; d <= D; ++d) load_x(d, d % D);
+#pragma unroll
+  for (int d = 1; d < D; ++d) load_w(d, d);
   __syncthreads();
   operands(0, 0);
-  for (int64_t u = 0; u < steps; ++u) {
-    const int here = static_cast<int>(u & 1), next = here ^ 1;
-    store_x(next);
-    load_w(u + 1);
-    load_x(u + 2);
-    __builtin_amdgcn_sched_barrier(0);
-    operands(here, 1);
-    multiply(0);
-    interleave<TM, TN>();
-    operands(here, 2);
-    multiply(1);
-    interleave<TM, TN>();
-    operands(here, 3);
-    multiply(2);
-    interleave<TM, TN>();
-    __syncthreads();
-    take_w(u + 1);
-    operands(next, 0);
-    multiply(3);
-    interleave<TM, TN>();
+  // steps past the last one (to a whole number of D) multiply codes 0
+  for (int64_t u0 = 0; u0 < steps; u0 += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int64_t u = u0 + d;
+      const int here = D > 1 ? d & 1 : static_cast<int>(u & 1), next = here ^ 1;
+      store_x(next, (d + 1) % D);
+      load_w(u + D, d);
+      load_x(u + 1 + D, (d + 1) % D);
+      __builtin_amdgcn_sched_barrier(0);
+      operands(here, 1);
+      multiply(0);
+      interleave<TM, TN>();
+      operands(here, 2);
+      multiply(1);
+      interleave<TM, TN>();
+      operands(here, 3);
+      multiply(2);
+      interleave<TM, TN>();
+      __syncthreads();
+      take_w(u + 1, (d + 1) % D);
+      operands(next, 0);
+      multiply(3);
+      interleave<TM, TN>();
+    }
   }
 
   // lane: column li of a tile, rows 8 g + 4 lg + e; whole tiles store without a check
@@ -370,33 +408,117 @@ __global__ __launch_bounds__(WM* WN* kWave) void gemm_i8_tile_kernel(
     }
 }
 
-template <int WM, int WN, int TM, int TN, bool SWIGLU>
+template <int WM, int WN, int TM, int TN, int D, bool SWIGLU>
 void launch_tile(const uint32_t* p1, const float* s1, const uint32_t* p2, const float* s2, int64_t n, int64_t k,
                  const int8_t* q, const float* q_scale, int64_t m, float* y, uint16_t* h, hipStream_t stream) {
   constexpr int BM = 32 * TM * WM, BN = 32 * (SWIGLU ? TN / 2 : TN) * WN;
   const int64_t nb = (n + BN - 1) / BN, mb = (m + BM - 1) / BM;
-  hipLaunchKernelGGL((gemm_i8_tile_kernel<WM, WN, TM, TN, SWIGLU>), dim3(static_cast<unsigned>(nb * mb)),
+  hipLaunchKernelGGL((gemm_i8_tile_kernel<WM, WN, TM, TN, D, SWIGLU>), dim3(static_cast<unsigned>(nb * mb)),
                      dim3(WM * WN * kWave), 0, stream, reinterpret_cast<const uint4*>(p1), s1,
                      reinterpret_cast<const uint4*>(p2), s2, n, words_per_row(k) / 4, q, q_scale, m,
                      static_cast<int>(mb), static_cast<int>(nb), y, h);
 }
 
+// The tile that finishes first, counted in rounds of 256 workgroups (one a
+// CU) times the time of a round: 51, 32, 20, 14 and 11.5 us at k = 4,096 on
+// MI355X for 256 x 256, 128 x 256, 64 x 256, 64 x 128 and 32 x 128 (measured
+// with 192 to 256 workgroups of each). Each was the fastest of twenty shapes
+// where this picks it: n = 12,288 at m = 64 / 100 / 256 / 512 / 1,024 takes
+// 11.5 / 14.3 / 18.9 / 31.9 / 51.1 us, against 15.3 / 22.2 / 21.5 / 33.2 /
+// 54.2 us for the neighbouring choice. None below 192 workgroups: few rows
+// stream the weights instead (100 rows, n = 4,096: 8.2 against 11.9 us).
+enum Tile { kNone, k256x256, k128x256, k64x256, k64x128, k32x256, k32x128 };
+
+Tile pick_tile(int64_t m, int64_t columns, bool swiglu) {
+  struct Shape {
+    Tile tile;
+    int rows, columns;
+    double round;
+    bool plain, swiglu;
+  };
+  static const Shape shapes[] = {{k256x256, 256, 256, 51.0, true, true}, {k128x256, 128, 256, 32.0, true, true},
+                                 {k64x256, 64, 256, 20.0, true, true},   {k64x128, 64, 128, 14.0, true, false},
+                                 {k32x256, 32, 256, 16.0, false, true},  {k32x128, 32, 128, 11.5, true, false}};
+  Tile best = kNone;
+  double least = 0.0;
+  int64_t most = 0;
+  for (const Shape& s : shapes) {
+    if (!(swiglu ? s.swiglu : s.plain)) continue;
+    const int64_t groups = (m + s.rows - 1) / s.rows * ((columns + s.columns - 1) / s.columns);
+    const double t = static_cast<double>((groups + 255) / 256) * s.round;
+    if (groups > most) most = groups;
+    if (best == kNone || t < least) {
+      best = s.tile;
+      least = t;
+    }
+  }
+  return most < 192 || m <= 32 ? kNone : best;
+}
+
 }  // namespace
 
+// Streaming shapes by the workgroups they leave (us at m = 8, 32, 64 or 100
+// against the next best): n >= 8,192 three tiles of 8 waves (6.1; 6.5 for one
+// tile), n >= 5,120 two (5.0 against 5.2), fewer columns one tile of 16 waves
+// (4.2 against 4.4 of 8); 17 to 32 rows two row tiles at n >= 8,192 (8.5
+// against 9.5), else one (5.3 for two column tiles against 6.1); more rows
+// 2 x 4 tiles (8.2 against 8.8), at n <= 2,048 one row tile (4.9 against 5.3).
 hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
                                   const float* q_scale, int64_t m, float* y, hipStream_t stream) {
-  if (m > 128) launch_tile<2, 4, 4, 2, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream);
-  else launch_stream<1, 1, 8, 2, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream);
+#define PBG_TILE(...) launch_tile<__VA_ARGS__, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream)
+#define PBG_STREAM(...) \
+  launch_stream<__VA_ARGS__, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream)
+  switch (pick_tile(m, n, false)) {
+    case k256x256: PBG_TILE(2, 4, 4, 2, 1); break;
+    case k128x256: PBG_TILE(2, 4, 2, 2, 2); break;
+    case k64x256: PBG_TILE(1, 8, 2, 1, 2); break;
+    case k64x128: PBG_TILE(1, 4, 2, 1, 4); break;
+    case k32x128: PBG_TILE(1, 4, 1, 1, 4); break;
+    default:
+      if (m <= 16) {
+        if (n >= 8192) PBG_STREAM(1, 3, 8);
+        else if (n >= 5120) PBG_STREAM(1, 2, 8);
+        else PBG_STREAM(1, 1, 16);
+      } else if (m <= 32) {
+        if (n >= 8192) PBG_STREAM(2, 3, 8);
+        else if (n > 2048) PBG_STREAM(1, 2, 8);
+        else PBG_STREAM(1, 1, 16);
+      } else {
+        if (n > 2048) PBG_STREAM(2, 4, 8);
+        else if (m > 64) PBG_STREAM(1, 2, 8);
+        else PBG_STREAM(1, 1, 16);
+      }
+  }
+#undef PBG_TILE
+#undef PBG_STREAM
   return hipGetLastError();
 }
 
+// As above with twice the columns; the streaming shapes hold as many gate as
+// up tiles (m = 8, d_ff = 12,288: 9.2 us for three of each against 9.5; m = 32
+// 11.9 against 14.9; d_ff = 1,024 3.3 for one of each).
 hipError_t launch_swiglu_gate_up_i8(const uint32_t* gate, const float* gate_scale, const uint32_t* up,
                                     const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
                                     const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream) {
-  if (m > 128)
-    launch_tile<2, 4, 4, 2, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream);
-  else
-    launch_stream<1, 1, 8, 2, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream);
+#define PBG_TILE(...) launch_tile<__VA_ARGS__, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream)
+#define PBG_STREAM(...) \
+  launch_stream<__VA_ARGS__, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream)
+  switch (pick_tile(m, 2 * d_ff, true)) {
+    case k256x256: PBG_TILE(2, 4, 4, 2, 1); break;
+    case k128x256: PBG_TILE(2, 4, 2, 2, 2); break;
+    case k64x256: PBG_TILE(1, 4, 2, 2, 2); break;
+    case k32x256: PBG_TILE(1, 4, 1, 2, 4); break;
+    default:
+      if (m <= 16) {
+        if (d_ff >= 8192) PBG_STREAM(1, 3, 8);
+        else PBG_STREAM(1, 1, 8);
+      } else {
+        if (d_ff >= 8192) PBG_STREAM(2, 3, 8);
+        else PBG_STREAM(2, 2, 8);
+      }
+  }
+#undef PBG_TILE
+#undef PBG_STREAM
   return hipGetLastError();
 }
 
