@@ -525,37 +525,42 @@ def ternary3_ffn_swiglu(gate: torch.Tensor, gate_scale: torch.Tensor, up: torch.
 
 def q8_row_bytes(k: int) -> int:
     """Bytes of an 8-bit activation row of k codes (64 * ceil(k / 64))."""
-    return 0 if k <= 0 else 64 * ((int(k) + 63) // 64)
+    return 0 if k <= 0 else (int(k) + 63) // 64 * 64
 
 
-def _call(name: str, dev: torch.device, *args) -> None:
-    """Call a C entry point on dev's current stream, whatever the current device is."""
-    # The raw handles: the Stream objects of torch.cuda.current_stream cost as much as a small kernel.
-    index = dev.index
+# The calls below run for every token, with kernels of a few microseconds, so their checks use the cheapest queries:
+# the device index, the raw stream handle (a torch.cuda.Stream object costs as much as a small kernel) and identity
+# of types; what fails them is looked at again to say why.
+
+
+def _call(name: str, fn, index: int, *args) -> None:
+    """Call the C entry point fn on the current stream of device `index`, whatever the current device is."""
     if index == torch._C._cuda_getDevice():
-        rc = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
-            rc = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         _check(name, rc)
 
 
-def _on(dev: torch.device, t, name: str, dtype: torch.dtype, shape: tuple) -> int:
-    """Address of t after checking that it is a contiguous dtype tensor of that shape on dev."""
-    if isinstance(t, torch.Tensor) and t.device == dev and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+def _on(index: int, t, name: str, dtype: torch.dtype, shape: tuple) -> int:
+    """Address of t after checking that it is a contiguous dtype tensor of that shape on device `index`."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape \
+            and t.is_contiguous():
         return t.data_ptr()
     _dev(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    raise ValueError(f"{name} is on {t.device}, not on device {index}")
 
 
-def _matrix(t, name: str, dtype: torch.dtype) -> tuple[int, int]:
+def _matrix(t, name: str, dtype: torch.dtype):
+    """Shape (rows, columns) and device index of t after checking that it is a contiguous dtype matrix."""
     _dev(t, name, dtype)
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
-    return t.shape
+    return *t.shape, t.get_device()
 
 
 def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -564,12 +569,12 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     """Residual addition and root-mean-square norm of fp32 rows x [m, k]: (residual_out, h, q, q_scale).
 
     r = x + residual goes to residual_out, which may be x or residual for an update in place; without
-    a residual r is x, which is returned itself unless residual_out is given. h is the normed row in fp16 [m, k]; q int8 [m, q8_row_bytes(k)] and q_scale fp32
-    [m] are the same row in 8 bits. Outputs are the tensors given; `want` ("h", "q" or "hq") allocates
-    those of its letters that are not. With neither, h is allocated. Outputs not asked for are None.
+    a residual r is x, which is returned itself unless residual_out is given. h is the normed row in
+    fp16 [m, k]; q int8 [m, q8_row_bytes(k)] and q_scale fp32 [m] are the same row in 8 bits. Outputs
+    are the tensors given; `want` ("h", "q" or "hq") allocates those of its letters that are not. With
+    neither, h is allocated. Outputs not asked for are None.
     """
-    m, k = _matrix(x, "x", torch.float32)
-    dev = x.device
+    m, k, dev = _matrix(x, "x", torch.float32)
     if want is None:
         want = "h" if h is None and q is None and q_scale is None else ""
     elif want not in ("h", "q", "hq"):
@@ -583,7 +588,7 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
             q = torch.empty((m, q8_row_bytes(k)), dtype=torch.int8, device=dev)
         if q_scale is None:
             q_scale = torch.empty((m,), dtype=torch.float32, device=dev)
-    _call("add_rmsnorm", dev, x.data_ptr(),
+    _call("add_rmsnorm", lib().add_rmsnorm, dev, x.data_ptr(),
           None if residual is None else _on(dev, residual, "residual", torch.float32, (m, k)),
           _on(dev, weight, "weight", torch.float32, (k,)), eps, m, k,
           None if residual_out is None else _on(dev, residual_out, "residual_out", torch.float32, (m, k)),
@@ -595,14 +600,13 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
 
 def quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None, q_scale: torch.Tensor | None = None):
     """8-bit form of fp16 rows x [m, k]: (q int8 [m, q8_row_bytes(k)], q_scale fp32 [m]), x ~ q_scale * q."""
-    m, k = _matrix(x, "x", torch.float16)
-    dev = x.device
+    m, k, dev = _matrix(x, "x", torch.float16)
     if q is None:
         q = torch.empty((m, q8_row_bytes(k)), dtype=torch.int8, device=dev)
     if q_scale is None:
         q_scale = torch.empty((m,), dtype=torch.float32, device=dev)
-    _call("quantize_rows", dev, x.data_ptr(), m, k, _on(dev, q, "q", torch.int8, (m, q8_row_bytes(k))),
-          _on(dev, q_scale, "q_scale", torch.float32, (m,)))
+    _call("quantize_rows", lib().quantize_rows, dev, x.data_ptr(), m, k,
+          _on(dev, q, "q", torch.int8, (m, q8_row_bytes(k))), _on(dev, q_scale, "q_scale", torch.float32, (m,)))
     return q, q_scale
 
 
@@ -612,16 +616,15 @@ def ternary_gemm_i8(packed: torch.Tensor, scale: torch.Tensor, k: int, q: torch.
 
     q int8 [m, q8_row_bytes(k)] and q_scale fp32 [m] as add_rmsnorm and quantize_rows leave them; Y fp32 [m, n].
     """
-    n, words = _matrix(packed, "packed", torch.int32)
-    m, _ = _matrix(q, "q", torch.int8)
-    dev = packed.device
-    kp = q8_row_bytes(k)
+    n, words, dev = _matrix(packed, "packed", torch.int32)
+    m, kp = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() == 2 else 0, q8_row_bytes(k)
     if words != kp // 16:
         raise ValueError(f"packed must be [n, {kp // 16}] for k={k}")
     if y is None:
         y = torch.empty((m, n), dtype=torch.float32, device=dev)
-    _call("ternary_gemm_i8", dev, packed.data_ptr(), _on(dev, scale, "scale", torch.float32, (n,)), n, k,
-          _on(dev, q, "q", torch.int8, (m, kp)), _on(dev, q_scale, "q_scale", torch.float32, (m,)), m,
+    _call("ternary_gemm_i8", lib().ternary_gemm_i8, dev, packed.data_ptr(),
+          _on(dev, scale, "scale", torch.float32, (n,)), n, k, _on(dev, q, "q", torch.int8, (m, kp)),
+          _on(dev, q_scale, "q_scale", torch.float32, (m,)), m,
           _on(dev, y, "y", torch.float32, (m, n)))
     return y
 
@@ -630,15 +633,14 @@ def ternary_swiglu_gate_up_i8(gate: torch.Tensor, gate_scale: torch.Tensor, up: 
                               d_model: int, q: torch.Tensor, q_scale: torch.Tensor,
                               h: torch.Tensor | None = None) -> torch.Tensor:
     """h = fp16(silu(gate q) * up q) for 8-bit rows q [m, q8_row_bytes(d_model)]; h fp16 [m, d_ff]."""
-    d_ff, words = _matrix(gate, "gate", torch.int32)
-    m, _ = _matrix(q, "q", torch.int8)
-    dev = gate.device
-    kp = q8_row_bytes(d_model)
+    d_ff, words, dev = _matrix(gate, "gate", torch.int32)
+    m, kp = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() == 2 else 0, q8_row_bytes(d_model)
     if words != kp // 16:
         raise ValueError(f"gate and up must be [d_ff, {kp // 16}]")
     if h is None:
         h = torch.empty((m, d_ff), dtype=torch.float16, device=dev)
-    _call("ternary_swiglu_gate_up_i8", dev, gate.data_ptr(), _on(dev, gate_scale, "gate_scale", torch.float32, (d_ff,)),
+    _call("ternary_swiglu_gate_up_i8", lib().ternary_swiglu_gate_up_i8, dev, gate.data_ptr(),
+          _on(dev, gate_scale, "gate_scale", torch.float32, (d_ff,)),
           _on(dev, up, "up", torch.int32, (d_ff, words)), _on(dev, up_scale, "up_scale", torch.float32, (d_ff,)),
           d_model, d_ff, _on(dev, q, "q", torch.int8, (m, kp)), _on(dev, q_scale, "q_scale", torch.float32, (m,)), m,
           _on(dev, h, "h", torch.float16, (m, d_ff)))
@@ -659,20 +661,18 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, ids: torch.Tensor, a: torch.Tenso
     b fp16 [adapters, n, rank]; scale fp32 [adapters]; workspace from lora_workspace(m, rank) or any
     larger tensor (a new one is allocated if not given).
     """
-    m, n = _matrix(y, "y", torch.float32)
-    _, k = _matrix(x, "x", torch.float16)
-    dev = y.device
+    m, n, dev = _matrix(y, "y", torch.float32)
     _dev(a, "a", torch.float16)
     if a.dim() != 3:
         raise ValueError("a must be [adapters, rank, k]")
-    adapters, rank, _ = a.shape
+    adapters, rank, k = a.shape
     if out is None:
         out = torch.empty_like(y)
     if workspace is None:
         workspace = lora_workspace(m, rank, dev)
-    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    _call("lora_add", dev, y.data_ptr(), _on(dev, x, "x", torch.float16, (m, k)),
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
+    _call("lora_add", lib().lora_add, dev, y.data_ptr(), _on(dev, x, "x", torch.float16, (m, k)),
           _on(dev, ids, "ids", torch.int32, (m,)), _on(dev, a, "a", torch.float16, (adapters, rank, k)),
           _on(dev, b, "b", torch.float16, (adapters, n, rank)), _on(dev, scale, "scale", torch.float32, (adapters,)),
           m, n, k, adapters, rank, _on(dev, out, "out", torch.float32, (m, n)), workspace.data_ptr(),

@@ -219,8 +219,9 @@ __device__ __forceinline__ void join_row(const float* __restrict__ v, int64_t sl
 // The same for every row with an adapter, parts [m][2][16 RT] and factors [m]
 // to memory; 16 rows a workgroup.
 template <int RT>
-__global__ __launch_bounds__(256) void lora_join_kernel(const int32_t* __restrict__ ids, const float* __restrict__ scale,
-                                                        int64_t m, int adapters, int rank, int slices,
+__global__ __launch_bounds__(256) void lora_join_kernel(const int32_t* __restrict__ ids,
+                                                        const float* __restrict__ scale, int64_t m, int adapters,
+                                                        int rank, int slices,
                                                         const float* __restrict__ v, _Float16* __restrict__ parts,
                                                         float* __restrict__ factors) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
@@ -406,17 +407,21 @@ void launch(const Args& g) {
     launch_up<16, RT, 1, true, FAST>(g, slices, g.m);
     return;
   }
-  // A block of 64 rows has 4 groups or a few more where rows come in runs and up to 64 where they mix. Many
-  // blocks fill the chip by themselves, and a workgroup without a group costs its sort: 4 (first launch) and 2
-  // (second) of them share a block's groups against 16 and 4 at 1,531 rows: 65.9 against 72.5 us (rank 64, n 12,288).
+  // A block of 64 rows has 4 groups or a few more where rows come in runs and up to 64 where they mix; z workgroups
+  // share them. One block wants them spread (64 rows of 24 adapters, n = k = 4,096: 13.5 us with 32 against 15.4 with
+  // 16), a few blocks less so (256 rows of 16 adapters: 16.9 with 16, 19.6 with 32). Many blocks fill the chip by
+  // themselves, and a workgroup without a group costs its sort: 4 in the first launch and 2 in the second against 16
+  // and 4 at 1,531 rows, rank 64, n = 12,288: 65.9 against 72.5 us. (One launch less, with the first product unsliced
+  // on 16 waves and its parts finished in place, is slower: 15.9 us for the 64 rows, 80 against 37 at rank 64.)
   const bool many = g.m > 256;
-  launch_down<64, RT, FAST>(g, slices, ks, many ? 4 : 16);
+  const int z = g.m <= 64 ? 32 : 16;
+  launch_down<64, RT, FAST>(g, slices, ks, many ? 4 : z);
   _Float16* parts = reinterpret_cast<_Float16*>(static_cast<char*>(g.ws) + sums_bytes(g.m, g.rank));
   hipLaunchKernelGGL((lora_join_kernel<RT>), dim3(static_cast<unsigned>((g.m + 15) / 16)), dim3(256), 0, g.stream,
                      g.ids, g.scale, g.m, g.adapters, g.rank, slices, static_cast<const float*>(g.ws), parts,
                      reinterpret_cast<float*>(parts + g.m * 32 * RT));
   if (many) launch_up<64, RT, 4, false, FAST>(g, slices, 2);
-  else launch_up<64, RT, 2, false, FAST>(g, slices, 16);
+  else launch_up<64, RT, 2, false, FAST>(g, slices, z);
 }
 
 template <bool FAST>

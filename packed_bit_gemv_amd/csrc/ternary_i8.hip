@@ -43,13 +43,14 @@ __device__ __forceinline__ i32x4_t load_chunk(const uint4* __restrict__ row, int
 // Matrix product of few activation rows: a workgroup owns T tiles of 16
 // weight rows (of gate and of up each with SWIGLU) against MT tiles of 16
 // activation rows and streams the weights. Its SK waves share K in units of
-// 256 columns, the next unit's loads in flight under a unit's products: lane (i, g) = (l % 16, l / 16) holds the 16-byte chunk
-// 4u + g (64 codes) of weight row i, and step w of a unit multiplies word w of
-// the chunk with bytes 16w .. 16w + 15 of chunk 4u + g of the activations.
-// Those are loaded 256 consecutive bytes of a row on 16 lanes and turned
-// through LDS that only this wave uses, without a barrier (piece p of row i at
-// place p ^ i: every bank once in 16 lanes): read directly, 16 lanes would
-// touch 16 lines. The waves add their int32 sums in LDS (exact in any order).
+// 256 columns, the next unit's loads in flight under a unit's products: lane
+// (i, g) = (l % 16, l / 16) holds the 16-byte chunk 4u + g (64 codes) of
+// weight row i, and step w of a unit multiplies word w of the chunk with bytes
+// 16w .. 16w + 15 of chunk 4u + g of the activations. Those are loaded 256
+// consecutive bytes of a row on 16 lanes and turned through LDS that only this
+// wave uses, without a barrier (piece p of row i at place p ^ i: every bank
+// once in 16 lanes): read directly, 16 lanes would touch 16 lines. The waves
+// add their int32 sums in LDS (exact in any order).
 template <int MT, int T, int SK, bool SWIGLU>
 __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
     const uint4* __restrict__ packed, const float* __restrict__ scale, const uint4* __restrict__ packed2,
@@ -465,7 +466,8 @@ Tile pick_tile(int64_t m, int64_t columns, bool swiglu) {
 // 2 x 4 tiles (8.2 against 8.8), at n <= 2,048 one row tile (4.9 against 5.3).
 hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
                                   const float* q_scale, int64_t m, float* y, hipStream_t stream) {
-#define PBG_TILE(...) launch_tile<__VA_ARGS__, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream)
+#define PBG_TILE(...) \
+  launch_tile<__VA_ARGS__, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream)
 #define PBG_STREAM(...) \
   launch_stream<__VA_ARGS__, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream)
   switch (pick_tile(m, n, false)) {
@@ -500,7 +502,8 @@ hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, in
 hipError_t launch_swiglu_gate_up_i8(const uint32_t* gate, const float* gate_scale, const uint32_t* up,
                                     const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
                                     const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream) {
-#define PBG_TILE(...) launch_tile<__VA_ARGS__, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream)
+#define PBG_TILE(...) \
+  launch_tile<__VA_ARGS__, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream)
 #define PBG_STREAM(...) \
   launch_stream<__VA_ARGS__, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream)
   switch (pick_tile(m, 2 * d_ff, true)) {

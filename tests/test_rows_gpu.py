@@ -177,7 +177,9 @@ def pad(q):
 
 GEMM_SHAPES = [(1, 1, 1), (1, 17, 64), (2, 5, 65), (16, 16, 256), (17, 33, 320), (1, 6144, 4096), (7, 4096, 12288), (8, 1024, 4096),
                (33, 100, 4100), (64, 48, 1000), (100, 1024, 4096), (129, 130, 192), (257, 300, 640), (300, 1000, 1096),
-               (512, 512, 512), (1000, 257, 64), (2, 70000, 64), (70000, 3, 130), (130, 640, 12288), (513, 2050, 4096)]
+               (512, 512, 512), (1000, 257, 64), (2, 70000, 64), (70000, 3, 130), (130, 640, 12288), (513, 2050, 4096),
+               (20, 9000, 700), (50, 900, 1100),  # and each tile, with rows, columns and K that end inside it
+               (63, 12288, 580), (250, 12290, 328), (510, 12288, 700), (1000, 12290, 328)]
 
 
 @pytest.mark.parametrize("m,n,k", GEMM_SHAPES)
@@ -230,7 +232,8 @@ def test_gemm_i8_reads_every_code(pbg):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 12288, 4096), (8, 333, 4096), (16, 40, 72), (65, 100, 200), (130, 257, 1000),
-                                   (300, 520, 4096), (40, 2048, 4096), (600, 130, 640)])
+                                   (300, 520, 4096), (40, 2048, 4096), (600, 130, 640), (30, 9000, 200), (63, 12300, 580),
+                                   (100, 12290, 328), (256, 12300, 700), (510, 12290, 328)])
 def test_swiglu_gate_up_i8(pbg, m, n, k):
     say(f"swiglu_gate_up_i8 m={m} n={n} k={k}")
     rng = np.random.default_rng(m + n + k)
@@ -410,6 +413,54 @@ def test_block_in_a_graph_and_on_a_stream(pbg):
         torch.cuda.synchronize()
         for a, b, c in zip(outs, eager, other):
             assert torch.equal(a, b) and torch.equal(c, b)
+
+
+def test_two_streams_at_once(pbg):
+    """Two chains on two streams, separate workspaces: each keeps its results."""
+    d, f = 256, 712
+    _, w = block_weights(pbg, d, f)
+    jobs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for m in (6, 90):
+        x, res, _ = norm_case(m, m, d)
+        a = dev(x), dev(res), dev((np.arange(m) % 4 - 1).astype(np.int32))
+        jobs.append((a, block(pbg, w, *a)))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        for (a, _), st in zip(jobs, streams):
+            with torch.cuda.stream(st):
+                outs.append(block(pbg, w, *a))
+    torch.cuda.synchronize()
+    for i, got in enumerate(outs):
+        for a, b in zip(got, jobs[i % 2][1]):
+            assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(pbg):
+    """2^20 rows of 2,100 columns: element offsets past 2^31 in every operator, checked at rows across the range."""
+    m, k, n = 1 << 20, 64, 2100
+    some = np.array([0, 1, 511, 12345, m // 2 - 1, m // 2, m - 1000, m - 2, m - 1])
+    at = torch.from_numpy(some).to("cuda:0")
+    g = torch.Generator(device="cuda:0").manual_seed(1)
+    q = torch.randint(-127, 128, (m, k), generator=g, device="cuda:0", dtype=torch.int8)
+    qs = torch.rand(m, generator=g, device="cuda:0") + 0.5
+    codes, s = synth.ternary_codes(5, n, k), synth.row_scales(6, n)
+    y = pbg.ternary_gemm_i8(pbg.pack_ternary(dev(codes))[0], dev(s), k, q, qs)
+    ref = oracle.ternary_gemm_i8(oracle.pack(codes)[0], s, k, host(q[at]), host(qs[at]))
+    assert_within(host(y[at]), ref, np.abs(ref) * 2.01 * U, "y")
+    w = np.ones(n, np.float32)
+    r, h, hq, hs = pbg.add_rmsnorm(y, dev(w), 1e-6, want="hq")
+    check_norm((None, h[at], hq[at], hs[at]), oracle.add_rmsnorm(host(y[at]), w, 1e-6), n)
+    x2, xs2 = pbg.quantize_rows(h)
+    rq, rs = oracle.quantize_rows(host(h[at]))
+    assert np.array_equal(host(x2[at])[:, :n], rq) and np.array_equal(host(xs2[at]), rs.astype(np.float32))
+    del hq, x2
+    c = lora_case(3, len(some), n, n, 2, 8)
+    ids = torch.full((m,), -1, dtype=torch.int32, device="cuda:0")
+    ids[at] = dev(c["ids"] % 2)
+    c.update(y=host(y[at]), x=host(h[at]), ids=host(ids[at]))
+    out = pbg.lora_add(y, h, ids, dev(c["a"]), dev(c["b"]), dev(c["scale"]), out=y)
+    assert_within(host(out[at]), oracle.lora_add(**c), lora_bound(c), "lora")
 
 
 def test_refusals(pbg):
