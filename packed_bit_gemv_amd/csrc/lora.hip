@@ -346,7 +346,8 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, 
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       if (in[i] && r0 + 4 <= n) {
-        *reinterpret_cast<f32x4_any_t*>(out + row[i] + r0) = base[i];
+        // not kept in the caches, where B_a is: 61.7 against 66.3 us for the prompt below
+        __builtin_nontemporal_store(f32x4_any_t(base[i]), reinterpret_cast<f32x4_any_t*>(out + row[i] + r0));
       } else if (in[i]) {
 #pragma unroll
         for (int e = 0; e < 3; ++e)
@@ -407,21 +408,26 @@ void launch(const Args& g) {
     launch_up<16, RT, 1, true, FAST>(g, slices, g.m);
     return;
   }
-  // A block of 64 rows has 4 groups or a few more where rows come in runs and up to 64 where they mix; z workgroups
-  // share them. One block wants them spread (64 rows of 24 adapters, n = k = 4,096: 13.5 us with 32 against 15.4 with
-  // 16), a few blocks less so (256 rows of 16 adapters: 16.9 with 16, 19.6 with 32). Many blocks fill the chip by
-  // themselves, and a workgroup without a group costs its sort: 4 in the first launch and 2 in the second against 16
-  // and 4 at 1,531 rows, rank 64, n = 12,288: 65.9 against 72.5 us. (One launch less, with the first product unsliced
-  // on 16 waves and its parts finished in place, is slower: 15.9 us for the 64 rows, 80 against 37 at rank 64.)
-  const bool many = g.m > 256;
-  const int z = g.m <= 64 ? 32 : 16;
-  launch_down<64, RT, FAST>(g, slices, ks, many ? 4 : z);
+  // A block of 64 rows has 4 groups or a few more where rows come in runs, and up to one for each adapter (and 4 more)
+  // where they mix; z workgroups share them. A workgroup without a group costs its sort, one with many takes them one
+  // after another, so z fills the chip and no more: 1,531 rows of 3 adapters in runs (rank 64, n = 12,288) take 66 us
+  // with 4 and 2 in the two launches against 72 with 16 and 4; 64 mixed rows of 24 adapters 13.5 with 28 against 15.4
+  // with 16. (One launch less, with the first product unsliced on 16 waves and its parts finished in place, is slower:
+  // 15.9 us for the 64 rows, 80 against 37 at rank 64 and n = 12,288.)
+  const int64_t blocks = (g.m + 63) / 64;
+  const int64_t most = g.adapters < 59 ? g.adapters + 5 : 64;
+  auto share = [&](int64_t workgroups, int64_t fill) {
+    const int64_t z = fill / workgroups < 2 ? 2 : fill / workgroups;
+    return z < most ? z : most;
+  };
+  launch_down<64, RT, FAST>(g, slices, ks, share(blocks * slices, 768));
   _Float16* parts = reinterpret_cast<_Float16*>(static_cast<char*>(g.ws) + sums_bytes(g.m, g.rank));
   hipLaunchKernelGGL((lora_join_kernel<RT>), dim3(static_cast<unsigned>((g.m + 15) / 16)), dim3(256), 0, g.stream,
                      g.ids, g.scale, g.m, g.adapters, g.rank, slices, static_cast<const float*>(g.ws), parts,
                      reinterpret_cast<float*>(parts + g.m * 32 * RT));
-  if (many) launch_up<64, RT, 4, false, FAST>(g, slices, 2);
-  else launch_up<64, RT, 2, false, FAST>(g, slices, z);
+  const int64_t wide = blocks * ((g.n + 64 * kWaves - 1) / (64 * kWaves));
+  if (wide >= 256) launch_up<64, RT, 4, false, FAST>(g, slices, share(wide, 2048));
+  else launch_up<64, RT, 2, false, FAST>(g, slices, share(2 * wide, 2048));
 }
 
 template <bool FAST>
