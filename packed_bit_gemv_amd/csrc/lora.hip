@@ -410,14 +410,15 @@ void launch(const Args& g) {
   }
   // A block of 64 rows has 4 groups or a few more where rows come in runs, and up to one for each adapter (and 4 more)
   // where they mix; z workgroups share them. A workgroup without a group costs its sort, one with many takes them one
-  // after another, so z fills the chip and no more: 1,531 rows of 3 adapters in runs (rank 64, n = 12,288) take 66 us
-  // with 4 and 2 in the two launches against 72 with 16 and 4; 64 mixed rows of 24 adapters 13.5 with 28 against 15.4
-  // with 16. (One launch less, with the first product unsliced on 16 waves and its parts finished in place, is slower:
-  // 15.9 us for the 64 rows, 80 against 37 at rank 64 and n = 12,288.)
+  // after another, so z fills the chip and no more, and is at least 3: 1,531 rows of 3 adapters in runs (rank 64, n =
+  // 12,288) take 66 us with 4 and 2 in the two launches against 72 with 16 and 4, and 60.8 against 61.2 us with 3 and
+  // 2 in the second; 64 mixed rows of 24 adapters 13.5 with 28 against 15.4 with 16. (One launch less, with the first
+  // product unsliced on 16 waves and its parts finished in place, is slower: 15.9 us for the 64 rows, 80 against 37 at
+  // rank 64 and n = 12,288.)
   const int64_t blocks = (g.m + 63) / 64;
   const int64_t most = g.adapters < 59 ? g.adapters + 5 : 64;
   auto share = [&](int64_t workgroups, int64_t fill) {
-    const int64_t z = fill / workgroups < 2 ? 2 : fill / workgroups;
+    const int64_t z = fill / workgroups < 3 ? 3 : fill / workgroups;
     return z < most ? z : most;
   };
   launch_down<64, RT, FAST>(g, slices, ks, share(blocks * slices, 768));
