@@ -117,7 +117,8 @@ __device__ __forceinline__ float row_max16(float v) {
 // First product: v[slice][row][rank] for the row block blockIdx.x, the slice
 // of K blockIdx.y and the groups blockIdx.z, + gridDim.z, ... The waves take
 // 32-column steps in turn, U steps of loads in flight. A group alone is bound
-// by the latency of its loads, so K is sliced until the launch fills the chip.
+// by the latency of its loads, so K is sliced until the launch fills the chip:
+// 1,531 rows at rank 64, k = 4,096 take 13 us with 8 slices, 24 unsliced.
 template <int R, int RT, bool FAST>
 __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t* __restrict__ x,
                                                                   const int32_t* __restrict__ ids,
@@ -241,7 +242,9 @@ typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
 // on one load of B_a; up to 16 one instruction takes both, [hi | lo] against
 // [B_a | B_a]. Bound by y and out, which a wave reads and writes in pieces of
 // 64 C bytes a row: the product goes through LDS to that order. JOIN: the
-// workgroup adds the slices of its groups' v itself.
+// workgroup adds the slices of its groups' v itself. 1,531 rows at rank 64, n
+// = 12,288: 45 us, 3.4 TB/s of y and out (pieces of 64 bytes, straight from
+// the product's layout: 73 us).
 template <int R, int RT, int C, bool JOIN, bool FAST>
 __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, const int32_t* __restrict__ ids,
                                                                 const uint16_t* __restrict__ b,

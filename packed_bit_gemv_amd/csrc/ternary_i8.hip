@@ -50,7 +50,9 @@ __device__ __forceinline__ i32x4_t load_chunk(const uint4* __restrict__ row, int
 // consecutive bytes of a row on 16 lanes and turned through LDS that only this
 // wave uses, without a barrier (piece p of row i at place p ^ i: every bank
 // once in 16 lanes): read directly, 16 lanes would touch 16 lines. The waves
-// add their int32 sums in LDS (exact in any order).
+// add their int32 sums in LDS (exact in any order). Bound by the weight stream
+// and the launch: 8 rows by 12,288 x 4,096 take 6.1 us, 7 rows by 4,096 x
+// 12,288 6.3-6.5, gate and up for 8 rows 8.6 (25.5 MB, 3.0 TB/s).
 template <int MT, int T, int SK, bool SWIGLU>
 __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
     const uint4* __restrict__ packed, const float* __restrict__ scale, const uint4* __restrict__ packed2,
@@ -246,6 +248,9 @@ __device__ __forceinline__ void interleave() {
 // registers; they run while the first operands of the next step are read.
 // 16-byte piece c of row i sits at place c ^ (i / 2 % 8) of its 128 bytes, so
 // that 16 lanes of a store or an operand read touch each of the 64 banks once.
+// Bound by the matrix cores at the clock that the power allows: 4,096 x 4,096
+// x 12,288 takes 156-165 us, 2.5-2.65e15 operations/s (3.13e15 on zeros, the
+// matrix cores then busy 62 % of the cycles).
 // Loads are issued D steps ahead (one for the largest tile, whose step is
 // longer than a load; four for small tiles, whose steps are short). The
 // packed words come straight to registers (lane (i, g) = (l % 32, l / 32) the
