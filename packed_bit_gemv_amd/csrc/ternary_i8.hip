@@ -224,6 +224,121 @@ __device__ __forceinline__ void tile_of_block(int m_blocks, int n_blocks, int& m
   nb = in / rows;
 }
 
+// Up to M activation rows, K of at most 64 CPL chunks: a wave owns R weight
+// rows (of gate and of up each with SWIGLU), lane l the chunks l, l + 64, ...
+// of every row, so that each load of a wave is 1 KiB of one row. The
+// activations are loaded first, before a barrier that nothing waits for
+// behind it, so that they return first; they go through LDS (piece p of chunk
+// 64 j + l at (4 j + p) 64 + l) and meet the decoded bytes in dot products of
+// four: 8 + 4 M vector instructions a word. The lanes' sums are multiples of
+// 64 below 2^30, so the transposed fp32 reduction adds them exactly. Bound by
+// the launch and the first bytes, as ternary_gemv is: gate at one row 4.3 us,
+// down 4.4, gate and up 6.4 (5.5, 5.5 and 8.2 for the streaming kernel, whose
+// loads are 64 bytes of 16 rows).
+template <int M, int CPL, int G, int R, bool SWIGLU>
+__global__ __launch_bounds__(G* kWave) void gemv_i8_kernel(const uint4* __restrict__ packed,
+                                                           const float* __restrict__ scale,
+                                                           const uint4* __restrict__ packed2,
+                                                           const float* __restrict__ scale2, int64_t n, int64_t chunks,
+                                                           const int8_t* q, const float* __restrict__ q_scale, int m,
+                                                           float* __restrict__ y, uint16_t* __restrict__ h) {
+  constexpr int RR = SWIGLU ? 2 * R : R;  // row i of the wave: weight row i / 2 of gate (even) or up (odd) with SWIGLU
+  constexpr int kSums = M * RR;           // sum of activation row a and weight row i at a RR + i
+  constexpr int kRed = (kSums + 3) / 4;
+  static_assert(!SWIGLU || kSums % 2 == 0, "a gate sum and its up sum in one reduction");
+  constexpr int kThreads = G * kWave;
+  constexpr int kPieces = CPL * kWave * 4;
+  constexpr int kXPer = (M * kPieces + kThreads - 1) / kThreads;
+  __shared__ i32x4_t xs[M][kPieces];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * G + wave) * R;
+  const int pieces = static_cast<int>(chunks) * 4;
+  const i32x4_t* xg = reinterpret_cast<const i32x4_t*>(q);
+
+  i32x4_t xv[kXPer];
+#pragma unroll
+  for (int i = 0; i < kXPer; ++i) {
+    const int at = threadIdx.x + i * kThreads, a = at / kPieces, p = at % kPieces;
+    xv[i] = xg[a < m && p < pieces ? a * pieces + p : 0];
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");  // order, not wait: the loads stay in flight across it
+  __builtin_amdgcn_sched_barrier(0);
+
+  i32x4_t w[RR][CPL];
+#pragma unroll
+  for (int j = 0; j < CPL; ++j) {
+    const int64_t c = lane + kWave * j;
+    const int64_t cc = c < chunks ? c : chunks - 1;
+#pragma unroll
+    for (int i = 0; i < RR; ++i) {
+      const int64_t r = row0 + (SWIGLU ? i / 2 : i);
+      const uint4* base = SWIGLU && (i & 1) ? packed2 : packed;
+      w[i][j] = __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(base + (r < n ? r : n - 1) * chunks + cc));
+    }
+  }
+  // the sums that this lane gets: slot i of each reduction
+  const int slot = reduce4_slot(lane);
+  float sc[kRed];
+#pragma unroll
+  for (int e = 0; e < kRed; ++e) {
+    const int idx = 4 * e + (slot < 0 ? 0 : slot), a = idx / RR, i = idx % RR;
+    const int64_t r = row0 + (SWIGLU ? i / 2 : i);
+    sc[e] = (SWIGLU && (i & 1) ? scale2 : scale)[r < n ? r : n - 1] * q_scale[a < m ? a : m - 1];
+  }
+  __builtin_amdgcn_sched_barrier(0);
+
+  // chunks past the row hold 0 activations
+#pragma unroll
+  for (int i = 0; i < kXPer; ++i) {
+    const int at = threadIdx.x + i * kThreads, a = at / kPieces, p = at % kPieces, c = p >> 2;
+    if (a < M) xs[a][((c >> 6) * 4 + (p & 3)) * kWave + (c & (kWave - 1))] = xv[i] & (p < pieces ? -1 : 0);
+  }
+  __syncthreads();
+  int acc[4 * kRed] = {};
+#pragma unroll
+  for (int j = 0; j < CPL; ++j)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      i32x4_t x[M];
+#pragma unroll
+      for (int a = 0; a < M; ++a) x[a] = xs[a][(4 * j + s) * kWave + lane];
+#pragma unroll
+      for (int i = 0; i < RR; ++i) {
+        const i32x4_t b = word_bytes(static_cast<uint32_t>(w[i][j][s]));
+#pragma unroll
+        for (int a = 0; a < M; ++a)
+#pragma unroll
+          for (int d = 0; d < 4; ++d) acc[a * RR + i] = __builtin_amdgcn_sdot4(b[d], x[a][d], acc[a * RR + i], false);
+      }
+    }
+#pragma unroll
+  for (int e = 0; e < kRed; ++e) {
+    const float red = wave_reduce4(static_cast<float>(acc[4 * e]), static_cast<float>(acc[4 * e + 1]),
+                                   static_cast<float>(acc[4 * e + 2]), static_cast<float>(acc[4 * e + 3]));
+    const float v = red * (1.0f / (1 << kCodeShift)) * sc[e];
+    const int idx = 4 * e + slot, a = idx / RR, i = idx % RR;
+    const int64_t r = row0 + (SWIGLU ? i / 2 : i);
+    const bool in = slot >= 0 && idx < kSums && a < m && r < n;
+    if constexpr (SWIGLU) {
+      const float u = __shfl_xor(v, 32);  // slots 0 and 1, 2 and 3 are 32 lanes apart
+      if (in && (slot & 1) == 0) h[a * n + r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(silu(v) * u));
+    } else {
+      if (in) y[a * n + r] = v;
+    }
+  }
+}
+
+template <int M, int CPL, int G, int R, bool SWIGLU>
+void launch_gemv(const uint32_t* p1, const float* s1, const uint32_t* p2, const float* s2, int64_t n, int64_t k,
+                 const int8_t* q, const float* q_scale, int64_t m, float* y, uint16_t* h, hipStream_t stream) {
+  hipLaunchKernelGGL((gemv_i8_kernel<M, CPL, G, R, SWIGLU>), dim3(static_cast<unsigned>((n + G * R - 1) / (G * R))),
+                     dim3(G * kWave), 0, stream, reinterpret_cast<const uint4*>(p1), s1,
+                     reinterpret_cast<const uint4*>(p2), s2, n, words_per_row(k) / 4, q, q_scale, static_cast<int>(m),
+                     y, h);
+}
+
 // Order of one word's work: the next word's operand reads first, then its
 // decode in shares between the matrix instructions, which cover both.
 template <int TM, int TN>
@@ -461,6 +576,66 @@ Tile pick_tile(int64_t m, int64_t columns, bool swiglu) {
   return most < 192 || m <= 32 ? kNone : best;
 }
 
+// The kernels of one to eight rows whose loads are whole pieces of one row (us
+// against the best streaming shape, k = 4,096 unless stated): one row n =
+// 1,024 / 4,096 / 6,144 / 12,288 2.3 / 2.9 / 3.3 / 4.3 against 3.2 / 3.9 / 4.6
+// / 5.5, k = 12,288 4.4 against 5.5; two rows 2.5 / 3.2 / 3.7 / 4.7 against
+// 3.7 / 4.0 / 4.7 / 5.7; three and four rows below n = 8,192 2.7 / 3.5 / 4.1
+// against 3.9 / 4.1 / 4.9 (12,288: 6.1 against 5.8); up to eight rows at n <=
+// 2,048 3.2 against 4.1 (4,096: 4.8 against 4.3). Two weight rows a wave from
+// n = 8,192 on (4.28 against 4.8 us for one), below it one (3.27 against 3.38
+// at 6,144), for K of several chunks a lane two from n = 4,096 on.
+bool launch_gemv_rows(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
+                      const float* q_scale, int64_t m, float* y, hipStream_t stream) {
+#define PBG_GEMV(...) \
+  (launch_gemv<__VA_ARGS__, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream), true)
+  const int64_t cpl = (words_per_row(k) / 4 + kWave - 1) / kWave;  // chunks a lane
+  if (m == 1) {
+    switch (cpl) {
+      case 1: return n >= 8192 ? PBG_GEMV(1, 1, 4, 2) : PBG_GEMV(1, 1, 4, 1);
+      case 2: return n >= 4096 ? PBG_GEMV(1, 2, 4, 2) : PBG_GEMV(1, 2, 4, 1);
+      case 3: return n >= 4096 ? PBG_GEMV(1, 3, 4, 2) : PBG_GEMV(1, 3, 4, 1);
+      case 4: return n >= 4096 ? PBG_GEMV(1, 4, 4, 2) : PBG_GEMV(1, 4, 4, 1);
+      default: return false;
+    }
+  }
+  if (m == 2) {
+    switch (cpl) {
+      case 1: return n >= 4096 ? PBG_GEMV(2, 1, 4, 2) : PBG_GEMV(2, 1, 4, 1);
+      case 2: return PBG_GEMV(2, 2, 4, 2);
+      case 3: return PBG_GEMV(2, 3, 4, 2);
+      default: return false;
+    }
+  }
+  if (m <= 4 && cpl == 1 && n < 8192) return PBG_GEMV(4, 1, 8, 1);
+  if (m <= 8 && cpl == 1 && n <= 2048) return PBG_GEMV(8, 1, 4, 1);
+#undef PBG_GEMV
+  return false;
+}
+
+// The same for gate and up: one row 6.4 us against 8.2 (d_ff = 12,288, k =
+// 4,096; two pairs for two waves, 6.9 for four), two rows 7.3 against 8.4.
+bool launch_gemv_gate_up(const uint32_t* gate, const float* gate_scale, const uint32_t* up, const float* up_scale,
+                         int64_t d_model, int64_t d_ff, const int8_t* q, const float* q_scale, int64_t m, uint16_t* h,
+                         hipStream_t stream) {
+#define PBG_GEMV(...)                                                                                                 \
+  (launch_gemv<__VA_ARGS__, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream), \
+   true)
+  const int64_t cpl = (words_per_row(d_model) / 4 + kWave - 1) / kWave;
+  if (m == 1) {
+    switch (cpl) {
+      case 1: return PBG_GEMV(1, 1, 2, 2);
+      case 2: return PBG_GEMV(1, 2, 4, 1);
+      case 3: return PBG_GEMV(1, 3, 4, 1);
+      case 4: return PBG_GEMV(1, 4, 4, 1);
+      default: return false;
+    }
+  }
+  if (m == 2 && cpl == 1) return PBG_GEMV(2, 1, 4, 1);
+#undef PBG_GEMV
+  return false;
+}
+
 }  // namespace
 
 // Streaming shapes by the workgroups they leave (us at m = 8, 32, 64 or 100
@@ -471,6 +646,7 @@ Tile pick_tile(int64_t m, int64_t columns, bool swiglu) {
 // 2 x 4 tiles (8.2 against 8.8), at n <= 2,048 one row tile (4.9 against 5.3).
 hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
                                   const float* q_scale, int64_t m, float* y, hipStream_t stream) {
+  if (launch_gemv_rows(packed, scale, n, k, q, q_scale, m, y, stream)) return hipGetLastError();
 #define PBG_TILE(...) \
   launch_tile<__VA_ARGS__, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream)
 #define PBG_STREAM(...) \
@@ -507,6 +683,8 @@ hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, in
 hipError_t launch_swiglu_gate_up_i8(const uint32_t* gate, const float* gate_scale, const uint32_t* up,
                                     const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
                                     const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream) {
+  if (launch_gemv_gate_up(gate, gate_scale, up, up_scale, d_model, d_ff, q, q_scale, m, h, stream))
+    return hipGetLastError();
 #define PBG_TILE(...) \
   launch_tile<__VA_ARGS__, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream)
 #define PBG_STREAM(...) \

@@ -178,6 +178,9 @@ def pad(q):
 GEMM_SHAPES = [(1, 1, 1), (1, 17, 64), (2, 5, 65), (16, 16, 256), (17, 33, 320), (1, 6144, 4096), (7, 4096, 12288), (8, 1024, 4096),
                (33, 100, 4100), (64, 48, 1000), (100, 1024, 4096), (129, 130, 192), (257, 300, 640), (300, 1000, 1096),
                (512, 512, 512), (1000, 257, 64), (2, 70000, 64), (70000, 3, 130), (130, 640, 12288), (513, 2050, 4096),
+               (1, 9001, 200), (1, 50, 5000), (1, 5003, 5000), (1, 41, 9000), (1, 4201, 9000), (1, 30, 16384),
+               (1, 4101, 16300), (1, 10, 20000), (2, 4097, 300), (2, 33, 8000), (2, 35, 12288), (2, 9, 14000),
+               (3, 33, 4000), (4, 5001, 1000), (3, 8200, 100), (5, 300, 4096), (8, 2048, 70), (6, 100, 5000),
                (20, 9000, 700), (50, 900, 1100),  # and each tile, with rows, columns and K that end inside it
                (63, 12288, 580), (250, 12290, 328), (510, 12288, 700), (1000, 12290, 328)]
 
@@ -233,6 +236,8 @@ def test_gemm_i8_reads_every_code(pbg):
 
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 12288, 4096), (8, 333, 4096), (16, 40, 72), (65, 100, 200), (130, 257, 1000),
                                    (300, 520, 4096), (40, 2048, 4096), (600, 130, 640), (30, 9000, 200), (63, 12300, 580),
+                                   (1, 99, 5000), (1, 101, 9000), (1, 33, 16300), (1, 9, 20000), (2, 101, 500),
+                                   (2, 50, 5000), (3, 40, 300),
                                    (100, 12290, 328), (256, 12300, 700), (510, 12290, 328)])
 def test_swiglu_gate_up_i8(pbg, m, n, k):
     say(f"swiglu_gate_up_i8 m={m} n={n} k={k}")
