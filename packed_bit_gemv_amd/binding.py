@@ -546,9 +546,11 @@ def _call(name: str, fn, index: int, *args) -> None:
 
 def _on(index: int, t, name: str, dtype: torch.dtype, shape: tuple) -> int:
     """Address of t after checking that it is a contiguous dtype tensor of that shape on device `index`."""
-    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape \
-            and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _dev(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -556,11 +558,15 @@ def _on(index: int, t, name: str, dtype: torch.dtype, shape: tuple) -> int:
 
 
 def _matrix(t, name: str, dtype: torch.dtype):
-    """Shape (rows, columns) and device index of t after checking that it is a contiguous dtype matrix."""
+    """Rows, columns and device index of t after checking that it is a contiguous dtype matrix on a GPU."""
+    try:
+        rows, columns = t.shape
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+            return rows, columns, t.get_device()
+    except (AttributeError, TypeError, ValueError):
+        pass
     _dev(t, name, dtype)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
-    return *t.shape, t.get_device()
+    raise ValueError(f"{name} must have two dimensions")
 
 
 def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
