@@ -86,8 +86,11 @@ struct Groups {
   }
 };
 
-// Eight fp16 elements p[c .. c + 7], zero from column k on; FAST: 16-byte
-// aligned and k a multiple of 8.
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight fp16 elements p[c .. c + 7], zero from column k on. FAST: 16-byte
+// aligned and k a multiple of 8; otherwise one load at any alignment, and
+// single elements at the end of a row only.
 template <bool FAST>
 __device__ __forceinline__ mfma_half8_t load8(const uint16_t* __restrict__ p, int64_t c, int64_t k) {
   if constexpr (FAST) {
@@ -95,6 +98,7 @@ __device__ __forceinline__ mfma_half8_t load8(const uint16_t* __restrict__ p, in
     if (c < k) v = *reinterpret_cast<const uint4*>(p + c);
     return __builtin_bit_cast(mfma_half8_t, v);
   } else {
+    if (c + 8 <= k) return __builtin_bit_cast(mfma_half8_t, u32x4_t(*reinterpret_cast<const u32x4_any_t*>(p + c)));
     mfma_half8_t v;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c + e < k ? __builtin_bit_cast(_Float16, p[c + e]) : static_cast<_Float16>(0.0f);
