@@ -540,40 +540,28 @@ void launch_tile(const uint32_t* p1, const float* s1, const uint32_t* p2, const 
                      static_cast<int>(mb), static_cast<int>(nb), y, h);
 }
 
-// The tile that finishes first, counted in rounds of 256 workgroups (one a
-// CU) times the time of a round: 51, 32, 20, 14 and 11.5 us at k = 4,096 on
-// MI355X for 256 x 256, 128 x 256, 64 x 256, 64 x 128 and 32 x 128 (measured
-// with 192 to 256 workgroups of each). Each was the fastest of twenty shapes
-// where this picks it: n = 12,288 at m = 64 / 100 / 256 / 512 / 1,024 takes
-// 11.5 / 14.3 / 18.9 / 31.9 / 51.1 us, against 15.3 / 22.2 / 21.5 / 33.2 /
-// 54.2 us for the neighbouring choice. None below 192 workgroups: few rows
-// stream the weights instead (100 rows, n = 4,096: 8.2 against 11.9 us).
-enum Tile { kNone, k256x256, k128x256, k64x256, k64x128, k32x256, k32x128 };
+// Rows and columns of a workgroup, and the time of a round of 256 of them (one
+// a CU) in us.
+struct Shape {
+  int rows, columns;
+  double round;
+};
 
-Tile pick_tile(int64_t m, int64_t columns, bool swiglu) {
-  struct Shape {
-    Tile tile;
-    int rows, columns;
-    double round;
-    bool plain, swiglu;
-  };
-  static const Shape shapes[] = {{k256x256, 256, 256, 51.0, true, true}, {k128x256, 128, 256, 32.0, true, true},
-                                 {k64x256, 64, 256, 20.0, true, true},   {k64x128, 64, 128, 14.0, true, false},
-                                 {k32x256, 32, 256, 16.0, false, true},  {k32x128, 32, 128, 11.5, true, false}};
-  Tile best = kNone;
+// The shape that takes the least rounds x time of a round.
+template <int N>
+int pick_shape(const Shape (&shapes)[N], int64_t m, int64_t columns) {
+  int best = 0;
   double least = 0.0;
-  int64_t most = 0;
-  for (const Shape& s : shapes) {
-    if (!(swiglu ? s.swiglu : s.plain)) continue;
+  for (int i = 0; i < N; ++i) {
+    const Shape& s = shapes[i];
     const int64_t groups = (m + s.rows - 1) / s.rows * ((columns + s.columns - 1) / s.columns);
     const double t = static_cast<double>((groups + 255) / 256) * s.round;
-    if (groups > most) most = groups;
-    if (best == kNone || t < least) {
-      best = s.tile;
+    if (i == 0 || t < least) {
+      best = i;
       least = t;
     }
   }
-  return most < 192 || m <= 32 ? kNone : best;
+  return best;
 }
 
 // The kernels of one to eight rows whose loads are whole pieces of one row (us
@@ -638,70 +626,70 @@ bool launch_gemv_gate_up(const uint32_t* gate, const float* gate_scale, const ui
 
 }  // namespace
 
-// Streaming shapes by the workgroups they leave (us at m = 8, 32, 64 or 100
-// against the next best): n >= 8,192 three tiles of 8 waves (6.1; 6.5 for one
-// tile), n >= 5,120 two (5.0 against 5.2), fewer columns one tile of 16 waves
-// (4.2 against 4.4 of 8); 17 to 32 rows two row tiles at n >= 8,192 (8.5
-// against 9.5), else one (5.3 for two column tiles against 6.1); more rows
-// 2 x 4 tiles (8.2 against 8.8), at n <= 2,048 one row tile (4.9 against 5.3).
+// Streaming shapes up to 48 x 64, tiles from 32 x 128 on. The times of a round
+// are those of 128 to 256 workgroups at k = 4,096 on MI355X; at k = 12,288 all
+// grow alike (by 2.0 to 2.4). Where it picks a shape, that shape was within 5
+// % of the fastest of 24 (m x n at k = 4,096, us against the runner-up of
+// another size): 8 x 4,096 4.2 / 5.0, 32 x 4,096 5.3 / 6.1, 64 x 4,096 6.6 /
+// 7.4, 100 x 4,096 8.2 / 8.7, 160 x 4,096 10.1 / 11.2, 64 x 12,288 11.5 /
+// 16.6, 100 x 12,288 14.3 / 17.2, 256 x 12,288 18.9 / 21.5, 512 x 12,288 31.9
+// / 33.2, 1,024 x 12,288 51.1 / 54.2.
 hipError_t launch_ternary_gemm_i8(const uint32_t* packed, const float* scale, int64_t n, int64_t k, const int8_t* q,
                                   const float* q_scale, int64_t m, float* y, hipStream_t stream) {
   if (launch_gemv_rows(packed, scale, n, k, q, q_scale, m, y, stream)) return hipGetLastError();
+  static const Shape shapes[] = {{16, 16, 4.3}, {16, 32, 5.2}, {16, 48, 6.3},   {16, 64, 6.5},   {32, 32, 6.3},
+                                 {32, 48, 8.0}, {32, 64, 8.3}, {48, 48, 9.6},   {48, 64, 10.0},  {32, 128, 11.5},
+                                 {64, 128, 14}, {64, 256, 20}, {128, 256, 32.0}, {256, 256, 51.0}};
 #define PBG_TILE(...) \
   launch_tile<__VA_ARGS__, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream)
 #define PBG_STREAM(...) \
   launch_stream<__VA_ARGS__, false>(packed, scale, nullptr, nullptr, n, k, q, q_scale, m, y, nullptr, stream)
-  switch (pick_tile(m, n, false)) {
-    case k256x256: PBG_TILE(2, 4, 4, 2, 1); break;
-    case k128x256: PBG_TILE(2, 4, 2, 2, 2); break;
-    case k64x256: PBG_TILE(1, 8, 2, 1, 2); break;
-    case k64x128: PBG_TILE(1, 4, 2, 1, 4); break;
-    case k32x128: PBG_TILE(1, 4, 1, 1, 4); break;
-    default:
-      if (m <= 16) {
-        if (n >= 8192) PBG_STREAM(1, 3, 8);
-        else if (n >= 5120) PBG_STREAM(1, 2, 8);
-        else PBG_STREAM(1, 1, 16);
-      } else if (m <= 32) {
-        if (n >= 8192) PBG_STREAM(2, 3, 8);
-        else if (n > 2048) PBG_STREAM(1, 2, 8);
-        else PBG_STREAM(1, 1, 16);
-      } else {
-        if (n > 2048) PBG_STREAM(2, 4, 8);
-        else if (m > 64) PBG_STREAM(1, 2, 8);
-        else PBG_STREAM(1, 1, 16);
-      }
+  switch (pick_shape(shapes, m, n)) {
+    case 0: PBG_STREAM(1, 1, 16); break;
+    case 1: PBG_STREAM(1, 2, 8); break;
+    case 2: PBG_STREAM(1, 3, 8); break;
+    case 3: PBG_STREAM(1, 4, 8); break;
+    case 4: PBG_STREAM(2, 2, 8); break;
+    case 5: PBG_STREAM(2, 3, 8); break;
+    case 6: PBG_STREAM(2, 4, 8); break;
+    case 7: PBG_STREAM(3, 3, 8); break;
+    case 8: PBG_STREAM(3, 4, 8); break;
+    case 9: PBG_TILE(1, 4, 1, 1, 4); break;
+    case 10: PBG_TILE(1, 4, 2, 1, 4); break;
+    case 11: PBG_TILE(1, 8, 2, 1, 2); break;
+    case 12: PBG_TILE(2, 4, 2, 2, 2); break;
+    default: PBG_TILE(2, 4, 4, 2, 1); break;
   }
 #undef PBG_TILE
 #undef PBG_STREAM
   return hipGetLastError();
 }
 
-// As above with twice the columns; the streaming shapes hold as many gate as
-// up tiles (m = 8, d_ff = 12,288: 9.2 us for three of each against 9.5; m = 32
-// 11.9 against 14.9; d_ff = 1,024 3.3 for one of each).
+// The same with d_ff columns of gate and of up in a workgroup (8 x 4,096 5.4
+// us against 5.7, 32 x 4,096 7.2 / 7.9, 64 x 4,096 9.1 / 9.9, 32 x 12,288 11.8
+// / 12.8, 64 x 12,288 16.4 / 21.3, 256 x 12,288 31.6 / 33.3).
 hipError_t launch_swiglu_gate_up_i8(const uint32_t* gate, const float* gate_scale, const uint32_t* up,
                                     const float* up_scale, int64_t d_model, int64_t d_ff, const int8_t* q,
                                     const float* q_scale, int64_t m, uint16_t* h, hipStream_t stream) {
   if (launch_gemv_gate_up(gate, gate_scale, up, up_scale, d_model, d_ff, q, q_scale, m, h, stream))
     return hipGetLastError();
+  static const Shape shapes[] = {{16, 16, 5.3},  {16, 32, 7.2},  {16, 48, 9.0},   {32, 32, 9.0},   {32, 48, 11.8},
+                                 {48, 48, 13.9}, {32, 128, 16.0}, {64, 128, 21.0}, {128, 128, 32.0}, {256, 128, 51.0}};
 #define PBG_TILE(...) \
   launch_tile<__VA_ARGS__, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream)
 #define PBG_STREAM(...) \
   launch_stream<__VA_ARGS__, true>(gate, gate_scale, up, up_scale, d_ff, d_model, q, q_scale, m, nullptr, h, stream)
-  switch (pick_tile(m, 2 * d_ff, true)) {
-    case k256x256: PBG_TILE(2, 4, 4, 2, 1); break;
-    case k128x256: PBG_TILE(2, 4, 2, 2, 2); break;
-    case k64x256: PBG_TILE(1, 4, 2, 2, 2); break;
-    case k32x256: PBG_TILE(1, 4, 1, 2, 4); break;
-    default:
-      if (m <= 16) {
-        if (d_ff >= 8192) PBG_STREAM(1, 3, 8);
-        else PBG_STREAM(1, 1, 8);
-      } else {
-        if (d_ff >= 8192) PBG_STREAM(2, 3, 8);
-        else PBG_STREAM(2, 2, 8);
-      }
+  switch (pick_shape(shapes, m, d_ff)) {
+    case 0: PBG_STREAM(1, 1, 16); break;
+    case 1: PBG_STREAM(1, 2, 8); break;
+    case 2: PBG_STREAM(1, 3, 8); break;
+    case 3: PBG_STREAM(2, 2, 8); break;
+    case 4: PBG_STREAM(2, 3, 8); break;
+    case 5: PBG_STREAM(3, 3, 8); break;
+    case 6: PBG_TILE(1, 4, 1, 2, 4); break;
+    case 7: PBG_TILE(1, 4, 2, 2, 2); break;
+    case 8: PBG_TILE(2, 4, 2, 2, 2); break;
+    default: PBG_TILE(2, 4, 4, 2, 1); break;
   }
 #undef PBG_TILE
 #undef PBG_STREAM

@@ -181,7 +181,8 @@ GEMM_SHAPES = [(1, 1, 1), (1, 17, 64), (2, 5, 65), (16, 16, 256), (17, 33, 320),
                (1, 9001, 200), (1, 50, 5000), (1, 5003, 5000), (1, 41, 9000), (1, 4201, 9000), (1, 30, 16384),
                (1, 4101, 16300), (1, 10, 20000), (2, 4097, 300), (2, 33, 8000), (2, 35, 12288), (2, 9, 14000),
                (3, 33, 4000), (4, 5001, 1000), (3, 8200, 100), (5, 300, 4096), (8, 2048, 70), (6, 100, 5000),
-               (20, 9000, 700), (50, 900, 1100),  # and each tile, with rows, columns and K that end inside it
+               (20, 9000, 700), (50, 900, 1100), (60, 4096, 300), (40, 6140, 600), (100, 4090, 500), (47, 12280, 260),
+               (150, 4096, 900), (16, 16380, 300), (33, 2000, 257),  # and each tile, with rows, columns and K that end inside it
                (63, 12288, 580), (250, 12290, 328), (510, 12288, 700), (1000, 12290, 328)]
 
 
@@ -236,7 +237,7 @@ def test_gemm_i8_reads_every_code(pbg):
 
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 12288, 4096), (8, 333, 4096), (16, 40, 72), (65, 100, 200), (130, 257, 1000),
                                    (300, 520, 4096), (40, 2048, 4096), (600, 130, 640), (30, 9000, 200), (63, 12300, 580),
-                                   (1, 99, 5000), (1, 101, 9000), (1, 33, 16300), (1, 9, 20000), (2, 101, 500),
+                                   (20, 4000, 300), (40, 4090, 500), (47, 12280, 260), (9, 12288, 600), (1, 99, 5000), (1, 101, 9000), (1, 33, 16300), (1, 9, 20000), (2, 101, 500),
                                    (2, 50, 5000), (3, 40, 300),
                                    (100, 12290, 328), (256, 12300, 700), (510, 12290, 328)])
 def test_swiglu_gate_up_i8(pbg, m, n, k):
