@@ -459,8 +459,9 @@ int quantize_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* q, float* q_s
 /*
  * ternary_gemm_i8 - Y[i][r] = q_scale[i] * scale[r] * sum_j c[r][j] * q[i][j]
  * for any number of 8-bit activation rows. The sum is exact; the two scales
- * are applied in fp32 afterwards, so the result does not depend on the split
- * of the work and is the same bits on every call.
+ * are applied in fp32 afterwards, q_scale first, so the result does not depend
+ * on the split of the work: a row's outputs are the same bits on every call
+ * and for every m.
  *   packed, scale, n  as ternary_gemv
  *   q        [m][pbg_q8_row_bytes(k)] int8, 16-byte aligned; the full range
  *            -128..127 is taken; bytes past column k - 1 may hold anything

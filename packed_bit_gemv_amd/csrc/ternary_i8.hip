@@ -280,12 +280,13 @@ __global__ __launch_bounds__(G* kWave) void gemv_i8_kernel(const uint4* __restri
   }
   // the sums that this lane gets: slot i of each reduction
   const int slot = reduce4_slot(lane);
-  float sc[kRed];
+  float row_s[kRed], col_s[kRed];  // applied one after the other, as the other kernels do
 #pragma unroll
   for (int e = 0; e < kRed; ++e) {
     const int idx = 4 * e + (slot < 0 ? 0 : slot), a = idx / RR, i = idx % RR;
     const int64_t r = row0 + (SWIGLU ? i / 2 : i);
-    sc[e] = (SWIGLU && (i & 1) ? scale2 : scale)[r < n ? r : n - 1] * q_scale[a < m ? a : m - 1];
+    row_s[e] = q_scale[a < m ? a : m - 1];
+    col_s[e] = (SWIGLU && (i & 1) ? scale2 : scale)[r < n ? r : n - 1];
   }
   __builtin_amdgcn_sched_barrier(0);
 
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(G* kWave) void gemv_i8_kernel(const uint4* __restri
   for (int e = 0; e < kRed; ++e) {
     const float red = wave_reduce4(static_cast<float>(acc[4 * e]), static_cast<float>(acc[4 * e + 1]),
                                    static_cast<float>(acc[4 * e + 2]), static_cast<float>(acc[4 * e + 3]));
-    const float v = red * (1.0f / (1 << kCodeShift)) * sc[e];
+    const float v = red * (1.0f / (1 << kCodeShift)) * row_s[e] * col_s[e];
     const int idx = 4 * e + slot, a = idx / RR, i = idx % RR;
     const int64_t r = row0 + (SWIGLU ? i / 2 : i);
     const bool in = slot >= 0 && idx < kSums && a < m && r < n;

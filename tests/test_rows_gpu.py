@@ -235,6 +235,21 @@ def test_gemm_i8_reads_every_code(pbg):
     assert np.array_equal(y.T, codes)
 
 
+def test_a_row_does_not_depend_on_its_batch(pbg):
+    """The same bits for a row alone and among 2 to 600 others, whichever kernel takes them."""
+    n, k, most = 520, 1088, 600
+    rng = np.random.default_rng(9)
+    q, qs = dev(rng.integers(-128, 128, (most, k)).astype(np.int8)), dev(synth.row_scales(1, most))
+    w = [pbg.pack_ternary(dev(synth.ternary_codes(i, n, k)))[0] for i in (1, 2)]
+    s = [dev(synth.row_scales(i, n)) for i in (3, 4)]
+    y = pbg.ternary_gemm_i8(w[0], s[0], k, q, qs)
+    h = pbg.ternary_swiglu_gate_up_i8(w[0], s[0], w[1], s[1], k, q, qs)
+    for m in (1, 2, 3, 5, 8, 9, 17, 33, 64, 100, 257):
+        a = slice(most - m, most)
+        assert torch.equal(pbg.ternary_gemm_i8(w[0], s[0], k, q[a], qs[a]), y[a]), m
+        assert torch.equal(pbg.ternary_swiglu_gate_up_i8(w[0], s[0], w[1], s[1], k, q[a], qs[a]), h[a]), m
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 12288, 4096), (8, 333, 4096), (16, 40, 72), (65, 100, 200), (130, 257, 1000),
                                    (300, 520, 4096), (40, 2048, 4096), (600, 130, 640), (30, 9000, 200), (63, 12300, 580),
                                    (20, 4000, 300), (40, 4090, 500), (47, 12280, 260), (9, 12288, 600), (1, 99, 5000), (1, 101, 9000), (1, 33, 16300), (1, 9, 20000), (2, 101, 500),
