@@ -13,7 +13,8 @@
 // adapter in LDS and cuts the sorted list into groups of at most 16 rows of
 // one adapter, which is what a matrix instruction takes: an adapter's weights
 // are read once per group, not once per row, and only for its own rows, so
-// that NaN in one adapter cannot reach another's rows.
+// that NaN in one adapter cannot reach another's rows. Where many adapters
+// share many rows, a launch before sorts those rows by adapter.
 #include "pbg_device.hpp"
 #include "pbg_internal.hpp"
 
@@ -23,6 +24,7 @@ namespace {
 constexpr int kRows = 16;       // rows of a group
 constexpr int kWaves = 4;
 constexpr int kMaxSlices = 16;  // slices of K
+constexpr int64_t kSortBytes = 160 << 20;  // of adapters that mixed rows would read again
 
 // Up to 16 rows are one block whose second launch adds the slices itself.
 bool lora_one_block(int64_t m) { return m <= kRows; }
@@ -36,23 +38,26 @@ int lora_slices(int64_t m) {
 
 int rank_padded(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
-// The groups of R rows from m0 on. Built by the first R threads (R <= 64: one
-// wave); group g is order[start[g]] .. order[start[g + 1] - 1]. Rows without
-// an adapter come last, in groups with id -1; rows past m are left out.
+// The groups of R places from m0 on: rows m0 .. m0 + R - 1, or perm of them
+// with their ids. Built by the first R threads (R <= 64: one wave); group g is
+// the rows row[start[g]] .. row[start[g + 1] - 1]. Rows without an adapter
+// come last, in groups with id -1; places past m are left out.
 template <int R>
 struct Groups {
   int key[R];         // adapter of a row, `adapters` for none, INT_MAX past m
-  int16_t order[R];   // rows by key
+  int row[R];         // rows by key
   int16_t start[R + 1];
   int id[R];          // adapter of a group
   int count;
 
-  __device__ void build(const int32_t* __restrict__ ids, int64_t m0, int64_t m, int adapters) {
+  __device__ void build(const int32_t* __restrict__ ids, const int32_t* __restrict__ perm, int64_t m0, int64_t m,
+                        int adapters) {
     static_assert(R <= kWave, "one wave sorts");
     const int i = threadIdx.x;
     if (i < kWave) {
-      int k = 0x7FFFFFFF;
+      int k = 0x7FFFFFFF, of = 0;
       if (i < R && m0 + i < m) {
+        of = perm ? perm[m0 + i] : static_cast<int>(m0 + i);
         const int t = ids[m0 + i];
         k = t >= 0 && t < adapters ? t : adapters;
       }
@@ -64,7 +69,7 @@ struct Groups {
       }
       if (i < R) {
         key[place] = k;
-        order[place] = static_cast<int16_t>(i);
+        row[place] = of;
       }
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -86,11 +91,65 @@ struct Groups {
   }
 };
 
+// Where many adapters mix in a prompt, a block of 64 rows holds few rows of
+// each. Then the rows are put in the order of their adapters first: perm, by a
+// counting sort of kChunk rows in a workgroup, and the ids in that order. Only
+// the grouping depends on it, no result does: rows of one adapter come in the
+// order of their atomics, and ids that share a bin are told apart by the
+// groups.
+constexpr int kChunk = 4096;
+constexpr int kBins = 1024;  // the last one for rows without an adapter
+
+__global__ __launch_bounds__(kBins) void lora_sort_kernel(const int32_t* __restrict__ ids, int64_t m, int adapters,
+                                                          int32_t* __restrict__ sorted, int32_t* __restrict__ perm) {
+  __shared__ int bin[kBins];
+  __shared__ int before[kBins / kWave];
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kChunk;
+  int id[kChunk / kBins], of[kChunk / kBins], at[kChunk / kBins];
+  bin[t] = 0;
+#pragma unroll
+  for (int u = 0; u < kChunk / kBins; ++u) {
+    const int64_t row = c0 + t + u * kBins;
+    id[u] = row < m ? ids[row] : 0;
+    of[u] = id[u] >= 0 && id[u] < adapters ? id[u] % (kBins - 1) : kBins - 1;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kChunk / kBins; ++u)
+    at[u] = c0 + t + u * kBins < m ? atomicAdd(&bin[of[u]], 1) : 0;
+  __syncthreads();
+  int sum = bin[t];
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const int other = __shfl_up(sum, d);
+    sum += lane >= d ? other : 0;
+  }
+  if (lane == kWave - 1) before[t / kWave] = sum;
+  __syncthreads();
+  int start = sum - bin[t];
+#pragma unroll
+  for (int w = 0; w < kBins / kWave; ++w) start += w < t / kWave ? before[w] : 0;
+  bin[t] = start;
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kChunk / kBins; ++u) {
+    const int64_t row = c0 + t + u * kBins;
+    if (row < m) {
+      const int64_t place = c0 + bin[of[u]] + at[u];
+      sorted[place] = id[u];
+      perm[place] = static_cast<int32_t>(row);
+    }
+  }
+}
+
 typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
 
 // Eight fp16 elements p[c .. c + 7], zero from column k on. FAST: 16-byte
 // aligned and k a multiple of 8; otherwise one load at any alignment, and
-// single elements at the end of a row only.
+// single elements at the end of a row only. The second does everything, the
+// first is faster: 900 rows of 12 adapters at rank 32, k = 6,000, take 27.9
+// against 32.4 us, 300 rows of 40 at rank 16 20.9 against 23.6.
 template <bool FAST>
 __device__ __forceinline__ mfma_half8_t load8(const uint16_t* __restrict__ p, int64_t c, int64_t k) {
   if constexpr (FAST) {
@@ -126,6 +185,7 @@ __device__ __forceinline__ float row_max16(float v) {
 template <int R, int RT, bool FAST>
 __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t* __restrict__ x,
                                                                   const int32_t* __restrict__ ids,
+                                                                  const int32_t* __restrict__ perm,
                                                                   const uint16_t* __restrict__ a, int64_t m, int64_t k,
                                                                   int adapters, int rank, int64_t k_slice,
                                                                   float* __restrict__ v) {
@@ -136,7 +196,7 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int li = lane & 15, lg = lane >> 4;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * R;
-  groups.build(ids, m0, m, adapters);
+  groups.build(ids, perm, m0, m, adapters);
   const int64_t k0 = blockIdx.y * k_slice;
   const int64_t k1 = k0 + k_slice < k ? k0 + k_slice : k;
   const int count = __builtin_amdgcn_readfirstlane(groups.count);
@@ -144,7 +204,7 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t
     const int ad = __builtin_amdgcn_readfirstlane(groups.id[g]);
     if (ad < 0) break;  // the groups without an adapter are the last ones
     const int p0 = groups.start[g], p1 = groups.start[g + 1];
-    const uint16_t* xr = x + (m0 + groups.order[p0 + li < p1 ? p0 + li : p0]) * k;
+    const uint16_t* xr = x + static_cast<int64_t>(groups.row[p0 + li < p1 ? p0 + li : p0]) * k;
     const uint16_t* ar[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -184,7 +244,7 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t
       for (int e = 0; e < 4; ++e) {
         const int at = p0 + 4 * lg + e;
         if (at < p1 && 16 * t + li < rank)
-          v[(blockIdx.y * m + m0 + groups.order[at]) * rank + 16 * t + li] = acc[t][e];
+          v[(blockIdx.y * m + groups.row[at]) * rank + 16 * t + li] = acc[t][e];
       }
     }
   }
@@ -251,6 +311,7 @@ typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
 // the product's layout: 73 us).
 template <int R, int RT, int C, bool JOIN, bool FAST>
 __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, const int32_t* __restrict__ ids,
+                                                                const int32_t* __restrict__ perm,
                                                                 const uint16_t* __restrict__ b,
                                                                 const float* __restrict__ scale, int64_t m, int64_t n,
                                                                 int adapters, int rank, int slices, int64_t n_blocks,
@@ -270,7 +331,7 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int li = lane & 15, lg = lane >> 4;
   const int64_t m0 = blockIdx.x / n_blocks * R;
-  groups.build(ids, m0, m, adapters);
+  groups.build(ids, perm, m0, m, adapters);
   const int64_t n0 = (blockIdx.x % n_blocks * kWaves + wave) * kTile;
   const int count = __builtin_amdgcn_readfirstlane(groups.count);
   const int pc = 4 * (lane % kGroup);  // this lane's columns of y and out, rows lane / kGroup + i (64 / kGroup)
@@ -287,7 +348,7 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, 
     for (int i = 0; i < kPieces; ++i) {
       const int at = p0 + lane / kGroup + i * (kWave / kGroup);
       in[i] = at < p1;
-      row[i] = (m0 + groups.order[in[i] ? at : p0]) * n;
+      row[i] = groups.row[in[i] ? at : p0] * n;
       base[i] = mfma_float4_t{};
       if (in[i] && r0 + 4 <= n) {
         base[i] = *reinterpret_cast<const f32x4_any_t*>(y + row[i] + r0);
@@ -314,13 +375,13 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, 
       if constexpr (JOIN) {
         const int i = threadIdx.x >> 4;
         __syncthreads();
-        join_row<RT>(v + (m0 + groups.order[p0 + i < p1 ? p0 + i : p0]) * rank, m * rank, slices, rank, scale[ad],
+        join_row<RT>(v + static_cast<int64_t>(groups.row[p0 + i < p1 ? p0 + i : p0]) * rank, m * rank, slices, rank, scale[ad],
                      own[i][0], own[i][1], own_factor + i);
         __syncthreads();
         src = own[li][0];
         bk = own_factor[li];
       } else {
-        const int64_t at = m0 + groups.order[p0 + li < p1 ? p0 + li : p0];
+        const int64_t at = groups.row[p0 + li < p1 ? p0 + li : p0];
         src = parts + at * (2 * RP);
         bk = factors[at];
       }
@@ -379,19 +440,22 @@ struct Args {
   int64_t m, n, k;
   int adapters, rank;
   float* out;
+  const int32_t* perm;  // with ids in its order; null: rows as they come
   void* ws;
   hipStream_t stream;
 };
 
 // Workspace: the slices' sums [slices][m][rank], then, 16-byte aligned, the
-// parts [m][2][padded rank] and the factors [m].
+// parts [m][2][padded rank] and the factors [m], then, for more rows than a
+// block, the sorted ids and perm [m].
 int64_t sums_bytes(int64_t m, int rank) { return (4 * m * rank * lora_slices(m) + 15) / 16 * 16; }
+int64_t parts_bytes(int64_t m, int rank) { return 4 * m * (rank_padded(rank) + 1); }
 
 template <int R, int RT, bool FAST>
 void launch_down(const Args& g, int slices, int64_t k_slice, int64_t z) {
   hipLaunchKernelGGL((lora_down_kernel<R, RT, FAST>),
                      dim3(static_cast<unsigned>((g.m + R - 1) / R), slices, static_cast<unsigned>(z)),
-                     dim3(kWaves * kWave), 0, g.stream, g.x, g.ids, g.a, g.m, g.k, g.adapters, g.rank, k_slice,
+                     dim3(kWaves * kWave), 0, g.stream, g.x, g.ids, g.perm, g.a, g.m, g.k, g.adapters, g.rank, k_slice,
                      static_cast<float*>(g.ws));
 }
 
@@ -401,13 +465,13 @@ void launch_up(const Args& g, int slices, int64_t z) {
   const _Float16* parts = reinterpret_cast<const _Float16*>(static_cast<char*>(g.ws) + sums_bytes(g.m, g.rank));
   hipLaunchKernelGGL((lora_up_kernel<R, RT, C, JOIN, FAST>),
                      dim3(static_cast<unsigned>(blocks * nb), static_cast<unsigned>(z)), dim3(kWaves * kWave), 0,
-                     g.stream, g.y, g.ids, g.b, g.scale, g.m, g.n, g.adapters, g.rank, slices, nb,
+                     g.stream, g.y, g.ids, g.perm, g.b, g.scale, g.m, g.n, g.adapters, g.rank, slices, nb,
                      static_cast<const float*>(g.ws), parts, reinterpret_cast<const float*>(parts + g.m * 32 * RT),
                      g.out);
 }
 
 template <int RT, bool FAST>
-void launch(const Args& g) {
+void launch(Args g) {
   const int64_t ks = slice_columns(g.k, lora_slices(g.m));
   const int slices = static_cast<int>((g.k + ks - 1) / ks);
   if (lora_one_block(g.m)) {
@@ -423,7 +487,23 @@ void launch(const Args& g) {
   // product unsliced on 16 waves and its parts finished in place, is slower: 15.9 us for the 64 rows, 80 against 37 at
   // rank 64 and n = 12,288.)
   const int64_t blocks = (g.m + 63) / 64;
-  const int64_t most = g.adapters < 59 ? g.adapters + 5 : 64;
+  const int32_t* by_row = g.ids;
+  int64_t most = g.adapters < 59 ? g.adapters + 5 : 64;
+  // In a prompt of mixed rows every block reads its part of nearly all the adapters, and sorted rows read each about
+  // once; the sort costs 4 us, which rows that come in runs pay for nothing. At n = 12,288, k = 4,096, rank 64, 1,531
+  // mixed rows of 64 / 24 / 8 / 3 adapters take 101 / 84 / 75 / 68 us sorted, 321 / 201 / 116 / 79 not, and in runs of
+  // 24 / 3 82 / 65.5 and 77 / 61.5; at n = 4,096 and rank 16, 1,000 rows of 16 take 25 and 29 us, 256 rows of 16 18.0
+  // and 16.6. So it runs from the bytes on at which mixed rows gain about four times its cost.
+  if ((blocks - 1) * (g.adapters < 60 ? g.adapters : 60) * (32 * RT) * (g.n + g.k) >= kSortBytes) {
+    int32_t* sorted = reinterpret_cast<int32_t*>(static_cast<char*>(g.ws) + sums_bytes(g.m, g.rank) +
+                                                 parts_bytes(g.m, g.rank));
+    hipLaunchKernelGGL(lora_sort_kernel, dim3(static_cast<unsigned>((g.m + kChunk - 1) / kChunk)), dim3(kBins), 0,
+                       g.stream, g.ids, g.m, g.adapters, sorted, sorted + g.m);
+    g.ids = sorted;
+    g.perm = sorted + g.m;
+    const int64_t few = 6 + g.adapters / (blocks < 64 ? blocks : 64);
+    most = few < most ? few : most;
+  }
   auto share = [&](int64_t workgroups, int64_t fill) {
     const int64_t z = fill / workgroups < 3 ? 3 : fill / workgroups;
     return z < most ? z : most;
@@ -439,10 +519,12 @@ void launch(const Args& g) {
   }
   _Float16* parts = reinterpret_cast<_Float16*>(static_cast<char*>(g.ws) + sums_bytes(g.m, g.rank));
   hipLaunchKernelGGL((lora_join_kernel<RT>), dim3(static_cast<unsigned>((g.m + 15) / 16)), dim3(256), 0, g.stream,
-                     g.ids, g.scale, g.m, g.adapters, g.rank, slices, static_cast<const float*>(g.ws), parts,
+                     by_row, g.scale, g.m, g.adapters, g.rank, slices, static_cast<const float*>(g.ws), parts,
                      reinterpret_cast<float*>(parts + g.m * 32 * RT));
+  // 64 columns of a wave need the workgroups to fill the chip: at n = 4,096 1,000 rows of 16 adapters take 29.1 us with
+  // them and 25.9 with 32, 512 rows 22.5 and 19.8; at n = 12,288 1,531 rows of 3 61.6 and 64.5.
   const int64_t wide = blocks * ((g.n + 64 * kWaves - 1) / (64 * kWaves));
-  if (wide >= 256) launch_up<64, RT, 4, false, FAST>(g, slices, share(wide, 2048));
+  if (wide >= 384) launch_up<64, RT, 4, false, FAST>(g, slices, share(wide, 2048));
   else launch_up<64, RT, 2, false, FAST>(g, slices, share(2 * wide, 2048));
 }
 
@@ -461,13 +543,13 @@ bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; 
 }  // namespace
 
 int64_t lora_workspace_bytes(int64_t m, int rank) {
-  return sums_bytes(m, rank) + (lora_one_block(m) ? 0 : 4 * m * (rank_padded(rank) + 1));
+  return sums_bytes(m, rank) + (lora_one_block(m) ? 0 : parts_bytes(m, rank)) + (m > 64 ? 8 * m : 0);
 }
 
 hipError_t launch_lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
                            const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out,
                            void* ws, hipStream_t stream) {
-  const Args g{y, x, ids, a, b, scale, m, n, k, adapters, rank, out, ws, stream};
+  const Args g{y, x, ids, a, b, scale, m, n, k, adapters, rank, out, nullptr, ws, stream};
   if (k % 8 == 0 && rank % 8 == 0 && !off16(x) && !off16(a) && !off16(b)) launch_rank<true>(g);
   else launch_rank<false>(g);
   return hipGetLastError();

@@ -319,6 +319,56 @@ def test_lora_add(pbg, m, n, k, na, r, runs):
     assert torch.equal(pbg.lora_add(**{**d, "y": y}, out=y), out)  # in place, the same bits
 
 
+# Calls that put their rows in the order of the adapters first: more than one chunk of 4,096 rows, ids that share a
+# bin (more than 1,023 adapters), odd ranks, few rows.
+LORA_SORTED = [(1000, 1200, 1100, 100, 128), (4200, 300, 520, 1100, 17), (1531, 4100, 64, 64, 16), (130, 9000, 9000, 40, 64)]
+
+
+@pytest.mark.parametrize("m,n,k,na,r", LORA_SORTED)
+def test_lora_sorted(pbg, m, n, k, na, r):
+    """Against the oracle; the order of the rows, and that of the sort's atomics, do not change a bit."""
+    say(f"lora sorted m={m} n={n} k={k} adapters={na} rank={r}")
+    c = lora_case(m + n + k, m, n, k, na, r)
+    d = {i: dev(v) for i, v in c.items()}
+    ws = torch.full((pbg.lora_workspace(m, r, "cuda:0").numel() + 64,), 255, dtype=torch.uint8, device="cuda:0")
+    out = pbg.lora_add(**d, workspace=ws)
+    assert_within(host(out), oracle.lora_add(**c), lora_bound(c), "lora")
+    without = (c["ids"] < 0) | (c["ids"] >= na)
+    assert np.array_equal(host(out)[without], c["y"][without])
+    assert (ws[-64:] == 255).all()
+    for _ in range(3):
+        assert torch.equal(pbg.lora_add(**d, workspace=ws), out)
+    by = torch.argsort(d["ids"], stable=True)
+    runs = {**d, "y": d["y"][by].contiguous(), "x": d["x"][by].contiguous(), "ids": d["ids"][by].contiguous()}
+    assert torch.equal(pbg.lora_add(**runs), out[by])
+    one = {**d, "ids": torch.full_like(d["ids"], na - 1)}  # all rows in one bin
+    assert_within(host(pbg.lora_add(**one)), oracle.lora_add(**{**c, "ids": host(one["ids"])}),
+                  lora_bound({**c, "ids": host(one["ids"])}), "one adapter")
+    assert torch.equal(pbg.lora_add(**{**d, "ids": torch.full_like(d["ids"], -1)}), d["y"])
+
+
+def test_lora_sorted_graph(pbg):
+    """Captured once, replayed on new ids and rows with eager work between: the eager result's bits every time."""
+    m, n, k, na, r = 1531, 4100, 64, 64, 16
+    d = {i: dev(v) for i, v in lora_case(1, m, n, k, na, r).items()}
+    out, ws = torch.empty_like(d["y"]), pbg.lora_workspace(m, r, "cuda:0")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        pbg.lora_add(**d, out=out, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pbg.lora_add(**d, out=out, workspace=ws)
+    for i in range(4):
+        c = lora_case(10 + i, m, n, k, na, r, runs=i == 2)
+        for name in ("x", "y", "ids"):
+            d[name].copy_(dev(c[name]))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, pbg.lora_add(**d)), i
+
+
 @pytest.mark.parametrize("m,k,r", [(3, 64, 8), (40, 192, 16), (300, 64, 64), (9, 60, 5)])
 def test_lora_exact_probe(pbg, m, k, r):
     """Whole numbers and scales of powers of two: every sum is exact in fp32."""
