@@ -491,10 +491,11 @@ int ternary_swiglu_gate_up_i8(const uint32_t* gate_packed, const float* gate_sca
  * whose id is outside [0, adapters) have no adapter: out[i] = y[i]. Rows may
  * come in any order and mix; an adapter's weights are read for its own rows
  * only, so what another request's adapter holds (NaN included) does not reach
- * them. The inner sums of length `rank` keep 22 bits or more of each value;
- * accumulation is fp32.
+ * them. Each inner value (a row of a times x[i]) keeps 22 bits or more, however
+ * small it is beside the others of its row; accumulation is fp32. Infinities
+ * and NaN in y, x, a, b and scale have the effect that the formula gives them.
  *   y      [m][n] fp32, 4-byte aligned
- *   x      [m][k] fp16 bits, 2-byte aligned, finite
+ *   x      [m][k] fp16 bits, 2-byte aligned
  *   ids    [m] int32, 4-byte aligned
  *   a      [adapters][rank][k] fp16 bits, 2-byte aligned
  *   b      [adapters][n][rank] fp16 bits, 2-byte aligned

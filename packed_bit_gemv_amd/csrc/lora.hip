@@ -3,11 +3,15 @@
 // are passed through.
 //
 // v_i = A_a x_i on the f16 matrix cores (fp16 products are exact in its fp32
-// sums), then the product with B_a added to y. Between the two v is fp32 in
-// effect: it is split into two fp16 parts after a power of two has
-// brought the row's largest |v| to [2^13, 2^14), which hold v to 2^-22 of
-// itself (2^-38 of the row's largest) and let B_a stay fp16 on the matrix
-// cores.
+// sums), then the product with B_a added to y. Between the two each v keeps 22
+// bits or more: a power of two brings the row's largest |v| to [2^13, 2^14),
+// and v = hi + 2^-11 lo in two fp16 parts, the 2^11 giving lo the range of hi,
+// so that B_a stays fp16 on the matrix cores, with a sum for each part. That
+// holds for |v| down to 2^-27 of the row's largest. Rows with a smaller one (not
+// 0), and outputs that meet an infinity or NaN, are taken from the fp32 matrix
+// cores, an eighth of the f16 rate, on v itself: 1,531 rows at rank 64, n =
+// 12,288, that are all of this kind take 78 us against 58. (Those cores for
+// every row take 66.9 us against 61.9 of ordinary rows, at rank 128 110 against 98.)
 //
 // Rows come in any order. A workgroup takes a block of R rows, sorts them by
 // adapter in LDS and cuts the sorted list into groups of at most 16 rows of
@@ -143,38 +147,39 @@ __global__ __launch_bounds__(kBins) void lora_sort_kernel(const int32_t* __restr
   }
 }
 
-typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+template <int N>
+using half_t = _Float16 __attribute__((ext_vector_type(N)));
+// The same at the alignment of an element (an alias template would drop the attribute).
+template <int N>
+struct HalfAny;
+template <>
+struct HalfAny<4> {
+  typedef _Float16 type __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct HalfAny<8> {
+  typedef _Float16 type __attribute__((ext_vector_type(8), aligned(2)));
+};
+static_assert(alignof(HalfAny<4>::type) == 2 && alignof(HalfAny<8>::type) == 2, "element alignment");
 
-// Eight fp16 elements p[c .. c + 7], zero from column k on. FAST: 16-byte
-// aligned and k a multiple of 8; otherwise one load at any alignment, and
+// N (4 or 8) fp16 elements from column c, a multiple of N, zero from column k on. FAST: p
+// 16-byte aligned and k a multiple of 8; otherwise one load at any alignment, and
 // single elements at the end of a row only. The second does everything, the
 // first is faster: 900 rows of 12 adapters at rank 32, k = 6,000, take 27.9
 // against 32.4 us, 300 rows of 40 at rank 16 20.9 against 23.6.
-template <bool FAST>
-__device__ __forceinline__ mfma_half8_t load8(const uint16_t* __restrict__ p, int64_t c, int64_t k) {
+template <int N, bool FAST>
+__device__ __forceinline__ half_t<N> load_halves(const uint16_t* __restrict__ p, int64_t c, int64_t k) {
   if constexpr (FAST) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (c < k) v = *reinterpret_cast<const uint4*>(p + c);
-    return __builtin_bit_cast(mfma_half8_t, v);
+    half_t<N> v = {};
+    if (c < k) v = *reinterpret_cast<const half_t<N>*>(p + c);
+    return v;
   } else {
-    if (c + 8 <= k) return __builtin_bit_cast(mfma_half8_t, u32x4_t(*reinterpret_cast<const u32x4_any_t*>(p + c)));
-    mfma_half8_t v;
+    if (c + N <= k) return *reinterpret_cast<const typename HalfAny<N>::type*>(p + c);
+    half_t<N> v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < k ? __builtin_bit_cast(_Float16, p[c + e]) : static_cast<_Float16>(0.0f);
+    for (int e = 0; e < N; ++e) v[e] = c + e < k ? __builtin_bit_cast(_Float16, p[c + e]) : static_cast<_Float16>(0.0f);
     return v;
   }
-}
-
-// Power of two (as its exponent) that brings a row's largest |v| to [2^13, 2^14).
-__device__ __forceinline__ int exponent_of(float top) {
-  return top > 0.0f && top < __builtin_inff() ? 13 - ilogbf(top) : 0;
-}
-
-__device__ __forceinline__ float row_max16(float v) {
-  v = fmaxf(v, row_ror<8>(v));
-  v = fmaxf(v, row_ror<4>(v));
-  v = fmaxf(v, row_ror<2>(v));
-  return fmaxf(v, row_ror<1>(v));
 }
 
 // First product: v[slice][row][rank] for the row block blockIdx.x, the slice
@@ -218,9 +223,9 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t c = c0 + 32 * kWaves * u + 8 * lg;
-        xv[u] = load8<FAST>(xr, c, k1);
+        xv[u] = load_halves<8, FAST>(xr, c, k1);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) av[u][t] = load8<FAST>(ar[t], c, k1);
+        for (int t = 0; t < RT; ++t) av[u][t] = load_halves<8, FAST>(ar[t], c, k1);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -250,12 +255,31 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_down_kernel(const uint16_t
   }
 }
 
-// v of one row on the 16 lanes of a DPP row, the slices added in order: its
-// two fp16 parts to hi and lo [16 RT], and the factor that undoes the power of
-// two, times the adapter's scale.
+// Power of two (as its exponent) that brings a row's largest |v| to [2^13, 2^14).
+// A finite v is a multiple of 2^-48 below 2^50, so this and its negative are
+// within fp32's exponents.
+__device__ __forceinline__ int exponent_of(float top) {
+  return top > 0.0f && top < __builtin_inff() ? 13 - ilogbf(top) : 0;
+}
+
+__device__ __forceinline__ float row_max16(float v) {
+  v = fmaxf(v, row_ror<8>(v));
+  v = fmaxf(v, row_ror<4>(v));
+  v = fmaxf(v, row_ror<2>(v));
+  return fmaxf(v, row_ror<1>(v));
+}
+
+// v of one row on the 16 lanes of a DPP row, the slices added in order: its two
+// fp16 parts to hi and lo [16 RT], and the factor that undoes the power of two,
+// times the adapter's scale; v itself to sum[0 .. width), 0 past the rank (sum
+// may be the first slice, which one wave has read by then). The factor is NaN, which asks for the fp32 form of
+// the second product, where the parts do not hold every v to 2^-22 or the
+// factor is no normal number. With w in hi's normal range, w - hi is at most
+// 2^-11 |w|, and lo holds it, 2^11 times, to 2^-11 of itself or 2^-25: in w
+// 2^-22 |w| or less.
 template <int RT>
-__device__ __forceinline__ void join_row(const float* __restrict__ v, int64_t slice_stride, int slices, int rank,
-                                         float scale, _Float16* hi, _Float16* lo, float* factor) {
+__device__ __forceinline__ void join_row(const float* v, int64_t slice_stride, int slices, int rank, float scale,
+                                         float* sum, int width, _Float16* hi, _Float16* lo, float* factor) {
   const int li = threadIdx.x & 15;
   float s[RT], top = 0.0f;
 #pragma unroll
@@ -271,46 +295,87 @@ __device__ __forceinline__ void join_row(const float* __restrict__ v, int64_t sl
     top = fmaxf(top, fabsf(s[t]));
   }
   const int ex = exponent_of(row_max16(top));
+  bool wide = false;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const float w = ldexpf(s[t], ex);
     const _Float16 h = static_cast<_Float16>(w);
+    wide |= w != 0.0f && !(fabsf(w) >= 0x1p-14f && fabsf(w) < __builtin_inff());
+    if (16 * t + li < width) sum[16 * t + li] = s[t];
     hi[16 * t + li] = h;
-    lo[16 * t + li] = static_cast<_Float16>(w - static_cast<float>(h));
+    lo[16 * t + li] = static_cast<_Float16>(0x1p11f * (w - static_cast<float>(h)));
   }
-  if (li == 0) *factor = ldexpf(scale, -ex);
+  const float f = ldexpf(scale, -ex);
+  wide |= scale != 0.0f && !(fabsf(f) >= 0x1p-126f && fabsf(f) < __builtin_inff());
+  const uint64_t any = __ballot(wide) >> (threadIdx.x & 48) & 0xFFFF;
+  if (li == 0) *factor = any ? __builtin_nanf("") : f;
 }
 
-// The same for every row with an adapter, parts [m][2][16 RT] and factors [m]
-// to memory; 16 rows a workgroup.
+// The same for every row with an adapter, v to the first slice, parts [m][2][16
+// RT] and factors [m] to memory; 16 rows a workgroup.
 template <int RT>
 __global__ __launch_bounds__(256) void lora_join_kernel(const int32_t* __restrict__ ids,
                                                         const float* __restrict__ scale, int64_t m, int adapters,
-                                                        int rank, int slices,
-                                                        const float* __restrict__ v, _Float16* __restrict__ parts,
-                                                        float* __restrict__ factors) {
+                                                        int rank, int slices, float* v,
+                                                        _Float16* __restrict__ parts, float* __restrict__ factors) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
   if (row >= m) return;
   const int id = ids[row];
   if (id < 0 || id >= adapters) return;
   _Float16* hi = parts + row * (32 * RT);
-  join_row<RT>(v + row * rank, m * rank, slices, rank, scale[id], hi, hi + 16 * RT, factors + row);
+  float* vr = v + row * rank;
+  join_row<RT>(vr, m * rank, slices, rank, scale[id], vr, rank, hi, hi + 16 * RT, factors + row);
+}
+
+__device__ __forceinline__ mfma_float4_t multiply(half_t<8> a, half_t<8> b, mfma_float4_t d) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, d, 0, 0, 0);
+}
+__device__ __forceinline__ mfma_float4_t multiply(half_t<4> a, half_t<4> b, mfma_float4_t d) {
+  return __builtin_amdgcn_mfma_f32_16x16x16f16(a, b, d, 0, 0, 0);
 }
 
 typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
 
-// out = y + (s_a 2^-e) B_a (hi + lo) for a row block and 16 C columns of each
-// wave, the groups blockIdx.y, + gridDim.y, ... of the block. B_a is the row
-// operand of the matrix instruction, so a lane gets four consecutive outputs
-// of one row. Ranks over 16 take 32 of the rank at a time, first hi, then lo,
-// on one load of B_a; up to 16 one instruction takes both, [hi | lo] against
-// [B_a | B_a]. Bound by y and out, which a wave reads and writes in pieces of
+// Four elements p[c .. c + 3], zero from column k on.
+__device__ __forceinline__ mfma_float4_t load_floats(const float* __restrict__ p, int c, int k) {
+  mfma_float4_t v = {};
+  if (c + 4 <= k) {
+    v = *reinterpret_cast<const f32x4_any_t*>(p + c);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (c + e < k) v[e] = p[c + e];
+  }
+  return v;
+}
+
+// Waves a SIMD that the second product's registers must leave room for: as many
+// as its ordinary path alone would, where the compiler would give the fp32 form
+// registers past that (1,531 rows of n = 12,288 at rank 128 98 against 104 us, at
+// rank 32 45.5 against 47.3; 64 rows at rank 64 26.0 against 26.9; 300 rows of n
+// = 4,097 at rank 20 33.5 against 36.1). Elsewhere a bound costs: 1,531 mixed
+// rows of 64 adapters at rank 64 104.0 us with room for 4 waves against 100.2.
+constexpr int up_waves(int rt, int c, bool join, bool fast) {
+  if (join) return 1;
+  if (c == 4) return rt == 8 ? 3 : rt == 2 && fast ? 5 : 1;
+  return rt == 2 ? 8 : rt == 4 && fast ? 7 : 1;
+}
+
+// out = y + s_a 2^-e B_a (hi + 2^-11 lo) for a row block and 16 C columns of
+// each wave, the groups blockIdx.y, + gridDim.y, ... of the block. B_a is the
+// row operand of the matrix instruction, so a lane gets four consecutive
+// outputs of one row; an instruction takes 32 of the rank (16 up to rank 16),
+// hi and lo on one load of B_a. Outputs that come out infinite or NaN, as those
+// of a row marked by its factor do, are taken from the fp32 form, on v itself:
+// fp16 parts of an infinity, and a part of 0 against one in
+// B_a, would make NaN of it. Whether an output takes that form depends on its
+// own operands only. Bound by y and out, which a wave reads and writes in pieces of
 // 64 C bytes a row: the product goes through LDS to that order. JOIN: the
 // workgroup adds the slices of its groups' v itself. 1,531 rows at rank 64, n
 // = 12,288: 45 us, 3.4 TB/s of y and out (pieces of 64 bytes, straight from
 // the product's layout: 73 us).
 template <int R, int RT, int C, bool JOIN, bool FAST>
-__global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, const int32_t* __restrict__ ids,
+__global__ __launch_bounds__(kWaves* kWave, up_waves(RT, C, JOIN, FAST)) void lora_up_kernel(const float* y, const int32_t* __restrict__ ids,
                                                                 const int32_t* __restrict__ perm,
                                                                 const uint16_t* __restrict__ b,
                                                                 const float* __restrict__ scale, int64_t m, int64_t n,
@@ -319,6 +384,7 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, 
                                                                 const _Float16* __restrict__ parts,
                                                                 const float* __restrict__ factors, float* out) {
   constexpr int KT = RT > 1 ? RT / 2 : 1;  // loads of B_a per column tile
+  constexpr int kPer = RT > 1 ? 8 : 4;     // of the rank in one of them
   constexpr int RP = 16 * RT;
   constexpr int kTile = 16 * C;            // columns of a wave
   constexpr int kGroup = kTile / 4;        // lanes on one row of y
@@ -326,6 +392,7 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, 
   __shared__ Groups<R> groups;
   __shared__ _Float16 own[JOIN ? kRows : 1][2][RP + 8];
   __shared__ float own_factor[kRows];
+  __shared__ __align__(16) float own_v[JOIN ? kRows : 1][RP + 4];
   __shared__ float turn[kWaves][kRows][kTile + 4];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -359,51 +426,84 @@ __global__ __launch_bounds__(kWaves* kWave) void lora_up_kernel(const float* y, 
       }
     }
     if (ad >= 0) {
-      mfma_half8_t bv[C][KT];
+      half_t<kPer> bv[C][KT];
       const uint16_t* ba = b + static_cast<int64_t>(ad) * n * rank;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
+      auto load_b = [&](int c, int t) {
         const int64_t r = n0 + 16 * c + li;
+        return load_halves<kPer, FAST>(ba + (r < n ? r : n - 1) * rank, kPer * (4 * t + lg), rank);
+      };
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-          bv[c][t] = load8<FAST>(ba + (r < n ? r : n - 1) * rank, RT > 1 ? 32 * t + 8 * lg : 8 * (lg & 1), rank);
-      }
-      // operand of the rows: lane (li, lg) holds 8 values of part `half` of row li
-      mfma_half8_t vf[2][KT];
-      float bk;
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int t = 0; t < KT; ++t) bv[c][t] = load_b(c, t);
+      // operand of the rows: lane (li, lg) holds kPer values of row li for each load
+      const int64_t mine = groups.row[p0 + li < p1 ? p0 + li : p0];
       const _Float16* src;
+      float back;
       if constexpr (JOIN) {
         const int i = threadIdx.x >> 4;
         __syncthreads();
-        join_row<RT>(v + static_cast<int64_t>(groups.row[p0 + i < p1 ? p0 + i : p0]) * rank, m * rank, slices, rank, scale[ad],
-                     own[i][0], own[i][1], own_factor + i);
+        join_row<RT>(v + static_cast<int64_t>(groups.row[p0 + i < p1 ? p0 + i : p0]) * rank, m * rank, slices, rank,
+                     scale[ad], own_v[i], RP, own[i][0], own[i][1], own_factor + i);
         __syncthreads();
         src = own[li][0];
-        bk = own_factor[li];
+        back = own_factor[li];
       } else {
-        const int64_t at = groups.row[p0 + li < p1 ? p0 + li : p0];
-        src = parts + at * (2 * RP);
-        bk = factors[at];
+        src = parts + mine * (2 * RP);
+        back = factors[mine];
       }
       constexpr int kLo = JOIN ? RP + 8 : RP;  // from hi to lo
+      half_t<kPer> hi[KT], lo[KT];
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
-        if constexpr (RT > 1) {
-          vf[0][t] = *reinterpret_cast<const mfma_half8_t*>(src + 32 * t + 8 * lg);
-          vf[1][t] = *reinterpret_cast<const mfma_half8_t*>(src + kLo + 32 * t + 8 * lg);
-        } else {
-          vf[0][t] = *reinterpret_cast<const mfma_half8_t*>(src + (lg >> 1) * kLo + 8 * (lg & 1));
-        }
+        hi[t] = *reinterpret_cast<const half_t<kPer>*>(src + kPer * (4 * t + lg));
+        lo[t] = *reinterpret_cast<const half_t<kPer>*>(src + kLo + kPer * (4 * t + lg));
       }
+      mfma_float4_t d[C];
+      float none = 0.0f;  // NaN once an output is infinite or NaN
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        mfma_float4_t d = {};
+        mfma_float4_t low = {};
+        d[c] = mfma_float4_t{};
 #pragma unroll
-        for (int h = 0; h < (RT > 1 ? 2 : 1); ++h)
+        for (int t = 0; t < KT; ++t) low = multiply(bv[c][t], lo[t], low);
 #pragma unroll
-          for (int t = 0; t < KT; ++t) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(bv[c][t], vf[h][t], d, 0, 0, 0);
-        *reinterpret_cast<mfma_float4_t*>(&turn[wave][li][16 * c + 4 * lg]) = bk * d;
+        for (int t = 0; t < KT; ++t) d[c] = multiply(bv[c][t], hi[t], d[c]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // both parts under the row's factor
+          d[c][e] = back * (d[c][e] + 0x1p-11f * low[e]);
+          none += 0.0f * d[c][e];
+        }
       }
+      if (__any(none != none)) {
+        // an instruction takes four of the rank, element e of each lane's kPer; B_a is read again (kept, its registers
+        // cost the ordinary path: 1,531 rows at rank 128 106 against 98 us)
+        mfma_float4_t f[C] = {};
+#pragma unroll 1
+        for (int t = 0; t < KT; ++t) {
+          mfma_float4_t vf[kPer / 4];
+          half_t<kPer> bf[C];
+#pragma unroll
+          for (int c = 0; c < C; ++c) bf[c] = load_b(c, t);
+#pragma unroll
+          for (int u = 0; u < kPer / 4; ++u) {
+            const int j = kPer * (4 * t + lg) + 4 * u;
+            if constexpr (JOIN) vf[u] = *reinterpret_cast<const mfma_float4_t*>(own_v[li] + j);
+            else vf[u] = load_floats(v + mine * rank, j, rank);
+          }
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+              f[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(static_cast<float>(bf[c][e]), vf[e / 4][e % 4], f[c], 0, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[c][e] = fabsf(d[c][e]) < __builtin_inff() ? d[c][e] : scale[ad] * f[c][e];
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) *reinterpret_cast<mfma_float4_t*>(&turn[wave][li][16 * c + 4 * lg]) = d[c];
       // one wave writes and reads its own part: LDS is in order within a wave
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
@@ -519,7 +619,7 @@ void launch(Args g) {
   }
   _Float16* parts = reinterpret_cast<_Float16*>(static_cast<char*>(g.ws) + sums_bytes(g.m, g.rank));
   hipLaunchKernelGGL((lora_join_kernel<RT>), dim3(static_cast<unsigned>((g.m + 15) / 16)), dim3(256), 0, g.stream,
-                     by_row, g.scale, g.m, g.adapters, g.rank, slices, static_cast<const float*>(g.ws), parts,
+                     by_row, g.scale, g.m, g.adapters, g.rank, slices, static_cast<float*>(g.ws), parts,
                      reinterpret_cast<float*>(parts + g.m * 32 * RT));
   // 64 columns of a wave need the workgroups to fill the chip: at n = 4,096 1,000 rows of 16 adapters take 29.1 us with
   // them and 25.9 with 32, 512 rows 22.5 and 19.8; at n = 12,288 1,531 rows of 3 61.6 and 64.5.

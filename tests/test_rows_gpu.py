@@ -558,3 +558,71 @@ def test_refusals(pbg):
                      torch.zeros((1, 8, 64), dtype=torch.float16, device="cuda:0"),
                      torch.zeros((1, 64, 8), dtype=torch.float16, device="cuda:0"), torch.ones(1, device="cuda:0"),
                      workspace=torch.zeros(16, dtype=torch.uint8, device="cuda:0"))
+
+
+# ---- lora_add: the range of the inner values ---------------------------------
+
+# Each form of the second launch: one block, the slices joined in it, the joining launch, 32 and 64 columns a wave, rows
+# sorted by a launch before, odd ranks and widths.
+LORA_WIDE = [(3, 24, 64, 2, 8), (9, 41, 60, 3, 5), (12, 300, 200, 3, 128), (40, 50, 192, 3, 16), (40, 70, 200, 3, 30),
+             (300, 130, 64, 3, 64), (100, 300, 72, 4, 128), (1531, 4100, 72, 2, 64), (1000, 1200, 1100, 100, 128),
+             (1531, 4101, 75, 40, 61)]
+
+
+@pytest.mark.parametrize("span", [12, 36])
+@pytest.mark.parametrize("m,n,k,na,r", LORA_WIDE)
+def test_lora_inner_values_of_any_range(pbg, m, n, k, na, r, span):
+    """Inner values of one row from 2^12 down to 2^(12 - span) of a whole number, each with its own rows of b: every sum
+    has one term and every operation is exact, so each output is the small inner value itself, however large the others
+    are. 12: two fp16 parts hold them; 36: they do not."""
+    say(f"lora wide m={m} n={n} k={k} adapters={na} rank={r} span={span}")
+    rng = np.random.default_rng(m + r)
+    power = np.stack([rng.permutation(np.linspace(12, 12 - span, r).round()) for _ in range(na)])
+    a = rng.integers(-3, 4, (na, r, k)) * 2.0 ** power[:, :, None]
+    b = np.zeros((na, n, r), np.float16)
+    rows = np.arange(n)
+    b[:, rows, rows % r] = rng.choice([-3, -2, -1, 1, 2, 3], (na, n))
+    c = dict(y=np.zeros((m, n), np.float32), x=rng.integers(-8, 9, (m, k)).astype(np.float16),
+             ids=rng.integers(-1, na, m).astype(np.int32), a=a.astype(np.float16), b=b,
+             scale=2.0 ** rng.integers(-1, 2, na).astype(np.float32))
+    assert np.array_equal(c["a"].astype(np.float64), a)
+    out = host(pbg.lora_add(**{i: dev(v) for i, v in c.items()}))
+    assert np.array_equal(out.astype(np.float64), oracle.lora_add(**c))
+
+
+@pytest.mark.parametrize("m,n,k,na,r", [(5, 70, 64, 3, 8), (40, 100, 100, 4, 12), (300, 129, 640, 4, 32), (100, 64, 264, 5, 128),
+                                        (1531, 4100, 64, 64, 16)])
+def test_lora_infinities(pbg, m, n, k, na, r):
+    """An infinity in x, a, b or y reaches exactly the outputs that the formula gives it, with its sign; NaN only where
+    the formula has one (infinities of both signs in a sum)."""
+    say(f"lora infinities m={m} n={n} k={k} adapters={na} rank={r}")
+    c = lora_case(m + n, m, n, k, na, r)
+    c["ids"] = (np.arange(m) % (na + 1) - 1).astype(np.int32)
+    for name in "xab":
+        c[name][c[name] == 0] = 1
+    c["a"][0, r // 2, 3] = np.inf           # every output of the rows of adapter 0
+    c["b"][1, n // 2, r - 1] = -np.inf      # one output of the rows of adapter 1
+    c["x"][3, 5] = -np.inf                  # a row of adapter 2
+    c["x"][0, 7] = np.inf                   # a row without an adapter
+    c["y"][2, 1] = np.inf                   # one output of a row of adapter 1
+    with np.errstate(invalid="ignore"):
+        ref, bound = oracle.lora_add(**c), lora_bound(c)
+    out = host(pbg.lora_add(**{i: dev(v) for i, v in c.items()})).astype(np.float64)
+    ok = np.isfinite(ref)
+    assert np.isinf(ref[1]).all() and np.isinf(ref[2, n // 2]) and np.isinf(ref[2, 1]) and np.isnan(ref[3]).any() and ok[0].all()
+    assert np.array_equal(out[~ok], ref[~ok], equal_nan=True)
+    assert_within(out[ok], ref[ok], bound[ok], "finite outputs")
+
+
+@pytest.mark.parametrize("m,n,k,na,r", [(5, 70, 64, 5, 8), (40, 100, 100, 5, 12), (300, 129, 640, 5, 32), (100, 64, 264, 5, 128)])
+def test_lora_scales_of_any_size(pbg, m, n, k, na, r):
+    """Scales of 0, below and near the smallest normal number and large ones, on small inner values: the product of the
+    scale with the sum is the only rounding more, to half of 2^-149 below the normals."""
+    say(f"lora scales m={m} n={n} k={k} rank={r}")
+    c = lora_case(m + n, m, n, k, na, r)
+    c["y"][:] = 0
+    c["x"] = (c["x"] * np.float16(2.0 ** -8)).astype(np.float16)
+    c["a"] = (c["a"] * np.float16(2.0 ** -6)).astype(np.float16)
+    c["scale"] = np.array([0.0, 1.7 * 2.0 ** -130, 1.3 * 2.0 ** -120, -1.1 * 2.0 ** -100, 1.9 * 2.0 ** 110], np.float32)
+    out = host(pbg.lora_add(**{i: dev(v) for i, v in c.items()}))
+    assert_within(out, oracle.lora_add(**c), lora_bound(c) + 2.0 ** -149, "scales")
