@@ -505,15 +505,15 @@ int ternary_swiglu_gate_up_i8(const uint32_t* gate_packed, const float* gate_sca
  *          zero rows in a or zero columns in b
  *   out    [m][n] fp32 out; may be y itself, and must not overlap it otherwise
  *   workspace  device, 16-byte aligned, pbg_lora_workspace_bytes(m, rank)
- *          bytes, of any content; calls that overlap in time need separate
- *          workspaces
+ *          bytes, of any content; one for m rows serves any fewer rows and any
+ *          lower rank; calls that overlap in time need separate workspaces
  * k a multiple of 8, rank a multiple of 8 and 16-byte aligned x, a and b take
  * the fast loads.
  */
 #define PBG_LORA_MAX_RANK 128
 #define PBG_LORA_MAX_ADAPTERS 65536
 
-/* Workspace of lora_add for m rows; 0 for m or rank out of range. */
+/* Workspace of lora_add for up to m rows and ranks up to rank, growing with both; 0 for m or rank out of range. */
 int64_t pbg_lora_workspace_bytes(int64_t m, int64_t rank);
 
 int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,

@@ -654,7 +654,7 @@ def ternary_swiglu_gate_up_i8(gate: torch.Tensor, gate_scale: torch.Tensor, up: 
 
 
 def lora_workspace(m: int, rank: int, device) -> torch.Tensor:
-    """A workspace for lora_add on m rows (its contents do not matter)."""
+    """A workspace for lora_add on up to m rows and ranks up to rank (its contents do not matter)."""
     return torch.empty((int(lib().pbg_lora_workspace_bytes(int(m), int(rank))),), dtype=torch.uint8, device=device)
 
 
@@ -664,8 +664,8 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, ids: torch.Tensor, a: torch.Tenso
     """out[i] = y[i] + scale[t] * b[t] @ (a[t] @ x[i]) with t = ids[i]; rows with t outside [0, adapters) are copied.
 
     y, out fp32 [m, n] (out may be y); x fp16 [m, k]; ids int32 [m]; a fp16 [adapters, rank, k];
-    b fp16 [adapters, n, rank]; scale fp32 [adapters]; workspace from lora_workspace(m, rank) or any
-    larger tensor (a new one is allocated if not given).
+    b fp16 [adapters, n, rank]; scale fp32 [adapters]; workspace from lora_workspace of as many rows
+    and as high a rank, or any larger tensor (a new one is allocated if not given).
     """
     m, n, dev = _matrix(y, "y", torch.float32)
     _dev(a, "a", torch.float16)

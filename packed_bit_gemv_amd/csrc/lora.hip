@@ -28,15 +28,17 @@ namespace {
 constexpr int kRows = 16;       // rows of a group
 constexpr int kWaves = 4;
 constexpr int kMaxSlices = 16;  // slices of K
+constexpr int kSliced = 16384;  // rows times slices of K
 constexpr int64_t kSortBytes = 160 << 20;  // of adapters that mixed rows would read again
 
 // Up to 16 rows are one block whose second launch adds the slices itself.
 bool lora_one_block(int64_t m) { return m <= kRows; }
 
-// Slices of K that give the chip about 1,024 workgroups of the first launch.
+// Slices of K: 16 for one block, else 8 up to 2,048 rows, then as many as keep
+// rows times slices at kSliced, down to 2.
 int lora_slices(int64_t m) {
   if (lora_one_block(m)) return kMaxSlices;
-  const int64_t s = 1024 * kRows / m;
+  const int64_t s = kSliced / m;
   return static_cast<int>(s < 2 ? 2 : s > 8 ? 8 : s);
 }
 
@@ -642,8 +644,18 @@ bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; 
 
 }  // namespace
 
+// No less than for fewer rows: what one call needs falls where its slices do,
+// after 16 rows and after the last row count with each number of slices.
 int64_t lora_workspace_bytes(int64_t m, int rank) {
-  return sums_bytes(m, rank) + (lora_one_block(m) ? 0 : parts_bytes(m, rank)) + (m > 64 ? 8 * m : 0);
+  auto call = [&](int64_t rows) {
+    return sums_bytes(rows, rank) + (lora_one_block(rows) ? 0 : parts_bytes(rows, rank)) + (rows > 64 ? 8 * rows : 0);
+  };
+  int64_t most = call(m);
+  for (int64_t last : {kRows, kSliced / 8, kSliced / 7, kSliced / 6, kSliced / 5, kSliced / 4, kSliced / 3}) {
+    const int64_t b = call(last < m ? last : m);
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 hipError_t launch_lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,

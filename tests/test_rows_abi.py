@@ -146,3 +146,15 @@ def test_oracle_norm_and_products():
     assert np.array_equal(out[1], y[1])
     w0 = b[1].astype(np.float64) @ a[1].astype(np.float64)
     assert np.allclose(out[0] - y[0], 2.0 * w0 @ x[0].astype(np.float16).astype(np.float64), rtol=1e-9, atol=1e-9)
+
+
+def test_lora_workspace_grows_with_rows_and_rank():
+    """A workspace for the most rows and the highest rank serves every smaller call."""
+    f = lib().pbg_lora_workspace_bytes
+    rows = [*range(1, 9001), *range(9001, 2 ** 20, 4999), 2 ** 20]
+    for r in (1, 3, 4, 8, 16, 17, 33, 64, 128):
+        sizes = [f(m, r) for m in rows]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), r
+    for m in (1, 16, 17, 64, 65, 2048, 2049, 4097, 9000):
+        sizes = [f(m, r) for r in range(1, 129)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), m

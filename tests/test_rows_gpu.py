@@ -626,3 +626,19 @@ def test_lora_scales_of_any_size(pbg, m, n, k, na, r):
     c["scale"] = np.array([0.0, 1.7 * 2.0 ** -130, 1.3 * 2.0 ** -120, -1.1 * 2.0 ** -100, 1.9 * 2.0 ** 110], np.float32)
     out = host(pbg.lora_add(**{i: dev(v) for i, v in c.items()}))
     assert_within(out, oracle.lora_add(**c), lora_bound(c) + 2.0 ** -149, "scales")
+
+
+@pytest.mark.parametrize("r", [4, 16, 64])
+def test_lora_one_workspace_for_fewer_rows(pbg, r):
+    """A workspace allocated once for the most rows serves every smaller call, whatever it was used for before."""
+    n, k, na = 80, 192, 3
+    ws = pbg.lora_workspace(2100, r, "cuda:0")
+    for m in (2100, 2048, 1000, 65, 64, 33, 28, 24, 17, 16, 15, 1):
+        say(f"lora workspace rank={r} m={m}")
+        mine = pbg.lora_workspace(m, r, "cuda:0")
+        assert mine.numel() <= ws.numel()
+        d = {i: dev(v) for i, v in lora_case(m + r, m, n, k, na, r).items()}
+        assert torch.equal(pbg.lora_add(**d, workspace=ws), pbg.lora_add(**d, workspace=mine)), m
+    ws = pbg.lora_workspace(17, r, "cuda:0")
+    d = {i: dev(v) for i, v in lora_case(1, 16, n, k, na, r).items()}
+    assert torch.equal(pbg.lora_add(**d, workspace=ws), pbg.lora_add(**d))
