@@ -392,10 +392,10 @@ __global__ __launch_bounds__(kWaves* kWave, up_waves(RT, C, JOIN, FAST)) void lo
   constexpr int kGroup = kTile / 4;        // lanes on one row of y
   constexpr int kPieces = 16 * kGroup / kWave;
   __shared__ Groups<R> groups;
-  __shared__ _Float16 own[JOIN ? kRows : 1][2][RP + 8];
+  __shared__ __align__(16) _Float16 own[JOIN ? kRows : 1][2][RP + 8];
   __shared__ float own_factor[kRows];
   __shared__ __align__(16) float own_v[JOIN ? kRows : 1][RP + 4];
-  __shared__ float turn[kWaves][kRows][kTile + 4];
+  __shared__ __align__(16) float turn[kWaves][kRows][kTile + 4];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int li = lane & 15, lg = lane >> 4;

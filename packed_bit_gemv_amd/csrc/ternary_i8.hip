@@ -60,7 +60,7 @@ __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
     const float* __restrict__ q_scale, int64_t m, int64_t n_blocks, float* __restrict__ y, uint16_t* __restrict__ h) {
   constexpr int TT = SWIGLU ? 2 * T : T;
   constexpr int kThreads = SK * kWave;
-  __shared__ int sums[MT * TT][4][kWave];  // element e of a lane's four sums of a tile
+  __shared__ __align__(16) int sums[MT * TT][4][kWave];  // element e of a lane's four sums of a tile
   __shared__ __align__(16) float scales[(MT + TT) * 16];  // of the rows, then of the columns
   const float* row_scale = scales;
   const float* col_scale = scales + MT * 16;
