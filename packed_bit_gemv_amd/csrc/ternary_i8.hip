@@ -127,8 +127,7 @@ __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
   int64_t u = wave;
   if (u < units) load(u);
   __builtin_amdgcn_sched_barrier(0);
-  if constexpr (SK > 1)
-    for (int i = threadIdx.x; i < MT * TT * kWave; i += kThreads) reinterpret_cast<i32x4_t*>(sums)[i] = i32x4_t{};
+  for (int i = threadIdx.x; i < MT * TT * kWave; i += kThreads) reinterpret_cast<i32x4_t*>(sums)[i] = i32x4_t{};
   if (threadIdx.x < (MT + TT) * 16) scales[threadIdx.x] = one_scale;
   __syncthreads();
   while (u < units) {
@@ -166,11 +165,9 @@ __global__ __launch_bounds__(SK* kWave) void gemm_i8_stream_kernel(
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        int* at = &sums[a * TT + t][e][lane];
-        if constexpr (SK > 1) __hip_atomic_fetch_add(at, acc[a][t][e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        else *at = acc[a][t][e];
-      }
+      for (int e = 0; e < 4; ++e)
+        __hip_atomic_fetch_add(&sums[a * TT + t][e][lane], acc[a][t][e], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_WORKGROUP);
   __syncthreads();
   // the tiles in turn to the waves: column li, activation rows 4 lg + e
 #pragma unroll
