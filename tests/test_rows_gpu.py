@@ -642,3 +642,86 @@ def test_lora_one_workspace_for_fewer_rows(pbg, r):
     ws = pbg.lora_workspace(17, r, "cuda:0")
     d = {i: dev(v) for i, v in lora_case(1, 16, n, k, na, r).items()}
     assert torch.equal(pbg.lora_add(**d, workspace=ws), pbg.lora_add(**d))
+
+
+def test_a_row_does_not_depend_on_its_batch_in_any_tile(pbg):
+    """The same bits for a row alone, in the streaming shapes and in every tile (from 33, 63, 100, 250, 510 and 1,000 rows
+    on at this width), with an odd number of 64-column chunks."""
+    n, k, most = 12290, 392, 1000
+    rng = np.random.default_rng(19)
+    q, qs = dev(pad(rng.integers(-128, 128, (most, k)).astype(np.int8))), dev(synth.row_scales(1, most))
+    codes = [synth.ternary_codes(i, n, k) for i in (1, 2)]
+    w = [pbg.pack_ternary(dev(c))[0] for c in codes]
+    s = [dev(synth.row_scales(i, n)) for i in (3, 4)]
+    y = pbg.ternary_gemm_i8(w[0], s[0], k, q, qs)
+    h = pbg.ternary_swiglu_gate_up_i8(w[0], s[0], w[1], s[1], k, q, qs)
+    ref = oracle.ternary_gemm_i8(oracle.pack(codes[0])[0], host(s[0]), k, host(q), host(qs))
+    assert_within(host(y), ref, np.abs(ref) * 2.01 * U, "y")
+    for m in (1, 2, 3, 8, 9, 17, 33, 63, 100, 160, 250, 400, 510, 700):
+        say(f"same bits m={m}")
+        a = slice(most - m, most)
+        assert torch.equal(pbg.ternary_gemm_i8(w[0], s[0], k, q[a], qs[a]), y[a]), m
+        assert torch.equal(pbg.ternary_swiglu_gate_up_i8(w[0], s[0], w[1], s[1], k, q[a], qs[a]), h[a]), m
+
+
+@pytest.mark.parametrize("m,k", [(3, 1500), (1030, 1500), (1030, 2048), (1030, 3001), (1030, 4096)])
+def test_add_rmsnorm_row_kernels(pbg, m, k):
+    """The row kernels of 1,025 to 4,096 columns, for few and for many rows."""
+    test_add_rmsnorm(pbg, m, k)
+
+
+@pytest.mark.parametrize("m,k", [(1030, 3000), (1030, 5000), (1030, 12292), (1024, 16384), (3, 3000), (3, 5000)])
+def test_quantize_rows_row_kernels(pbg, m, k):
+    """The same for the quantizer, with rows of zeros, NaN and infinities."""
+    test_quantize_rows(pbg, m, k)
+
+
+# Every form of the launches at every padded rank, aligned and not: one block; 32 columns a wave; 64 from 384 workgroups
+# on, with the last wave's columns cut.
+LORA_FORMS = [(7, 70, 64, 2, 24), (7, 71, 65, 2, 25), (16, 100, 72, 2, 64), (16, 101, 75, 2, 41), (12, 130, 75, 2, 127),
+              (300, 600, 72, 4, 16), (300, 500, 75, 3, 61),
+              (1531, 4100, 72, 3, 16), (1531, 4100, 264, 3, 24), (1531, 4100, 72, 3, 64), (1531, 4100, 72, 4, 128),
+              (1600, 4110, 75, 3, 13), (1531, 4099, 75, 3, 30), (1531, 4101, 75, 3, 61), (1531, 4099, 75, 3, 127)]
+
+
+@pytest.mark.parametrize("runs", [False, True])
+@pytest.mark.parametrize("m,n,k,na,r", LORA_FORMS)
+def test_lora_add_forms(pbg, m, n, k, na, r, runs):
+    test_lora_add(pbg, m, n, k, na, r, runs)
+
+
+LORA_SORTED_FORMS = [(1000, 2000, 4000, 60, 16), (1000, 2001, 4001, 60, 15), (1000, 2000, 1000, 60, 32),
+                     (1000, 1001, 501, 60, 61), (1000, 600, 200, 60, 128), (1531, 4101, 75, 60, 13), (1531, 4100, 264, 30, 24),
+                     (1531, 4099, 75, 60, 30), (1531, 4100, 72, 20, 64), (1531, 4101, 75, 20, 61), (1531, 4100, 72, 12, 128),
+                     (1531, 4099, 75, 12, 127)]
+
+
+@pytest.mark.parametrize("m,n,k,na,r", LORA_SORTED_FORMS)
+def test_lora_sorted_forms(pbg, m, n, k, na, r):
+    test_lora_sorted(pbg, m, n, k, na, r)
+
+
+@pytest.mark.parametrize("m,n,k,na,r", [(16, 100, 72, 2, 64), (40, 100, 104, 3, 16), (300, 130, 72, 2, 24), (1531, 4100, 64, 64, 16)])
+def test_lora_rows_do_not_share_their_range(pbg, m, n, k, na, r):
+    """Rows of one group: some without inner values that two parts hold, some with infinities, NaN or zeros only. The
+    other rows keep their bits."""
+    say(f"lora neighbours m={m} n={n} k={k} adapters={na} rank={r}")
+    c = lora_case(m + r, m, n, k, na, r)
+    x = c["x"].copy()
+    odd = np.arange(m) % 5 == 2
+    x[odd] = np.float16(0)
+    x[2::20, 0] = np.inf
+    x[7::20, 0] = np.nan
+    x[12::20, :] = np.float16(2.0 ** -24)
+    x[12::20, 1] = np.float16(60000)
+    c["a"][:, : r // 2, 1] = 0
+    d = {i: dev(v) for i, v in c.items()}
+    base = pbg.lora_add(**d)
+    out = pbg.lora_add(**{**d, "x": dev(x)})
+    keep = torch.from_numpy(~odd).to("cuda:0")
+    assert torch.equal(out[keep], base[keep])
+    with np.errstate(invalid="ignore"):
+        ref, bound = oracle.lora_add(**{**c, "x": x}), lora_bound({**c, "x": x})
+    out, ok = host(out).astype(np.float64), np.isfinite(ref)
+    assert np.array_equal(np.isnan(out), np.isnan(ref))
+    assert_within(out[ok], ref[ok], bound[ok], "odd rows")
