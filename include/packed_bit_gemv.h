@@ -430,8 +430,9 @@ int64_t pbg_q8_row_bytes(int64_t k);
  *   q_scale[i] = A * g_i / 127
  * Each code is the result of single fp32 operations (g_i cancels in it), so
  * codes are the same bits whatever the order of the sum. A row with A < 2^-100
- * has codes 0 and scale 0. A row that holds NaN or an infinity, or whose sum
- * of squares overflows fp32, has codes 0 and scale NaN.
+ * has codes 0 and scale 0. A row whose r or p holds NaN or an infinity, or
+ * whose sum of squares overflows fp32, has codes 0 and scale NaN; where it is r
+ * or the sum, all of its h is NaN.
  *
  *   x         [m][k] fp32, 4-byte aligned
  *   residual  [m][k] fp32, or NULL: r = x

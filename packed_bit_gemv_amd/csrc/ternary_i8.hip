@@ -626,7 +626,8 @@ bool launch_gemv_gate_up(const uint32_t* gate, const float* gate_scale, const ui
 
 // Streaming shapes up to 48 x 64, tiles from 32 x 128 on. The times of a round
 // are those of 128 to 256 workgroups at k = 4,096 on MI355X; at k = 12,288 all
-// grow alike (by 2.0 to 2.4). Where it picks a shape, that shape was within 5
+// grow alike (by 2.0 to 2.4); below 4,096, where the fixed part of a round
+// weighs more, they are not measured. Where it picks a shape, that shape was within 5
 // % of the fastest of 24 (m x n at k = 4,096, us against the runner-up of
 // another size): 8 x 4,096 4.2 / 5.0, 32 x 4,096 5.3 / 6.1, 64 x 4,096 6.6 /
 // 7.4, 100 x 4,096 8.2 / 8.7, 160 x 4,096 10.1 / 11.2, 64 x 12,288 11.5 /
