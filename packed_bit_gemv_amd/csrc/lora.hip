@@ -369,22 +369,18 @@ constexpr int up_waves(int rt, int c, bool join, bool fast) {
 // outputs of one row; an instruction takes 32 of the rank (16 up to rank 16),
 // hi and lo on one load of B_a. Outputs that come out infinite or NaN, as those
 // of a row marked by its factor do, are taken from the fp32 form, on v itself:
-// fp16 parts of an infinity, and a part of 0 against one in
-// B_a, would make NaN of it. Whether an output takes that form depends on its
-// own operands only. Bound by y and out, which a wave reads and writes in pieces of
-// 64 C bytes a row: the product goes through LDS to that order. JOIN: the
-// workgroup adds the slices of its groups' v itself. 1,531 rows at rank 64, n
-// = 12,288: 45 us, 3.4 TB/s of y and out (pieces of 64 bytes, straight from
-// the product's layout: 73 us).
+// fp16 parts of an infinity, and a part of 0 against one in B_a, would make NaN
+// of it. Whether an output takes that form depends on its own operands only.
+// Bound by y and out, which a wave reads and writes in pieces of 64 C bytes a
+// row: the product goes through LDS to that order. JOIN: the workgroup adds the
+// slices of its groups' v itself. 1,531 rows at rank 64, n = 12,288: 45 us, 3.4
+// TB/s of y and out (pieces of 64 bytes, straight from the product's layout: 73
+// us).
 template <int R, int RT, int C, bool JOIN, bool FAST>
-__global__ __launch_bounds__(kWaves* kWave, up_waves(RT, C, JOIN, FAST)) void lora_up_kernel(const float* y, const int32_t* __restrict__ ids,
-                                                                const int32_t* __restrict__ perm,
-                                                                const uint16_t* __restrict__ b,
-                                                                const float* __restrict__ scale, int64_t m, int64_t n,
-                                                                int adapters, int rank, int slices, int64_t n_blocks,
-                                                                const float* __restrict__ v,
-                                                                const _Float16* __restrict__ parts,
-                                                                const float* __restrict__ factors, float* out) {
+__global__ __launch_bounds__(kWaves* kWave, up_waves(RT, C, JOIN, FAST)) void lora_up_kernel(
+    const float* y, const int32_t* __restrict__ ids, const int32_t* __restrict__ perm, const uint16_t* __restrict__ b,
+    const float* __restrict__ scale, int64_t m, int64_t n, int adapters, int rank, int slices, int64_t n_blocks,
+    const float* __restrict__ v, const _Float16* __restrict__ parts, const float* __restrict__ factors, float* out) {
   constexpr int KT = RT > 1 ? RT / 2 : 1;  // loads of B_a per column tile
   constexpr int kPer = RT > 1 ? 8 : 4;     // of the rank in one of them
   constexpr int RP = 16 * RT;
