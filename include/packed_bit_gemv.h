@@ -522,6 +522,188 @@ int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16
              void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
+ * The attention half of a step: what stands between the q|k|v linear and the
+ * o linear, over a cache of keys and values that many requests share, and the
+ * step from the head's logits to the next token. One step holds m rows: the
+ * tokens that each request adds (one, a tree of drafted tokens, a prompt),
+ * request after request, request i's rows being row_start[i] ..
+ * row_start[i + 1] - 1.
+ * Source: Neutrino-1 8B model page, geometry table (32 query heads over 8 key
+ * and value heads of 128, rotary base 1e6 over the whole head, norms of each
+ * q and k head, fp16 cache, context 40,960) and "speculative" section (a
+ * drafted run is scored in one forward pass).
+ *
+ * The cache is made of pages of page_size tokens (a power of two, at most
+ * PBG_MAX_PAGE): k_cache and v_cache are fp16 [pages][kv_heads][page_size]
+ * [head_dim], 16-byte aligned, one pair of them for each layer. Request i's
+ * token t lies in page table[i][t / page_size] at t % page_size; a slot is
+ * page * page_size + t % page_size. A page number outside [0, pages) is no
+ * page: it is never read or written.
+ */
+#define PBG_MAX_REQUESTS 4096
+#define PBG_MAX_PAGE 4096
+#define PBG_MAX_TREE 64       /* rows of one request that a tree can have */
+#define PBG_MAX_HEAD_DIM 256
+#define PBG_MAX_HEADS 1024
+
+/*
+ * cache_plan - the tables of one step from the requests' lengths, in one
+ * launch: which pages the new tokens take, where each row's key and value go,
+ * and at which position each row stands. Shared by all layers.
+ *   lengths     [requests] int32: tokens in the cache before the step
+ *   added       [requests] int32: rows of the step. Negative values of either
+ *               count as 0; rows beyond the m-th are dropped.
+ *   table       [requests][table_width] int32, in and out: entries of pages
+ *               that the request holds (ceil(length / page_size)) are read,
+ *               those of pages that the step opens are written, no others
+ *   free_pages  [free_capacity] int32, free_count [1] int32: a stack of free
+ *               pages, of which the first free_count entries are free. The
+ *               j-th page that the step opens, in the order of the rows, is
+ *               free_pages[free_count - 1 - j].
+ *   parents     NULL: request i's rows continue it one after another. Or [m]
+ *               int32: the rows of each request form a tree, parents[a] being
+ *               the index inside the request (0 is its first row) of the row
+ *               that row a follows; a parent that does not come before its
+ *               row means that the row follows the cached tokens.
+ *   row_start   [requests + 1] int32 out
+ *   request     [m] int32 out: the row's request
+ *   position    [m] int32 out: the length plus the number of rows between the
+ *               cached tokens and the row
+ *   slot        [m] int64 out: row c of request i is its token lengths[i] + c;
+ *               -1 where its page is missing (the stack ran out, the table
+ *               ended, or it held no page)
+ *   ancestors   [m] uint64 out, or NULL: bit c is set for each row c < 64 of
+ *               the request that the row is or follows
+ *   free_left   [1] int32 out: what free_count is after the step; not the
+ *               address of free_count itself (PBG_ERR_VALUE)
+ * Rows behind the last request get request, position and slot -1 and no
+ * ancestors. So do, but for their request, the rows of a tree from the 64th
+ * on. Calling it again on the same inputs gives the same tables: nothing is
+ * taken from the stack until free_count is set to free_left.
+ * table_width * page_size and pages * page_size stay below 2^31 and 2^40.
+ */
+int cache_plan(const int32_t* lengths, const int32_t* added, int64_t requests, int32_t* table, int64_t table_width,
+               const int32_t* free_pages, int64_t free_capacity, const int32_t* free_count, int64_t pages,
+               int64_t page_size, const int32_t* parents, int64_t m, int32_t* row_start, int32_t* request,
+               int32_t* position, int64_t* slot, uint64_t* ancestors, int32_t* free_left, hipStream_t stream);
+
+/*
+ * rotary_qkv - from the q|k|v linear's output to queries and a written cache:
+ * norms of the q and k heads, rotary positions, one rounding to fp16.
+ *   u     = x_head * weight / sqrt(sum x_head^2 / head_dim + eps), or x_head
+ *           where there is no weight
+ *   (a, b) -> (a c - b s, b c + a s) for the pairs j < rotary_dim / 2, a and b
+ *           being u[j], u[j + rotary_dim / 2], or u[2j], u[2j + 1] where
+ *           interleaved is not 0; c and s are amplitude times the cosine and
+ *           the sine of position * inv_freq[j], the angle taken in 64 bits.
+ *           Elements from rotary_dim on are not turned.
+ *   qkv       [m][(heads + 2 kv_heads) head_dim] fp32, 4-byte aligned
+ *   position  [m] int32: rows with a negative position are left out, nothing
+ *             of theirs is written
+ *   slot      [m] int64: where k and v go; outside [0, pages * page_size) they
+ *             are not written. Rows of one slot: one of them is kept, which is
+ *             not specified.
+ *   inv_freq  [rotary_dim / 2] fp64, 8-byte aligned; NULL exactly if rotary_dim
+ *             is 0. Scaling for long contexts is in these and in amplitude.
+ *   q_weight, k_weight  [head_dim] fp32, or NULL
+ *   eps       > 0, finite (read where there is a weight)
+ *   amplitude finite
+ *   heads, kv_heads  heads a multiple of kv_heads, at most PBG_MAX_HEADS, and
+ *             m * (heads + 2 kv_heads) at most 2^26
+ *   head_dim, rotary_dim  multiples of 8, rotary_dim <= head_dim <=
+ *             PBG_MAX_HEAD_DIM
+ *   q         [m][heads][head_dim] fp16 out, 16-byte aligned
+ *   k_cache, v_cache  see above
+ */
+int rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, const double* inv_freq,
+               const float* q_weight, const float* k_weight, float eps, float amplitude, int interleaved, int64_t m,
+               int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t rotary_dim, uint16_t* q, uint16_t* k_cache,
+               uint16_t* v_cache, int64_t pages, int64_t page_size, hipStream_t stream);
+
+/*
+ * tree_attention - each row's attention over its request's tokens:
+ *   out[a][e] = sum_t w_t v_t / sum_t w_t, w_t = exp(scale * q[a][e] . k_t)
+ * with k and v of key head e / (heads / kv_heads), over the tokens t that row
+ * a = row_start[i] + c sees: t < lengths[i], and of the rows of its own step
+ * the tokens lengths[i] + c' for which bit c' of ancestors[a] is set, or,
+ * where ancestors is NULL, those with c' <= c. One decoded token, a tree of
+ * drafted tokens and a prompt's rows are all calls of this one, and may stand
+ * side by side in one. Tokens in a place without a page are not seen. A row
+ * whose weights add to zero (it sees nothing, or only scores of -infinity) is
+ * all zeros. What the cache holds in places that a row does not see (NaN
+ * included) does not reach it.
+ *   q          [m][heads][head_dim] fp16 bits, 16-byte aligned
+ *   k_cache, v_cache, table  see above; the step's own keys and values are
+ *              already in them (rotary_qkv)
+ *   lengths    [requests] int32, as for cache_plan
+ *   row_start  [requests + 1] int32, as from cache_plan. Rows behind the last
+ *              request are left as they were.
+ *   ancestors  [m] uint64, or NULL; of a request's rows from the 64th on none
+ *              is seen
+ *   scale      > 0, and finite also times log2(e)
+ *   out        [m][heads][head_dim] fp16 bits out, 16-byte aligned
+ *   workspace  device, 16-byte aligned, pbg_attention_workspace_bytes(...)
+ *              bytes, of any content; one serves any number of rows and
+ *              requests and fewer heads, and calls of many graphs that do not overlap
+ *              in time
+ * Heads and head_dim as for rotary_qkv. Scores, weights' sums and the output's sums are fp32; the weights enter the
+ * second product rounded to fp16 relative to the row's largest.
+ */
+int64_t pbg_attention_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t head_dim);
+
+int tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages,
+                   int64_t page_size, const int32_t* table, int64_t table_width, const int32_t* lengths,
+                   const int32_t* row_start, int64_t requests, const uint64_t* ancestors, int64_t m, int64_t heads,
+                   int64_t kv_heads, int64_t head_dim, float scale, uint16_t* out, void* workspace,
+                   int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * penalize_logits - what a request's settings do to the head's logits before
+ * its next token is picked, in fp32, one IEEE operation after the other, so
+ * that every result is the same bits in any implementation:
+ *   x = x > 0 ? x / repetition[i] : x * repetition[i]   tokens of the prompt,
+ *                                                       the output or the drafts
+ *   x = (x - frequency[i] * count) - presence[i]        tokens that the output
+ *                                                       and the drafts hold count > 0 times
+ *   x = x + bias                                        tokens of the bias list
+ *   x = -infinity                                       tokens whose grammar bit is 0
+ * for row a of request i = request[a].
+ *   logits     [m][n] fp32, 4-byte aligned
+ *   request    [m] int32; rows with a request outside [0, requests) are left as
+ *              they were in every output
+ *   tokens     [requests][tokens_width] int32: prompt, then output; length and
+ *              prompt_length [requests] int32 say how many of both and how many
+ *              of the prompt. Tokens outside [0, n) are passed over.
+ *   repetition, frequency, presence  [requests] fp32
+ *   drafts, row_start, ancestors  all NULL, or the drafted token of each row [m]
+ *              int32 and the tables of cache_plan: the tokens of a row's
+ *              ancestors (itself among them) count as output
+ *   bias_start [requests + 1] int32, bias_token, bias_value [bias_entries]:
+ *              request i's list is entries bias_start[i] .. bias_start[i + 1] - 1;
+ *              of a token listed twice the last entry counts. All NULL for none.
+ *   grammar    [states][ceil(n / 32)] uint32, bit v % 32 of word v / 32 set for
+ *              allowed tokens, grammar_row [m] int32 (outside [0, states): the
+ *              row has none). Both NULL for none.
+ *   out        [m][n] fp32 out; may be logits itself
+ *   token, top [m] int32 and [m] fp32 out, both NULL if not wanted: the greedy
+ *              token (the lowest on ties) and its value; -1 and -infinity where
+ *              no value is above -infinity. NaN is never chosen.
+ *   workspace  [m][ceil(n / PBG_LOGITS_SLICE)] uint64, 8-byte aligned, of any
+ *              content; read only if token is wanted
+ * m * n is at most PBG_MAX_LOGITS, tokens_width at most 2^24.
+ */
+#define PBG_LOGITS_SLICE 1024
+#define PBG_MAX_LOGITS (1LL << 32)
+
+int penalize_logits(const float* logits, const int32_t* request, const int32_t* tokens, int64_t tokens_width,
+                    const int32_t* prompt_length, const int32_t* length, const float* repetition,
+                    const float* frequency, const float* presence, int64_t requests, const int32_t* drafts,
+                    const int32_t* row_start, const uint64_t* ancestors, const int32_t* bias_start,
+                    const int32_t* bias_token, const float* bias_value, int64_t bias_entries, const uint32_t* grammar,
+                    const int32_t* grammar_row, int64_t states, int64_t m, int64_t n, float* out, int32_t* token,
+                    float* top, uint64_t* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
  * pbg_stream_read - measurement helper, not a step of the decode path: reads
  * `bytes` of device memory once with the loads the GEMV kernels use (16-byte
  * non-temporal loads, 1 KiB of consecutive bytes per wave-wide load, up to

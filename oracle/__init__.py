@@ -485,3 +485,172 @@ def lora_add(y: np.ndarray, x: np.ndarray, ids: np.ndarray, a: np.ndarray, b: np
             v = a[t].astype(np.float64) @ x[i].astype(np.float64)
             out[i] += float(scale[t]) * (b[t].astype(np.float64) @ v)
     return out
+
+
+# ---- the attention half of a step ------------------------------------------
+
+TREE_ROWS = 64
+
+
+def tree_path(parents: np.ndarray, c: int) -> list[int]:
+    """Rows of a request's tree from row c up to the cached tokens (c itself first)."""
+    path = [c]
+    while 0 <= parents[path[-1]] < path[-1]:
+        path.append(int(parents[path[-1]]))
+    return path
+
+
+def cache_plan(lengths, added, table, free_pages, free_count, page_size, pages, m, parents=None):
+    """Tables of one step: (row_start, request, position, slot, ancestors, free_left, table), row by row.
+
+    Every page is opened by the row that stands first in it and taken from the end of the stack.
+    """
+    table = table.copy()
+    width = table.shape[1]
+    row_start, request, position = [0], np.full(m, -1, np.int32), np.full(m, -1, np.int32)
+    slot, ancestors = np.full(m, -1, np.int64), np.zeros(m, np.uint64)
+    left = min(max(int(free_count), 0), len(free_pages))
+    for i, (have, more) in enumerate(zip(lengths, added)):
+        have, first = max(int(have), 0), row_start[-1]
+        for c in range(min(max(int(more), 0), m - first)):
+            a, t = first + c, have + c
+            page = -1
+            if t // page_size < width:
+                if t % page_size == 0:
+                    page = int(free_pages[left - 1]) if left > 0 else -1
+                    left = max(left - 1, 0)
+                    table[i, t // page_size] = page if 0 <= page < pages else -1
+                page = int(table[i, t // page_size])
+            request[a] = i
+            if parents is None:
+                position[a] = min(have + c, 2 ** 31 - 1)
+                ancestors[a] = np.uint64((1 << min(c + 1, 64)) - 1)
+            elif c < TREE_ROWS:
+                path = tree_path(parents[first: first + c + 1], c)
+                position[a] = min(have + len(path) - 1, 2 ** 31 - 1)
+                ancestors[a] = np.uint64(sum(1 << p for p in path))
+            else:
+                continue
+            if 0 <= page < pages:
+                slot[a] = page * page_size + t % page_size
+        row_start.append(first + min(max(int(more), 0), m - first))
+    return np.array(row_start, np.int32), request, position, slot, ancestors, left, table
+
+
+def rotary_qkv(qkv, position, inv_freq, heads, kv_heads, head_dim, q_weight=None, k_weight=None, eps=1e-6, amplitude=1.0,
+               interleaved=False):
+    """(q, k, v) in fp64 [m, heads or kv_heads, head_dim]: normed, turned, not rounded (Neutrino-1 8B model page, geometry
+    table: rotary positions, norms of q and k heads)."""
+    m = qkv.shape[0]
+    x = qkv.astype(np.float64).reshape(m, heads + 2 * kv_heads, head_dim)
+    parts = [x[:, :heads], x[:, heads: heads + kv_heads], x[:, heads + kv_heads:]]
+    half = 0 if inv_freq is None else len(inv_freq)
+    for n, weight in enumerate((q_weight, k_weight)):
+        y = parts[n].copy()
+        if weight is not None:
+            y = y / np.sqrt(np.square(y).mean(axis=-1, keepdims=True) + eps) * weight.astype(np.float64)
+        turned = y.copy()
+        for j in range(half):
+            a, b = (2 * j, 2 * j + 1) if interleaved else (j, j + half)
+            angle = position.astype(np.float64) * float(inv_freq[j])
+            cos, sin = (amplitude * np.cos(angle))[:, None], (amplitude * np.sin(angle))[:, None]
+            turned[..., a] = y[..., a] * cos - y[..., b] * sin
+            turned[..., b] = y[..., b] * cos + y[..., a] * sin
+        parts[n] = turned
+    return tuple(parts)
+
+
+def cached_tokens(cache, table_row, count, head):
+    """Keys or values [count, head_dim] of one request and head, and which of them are in a page."""
+    pages, _, page_size, d = cache.shape
+    out, held = np.zeros((count, d), cache.dtype), np.zeros(count, bool)
+    for t in range(0, count, page_size):
+        number = int(table_row[t // page_size]) if t // page_size < len(table_row) else -1
+        if 0 <= number < pages:
+            n = min(page_size, count - t)
+            out[t: t + n], held[t: t + n] = cache[number, head, :n], True
+    return out, held
+
+
+def tree_attention(q, k_cache, v_cache, table, lengths, row_start, ancestors=None, scale=None):
+    """(out, size, far) fp64: out[a, e] = sum_t w_t v_t / sum_t w_t over the tokens that row a sees; size the same sum of
+    magnitudes |v_t|, far the largest sum_j |q_j k_j| of a token seen. Rows of no request are NaN."""
+    m, heads, d = q.shape
+    kv_heads = k_cache.shape[1]
+    scale = d ** -0.5 if scale is None else scale
+    out = np.full(q.shape, np.nan)
+    size, far = np.zeros(q.shape), np.zeros((m, heads))
+    for i in range(len(lengths)):
+        have, first, last = max(int(lengths[i]), 0), int(row_start[i]), int(row_start[i + 1])
+        count = min(have + last - first, table.shape[1] * k_cache.shape[2])
+        for g in range(kv_heads if last > first else 0):
+            k, held = cached_tokens(k_cache, table[i], count, g)
+            v, _ = cached_tokens(v_cache, table[i], count, g)
+            for a in range(first, last):
+                c = np.arange(count) - have
+                if ancestors is None:
+                    sees = c <= a - first
+                else:
+                    bits = int(ancestors[a])
+                    sees = np.array([n < 0 or (n < TREE_ROWS and bits >> int(n) & 1 == 1) for n in c], bool)
+                sees &= held
+                kk, vv = k[sees].astype(np.float64), v[sees].astype(np.float64)
+                for e in range(g * (heads // kv_heads), (g + 1) * (heads // kv_heads)):
+                    if not len(kk):
+                        out[a, e] = 0.0
+                        continue
+                    qq = q[a, e].astype(np.float64)
+                    with np.errstate(invalid="ignore", over="ignore"):
+                        s = kk @ qq * float(np.float32(scale))
+                        top = s.max()
+                        w = np.exp(s - (top if np.isfinite(top) else 0.0))
+                        total = w.sum()
+                        out[a, e] = 0.0 if total == 0 else w @ vv / total
+                        size[a, e] = 0.0 if total == 0 else w @ np.abs(vv) / total
+                        far[a, e] = (np.abs(kk) @ np.abs(qq)).max()
+    return out, size, far
+
+
+def penalize_logits(logits, request, tokens, prompt_length, length, repetition, frequency, presence, drafts=None, row_start=None,
+                    ancestors=None, bias_start=None, bias_token=None, bias_value=None, grammar=None, grammar_row=None):
+    """(out fp32, token, top): every step one fp32 operation. Rows without a request come back as NaN, token -2."""
+    m, n = logits.shape
+    f = np.float32
+    out, token, top = np.full((m, n), f(np.nan)), np.full(m, -2, np.int32), np.full(m, f(np.nan))
+    for a in range(m):
+        i = int(request[a])
+        if not 0 <= i < len(length):
+            continue
+        used = min(max(int(length[i]), 0), tokens.shape[1])
+        said, before = tokens[i, :used].astype(np.int64), min(max(int(prompt_length[i]), 0), used)
+        drafted = []
+        if drafts is not None:
+            rows = [int(row_start[i]) + c for c in range(TREE_ROWS) if int(ancestors[a]) >> c & 1]
+            drafted = [int(drafts[r]) for r in rows if 0 <= r < m]
+        output = np.array(list(said[before:]) + drafted, np.int64)
+        output = output[(output >= 0) & (output < n)]
+        count = np.bincount(output, minlength=n)
+        any_of = count > 0
+        given = said[:before]
+        any_of[given[(given >= 0) & (given < n)]] = True
+        x = logits[a].copy()
+        with np.errstate(all="ignore"):
+            x = np.where(any_of, np.where(x > 0, x / f(repetition[i]), x * f(repetition[i])), x)
+            x = np.where(count > 0, (x - f(frequency[i]) * count.astype(f)) - f(presence[i]), x)
+            if bias_start is not None:
+                last = {}
+                for j in range(max(int(bias_start[i]), 0), min(int(bias_start[i + 1]), len(bias_token))):
+                    last[int(bias_token[j])] = f(bias_value[j])
+                for v, b in last.items():
+                    if 0 <= v < n:
+                        x[v] = x[v] + b
+        if grammar is not None and 0 <= int(grammar_row[a]) < len(grammar):
+            words = grammar[int(grammar_row[a])].astype(np.uint32)
+            bits = (words[:, None] >> np.arange(32, dtype=np.uint32) & 1).reshape(-1)[:n]
+            x[bits == 0] = -np.inf
+        assert x.dtype == f
+        out[a] = x
+        known = np.where(np.isnan(x), -np.inf, x)
+        token[a] = int(known.argmax()) if known.max() > -np.inf else -1
+        top[a] = known.max()
+    return out, token, top

@@ -8,6 +8,7 @@ computation happens in the library's HIP kernels; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -19,6 +20,7 @@ PBG_ERR_CODE = -4
 ARGMAX_KEYS_PER_ROW = 4096  # PBG_ARGMAX_KEYS_PER_ROW
 MAX_M = 8  # PBG_MAX_M
 STREAM_READ_SINK_WORDS = 8192  # PBG_STREAM_READ_SINK_WORDS
+LOGITS_SLICE = 1024  # PBG_LOGITS_SLICE
 
 _c_int = ctypes.c_int
 _c_i64 = ctypes.c_int64
@@ -60,6 +62,15 @@ _SIGNATURES = {
     "pbg_lora_workspace_bytes": (_c_i64, [_c_i64, _c_i64]),
     "lora_add": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i64,
                           _vp]),
+    "cache_plan": (_c_int, [_vp, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _vp,
+                            _vp, _vp, _vp, _vp]),
+    "rotary_qkv": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _c_int, _c_i64, _c_i64, _c_i64,
+                            _c_i64, _c_i64, _vp, _vp, _vp, _c_i64, _c_i64, _vp]),
+    "pbg_attention_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+    "tree_attention": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _c_i64, _vp, _c_i64, _c_i64,
+                                _c_i64, _c_i64, ctypes.c_float, _vp, _vp, _c_i64, _vp]),
+    "penalize_logits": (_c_int, [_vp, _vp, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _c_i64, _vp]),
     "pbg_stream_read": (_c_int, [_vp, _c_i64, _vp, _vp]),
 }
 
@@ -684,6 +695,233 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, ids: torch.Tensor, a: torch.Tenso
           m, n, k, adapters, rank, _on(dev, out, "out", torch.float32, (m, n)), workspace.data_ptr(),
           workspace.nbytes)
     return out
+
+
+def _given(index: int, t, name: str, dtype: torch.dtype, shape: tuple):
+    """Address of t as _on has it, or None for None."""
+    return None if t is None else _on(index, t, name, dtype, shape)
+
+
+def _masks(index: int, t, name: str, m: int):
+    """Address of an int64 or uint64 [m] tensor of bit masks, or None."""
+    return _given(index, t, name, t.dtype if t is not None and t.dtype is torch.uint64 else torch.int64, (m,))
+
+
+def _cache(k_cache, v_cache):
+    """Pages, key heads, page size, head width and device index of a pair of caches."""
+    try:
+        pages, kv_heads, page_size, head_dim = k_cache.shape
+        fine = k_cache.dtype is torch.float16 and k_cache.is_cuda and k_cache.is_contiguous()
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _dev(k_cache, "k_cache", torch.float16)
+        raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim]")
+    dev = k_cache.get_device()
+    _on(dev, v_cache, "v_cache", torch.float16, k_cache.shape)
+    return pages, kv_heads, page_size, head_dim, dev
+
+
+def cache_plan(lengths: torch.Tensor, added: torch.Tensor, table: torch.Tensor, free_pages: torch.Tensor,
+               free_count: torch.Tensor, page_size: int, pages: int, row_start: torch.Tensor | None = None,
+               request: torch.Tensor | None = None, position: torch.Tensor | None = None,
+               slot: torch.Tensor | None = None, free_left: torch.Tensor | None = None,
+               parents: torch.Tensor | None = None, ancestors: torch.Tensor | None = None, rows: int | None = None):
+    """The tables of one step over the paged cache: (row_start, request, position, slot, ancestors, free_left).
+
+    lengths, added int32 [requests]: the tokens that each request has in the cache and the rows that it adds. table
+    int32 [requests, width] is read and, for pages that the step opens, written; free_pages int32 [n] is a stack of
+    free pages with free_count int32 [1] of them left, free_left int32 [1] what the step leaves. parents int32 [rows]
+    makes each request's rows a tree of drafted tokens (of at most 64). The step has as many rows as the outputs that are given, or
+    `rows`: request, position int32 [rows], slot int64 [rows] (-1 for rows behind the last request), row_start int32
+    [requests + 1], ancestors int64 [rows] (bit masks over the request's rows; allocated for a tree).
+    """
+    i32, i64 = torch.int32, torch.int64
+    requests, width, dev = _matrix(table, "table", i32)
+    try:
+        m = request.numel() if request is not None else int(rows)
+        capacity = free_pages.numel()
+    except (AttributeError, TypeError):
+        raise ValueError("free_pages must be a tensor, and rows (or the outputs) must be given") from None
+    if row_start is None:
+        row_start = torch.empty((requests + 1,), dtype=i32, device=dev)
+    if request is None:
+        request = torch.empty((m,), dtype=i32, device=dev)
+    if position is None:
+        position = torch.empty((m,), dtype=i32, device=dev)
+    if slot is None:
+        slot = torch.empty((m,), dtype=i64, device=dev)
+    if free_left is None:
+        free_left = torch.empty((1,), dtype=i32, device=dev)
+    if ancestors is None and parents is not None:
+        ancestors = torch.empty((m,), dtype=i64, device=dev)
+    _call("cache_plan", lib().cache_plan, dev, _on(dev, lengths, "lengths", i32, (requests,)),
+          _on(dev, added, "added", i32, (requests,)), requests, table.data_ptr(), width,
+          _on(dev, free_pages, "free_pages", i32, (capacity,)), capacity,
+          _on(dev, free_count, "free_count", i32, (1,)), pages, page_size, _given(dev, parents, "parents", i32, (m,)), m,
+          _on(dev, row_start, "row_start", i32, (requests + 1,)), _on(dev, request, "request", i32, (m,)),
+          _on(dev, position, "position", i32, (m,)), _on(dev, slot, "slot", i64, (m,)),
+          _masks(dev, ancestors, "ancestors", m), _on(dev, free_left, "free_left", i32, (1,)))
+    return row_start, request, position, slot, ancestors, free_left
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 1e6, scaling: str | None = None, factor: float = 1.0,
+                       original_length: int = 32768, device="cuda"):
+    """(inv_freq fp64 [rotary_dim / 2], amplitude) of rotary_qkv: base ** (-2 j / rotary_dim), scaled for contexts `factor` times as long.
+
+    scaling: None; "linear", positions divided by the factor; "ntk", the base raised so that the slowest pair turns
+    factor times slower and the fastest is kept; "yarn", pairs that turn more than 32 times over original_length tokens kept, those
+    that turn less than once divided by the factor, a ramp over the pair's number in between, and an amplitude of 1 + 0.1 ln(factor).
+    """
+    if rotary_dim < 0 or rotary_dim % 2 or not factor >= 1.0:
+        raise ValueError("rotary_dim must be even and factor at least 1")
+    half = rotary_dim // 2
+    amplitude = 1.0
+    if scaling == "ntk" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    freq = [base ** (-2.0 * j / rotary_dim) for j in range(half)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        # number of the pair that turns r times over the original length
+        def pair(r):
+            return rotary_dim * math.log(original_length / (r * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        low, high = max(math.floor(pair(32.0)), 0), min(math.ceil(pair(1.0)), rotary_dim - 1)
+        ramp = [min(max((j - low) / max(high - low, 0.001), 0.0), 1.0) for j in range(half)]
+        freq = [f / factor * r + f * (1.0 - r) for f, r in zip(freq, ramp)]
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError('scaling must be None, "linear", "ntk" or "yarn"')
+    return torch.tensor(freq, dtype=torch.float64, device=device), amplitude
+
+
+def rotary_qkv(qkv: torch.Tensor, position: torch.Tensor, slot: torch.Tensor, inv_freq: torch.Tensor | None,
+               k_cache: torch.Tensor, v_cache: torch.Tensor, q_weight: torch.Tensor | None = None,
+               k_weight: torch.Tensor | None = None, eps: float = 1e-6, amplitude: float = 1.0,
+               interleaved: bool = False, q: torch.Tensor | None = None) -> torch.Tensor:
+    """Queries fp16 [m, heads, head_dim] of a q|k|v linear's output, with its keys and values written into the cache.
+
+    qkv fp32 [m, (heads + 2 kv_heads) * head_dim]; position int32 [m] and slot int64 [m] from cache_plan; inv_freq
+    fp64 [rotary_dim / 2] and amplitude from rotary_frequencies (None: nothing is turned); k_cache, v_cache fp16
+    [pages, kv_heads, page_size, head_dim]; q_weight, k_weight fp32 [head_dim] norm each q and k head. Rows with a
+    negative position are left out.
+    """
+    pages, kv_heads, page_size, head_dim, dev = _cache(k_cache, v_cache)
+    m, columns, _ = _matrix(qkv, "qkv", torch.float32)
+    heads = columns // head_dim - 2 * kv_heads if head_dim else 0
+    if heads < 1 or columns != (heads + 2 * kv_heads) * head_dim:
+        raise ValueError(f"qkv must be [m, (heads + 2 * {kv_heads}) * {head_dim}]")
+    if q is None:
+        q = torch.empty((m, heads, head_dim), dtype=torch.float16, device=qkv.device)
+    half = 0 if inv_freq is None else inv_freq.numel()
+    _call("rotary_qkv", lib().rotary_qkv, dev, _on(dev, qkv, "qkv", torch.float32, (m, columns)),
+          _on(dev, position, "position", torch.int32, (m,)), _on(dev, slot, "slot", torch.int64, (m,)),
+          _on(dev, inv_freq, "inv_freq", torch.float64, (half,)) if half else None,
+          _given(dev, q_weight, "q_weight", torch.float32, (head_dim,)),
+          _given(dev, k_weight, "k_weight", torch.float32, (head_dim,)), eps, amplitude, int(interleaved), m, heads,
+          kv_heads, head_dim, 2 * half, _on(dev, q, "q", torch.float16, (m, heads, head_dim)), k_cache.data_ptr(),
+          v_cache.data_ptr(), pages, page_size)
+    return q
+
+
+def attention_workspace(heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
+    """A workspace for tree_attention with heads of these shapes, any number of rows (its contents do not matter)."""
+    size = int(lib().pbg_attention_workspace_bytes(int(heads), int(kv_heads), int(head_dim)))
+    return torch.empty((size,), dtype=torch.uint8, device=device)
+
+
+def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                   lengths: torch.Tensor, row_start: torch.Tensor, ancestors: torch.Tensor | None = None,
+                   scale: float | None = None, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of a step's rows over the paged cache: out fp16 [m, heads, head_dim].
+
+    q as rotary_qkv leaves it; k_cache, v_cache fp16 [pages, kv_heads, page_size, head_dim], which hold the step's own
+    keys and values already; table int32 [requests, width]; lengths int32 [requests], the tokens before the step;
+    row_start int32 [requests + 1] and ancestors int64 [m] from cache_plan. Each row sees its request's tokens from before the
+    step, and of the step's own those of its ancestors, or without ancestors those up to itself. scale defaults
+    to 1 / sqrt(head_dim). A row that sees nothing is zero; rows behind the last request are left as they were.
+    """
+    pages, kv_heads, page_size, head_dim, dev = _cache(k_cache, v_cache)
+    try:
+        m, heads, d = q.shape
+        requests, width = table.shape
+    except (AttributeError, ValueError):
+        raise ValueError("q must be [m, heads, head_dim] and table [requests, width]") from None
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = attention_workspace(heads, kv_heads, head_dim, q.device)
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
+    _call("tree_attention", lib().tree_attention, dev, _on(dev, q, "q", torch.float16, (m, heads, head_dim)),
+          k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
+          _on(dev, table, "table", torch.int32, (requests, width)), width,
+          _on(dev, lengths, "lengths", torch.int32, (requests,)),
+          _on(dev, row_start, "row_start", torch.int32, (requests + 1,)), requests,
+          _masks(dev, ancestors, "ancestors", m), m, heads, kv_heads, head_dim,
+          head_dim ** -0.5 if scale is None else scale, _on(dev, out, "out", torch.float16, (m, heads, head_dim)),
+          workspace.data_ptr(), workspace.nbytes)
+    return out
+
+
+def logits_workspace(m: int, n: int, device) -> torch.Tensor:
+    """A workspace for the greedy token of penalize_logits on [m, n] logits (its contents do not matter)."""
+    return torch.empty((int(m) * ((int(n) + LOGITS_SLICE - 1) // LOGITS_SLICE),), dtype=torch.int64, device=device)
+
+
+def penalize_logits(logits: torch.Tensor, request: torch.Tensor, tokens: torch.Tensor, prompt_length: torch.Tensor,
+                    length: torch.Tensor, repetition: torch.Tensor, frequency: torch.Tensor, presence: torch.Tensor,
+                    drafts: torch.Tensor | None = None, row_start: torch.Tensor | None = None,
+                    ancestors: torch.Tensor | None = None, bias_start: torch.Tensor | None = None,
+                    bias_token: torch.Tensor | None = None, bias_value: torch.Tensor | None = None,
+                    grammar: torch.Tensor | None = None, grammar_row: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, token: torch.Tensor | None = None,
+                    top: torch.Tensor | None = None, workspace: torch.Tensor | None = None, greedy: bool = False):
+    """Logits fp32 [m, n] under their requests' settings: (out, token, top).
+
+    request int32 [m]; tokens int32 [requests, width] with length and prompt_length int32 [requests] (all, and those of
+    the prompt); repetition, frequency, presence fp32 [requests]. drafts int32 [m], row_start and ancestors (cache_plan)
+    add each row's drafted tokens to its output. bias_start int32 [requests + 1], bias_token int32 and bias_value fp32
+    [entries] list biases; grammar int32 [states, ceil(n / 32)] holds bit masks of allowed tokens, grammar_row int32 [m]
+    each row's state (-1: none). out may be logits itself. With greedy=True or token and top given, token int32 [m]
+    and top fp32 [m] are the best token and its value (-1 and -infinity where nothing is allowed).
+    """
+    m, n, dev = _matrix(logits, "logits", torch.float32)
+    i32, f32 = torch.int32, torch.float32
+    try:
+        requests, width = tokens.shape
+    except (AttributeError, ValueError):
+        raise ValueError("tokens must be [requests, width]") from None
+    if out is None:
+        out = torch.empty_like(logits)
+    if greedy or token is not None or top is not None:
+        if token is None:
+            token = torch.empty((m,), dtype=i32, device=logits.device)
+        if top is None:
+            top = torch.empty((m,), dtype=f32, device=logits.device)
+        if workspace is None:
+            workspace = logits_workspace(m, n, logits.device)
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
+    entries = 0 if bias_token is None else bias_token.numel()
+    if bias_token is not None and entries == 0:
+        bias_start = bias_token = bias_value = None
+    states = 0 if grammar is None else grammar.shape[0]
+    _call("penalize_logits", lib().penalize_logits, dev, logits.data_ptr(), _on(dev, request, "request", i32, (m,)),
+          _on(dev, tokens, "tokens", i32, (requests, width)), width,
+          _on(dev, prompt_length, "prompt_length", i32, (requests,)), _on(dev, length, "length", i32, (requests,)),
+          _on(dev, repetition, "repetition", f32, (requests,)), _on(dev, frequency, "frequency", f32, (requests,)),
+          _on(dev, presence, "presence", f32, (requests,)), requests, _given(dev, drafts, "drafts", i32, (m,)),
+          _given(dev, row_start, "row_start", i32, (requests + 1,)), _masks(dev, ancestors, "ancestors", m),
+          _given(dev, bias_start, "bias_start", i32, (requests + 1,)), _given(dev, bias_token, "bias_token", i32, (entries,)),
+          _given(dev, bias_value, "bias_value", f32, (entries,)), entries,
+          _given(dev, grammar, "grammar", i32, (states, (n + 31) // 32)),
+          _given(dev, grammar_row, "grammar_row", i32, (m,)), states, m, n, _on(dev, out, "out", f32, (m, n)),
+          _given(dev, token, "token", i32, (m,)), _given(dev, top, "top", f32, (m,)),
+          None if token is None else workspace.data_ptr(), 0 if token is None else workspace.nbytes)
+    return out, token, top
 
 
 def stream_read(src: torch.Tensor, sink: torch.Tensor | None = None) -> torch.Tensor:

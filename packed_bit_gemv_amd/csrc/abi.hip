@@ -20,6 +20,22 @@ bool bad_rows(int64_t m, int64_t k) { return m < 1 || m > PBG_MAX_ROWS || k < 1 
 
 bool bad_outputs(int64_t m, int64_t n) { return n < 1 || n > PBG_MAX_N || m * n > PBG_MAX_OUTPUTS; }
 
+// The paged cache and the requests of a step.
+bool bad_pages(int64_t pages, int64_t page_size) {
+  return page_size < 1 || page_size > PBG_MAX_PAGE || (page_size & (page_size - 1)) != 0 || pages < 1 ||
+         pages > 0x7FFFFFFFLL || pages * page_size >= 1LL << 40;
+}
+
+bool bad_table(int64_t requests, int64_t table_width, int64_t page_size) {
+  return requests < 1 || requests > PBG_MAX_REQUESTS || table_width < 1 || table_width > 0x7FFFFFFFLL / page_size;
+}
+
+// Heads of a step's m rows; the elements of a key head's page stay below 2^31.
+bool bad_heads(int64_t m, int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  return m < 1 || m > PBG_MAX_ROWS || heads < 1 || heads > PBG_MAX_HEADS || kv_heads < 1 || heads % kv_heads != 0 ||
+         head_dim < 8 || head_dim > PBG_MAX_HEAD_DIM || head_dim % 8 != 0 || m * (heads + 2 * kv_heads) > 1LL << 26;
+}
+
 // True when earlier work on this thread left a HIP error pending. Such an
 // error is the caller's: it is left in place (not cleared) and the call
 // enqueues nothing. hipErrorNotReady from a completion query is a status,
@@ -371,6 +387,108 @@ int ternary3_ffn_swiglu_small(const uint32_t* gate_packed, const float* gate_sca
   if (pending_error()) return PBG_ERR_HIP;
   return finish(pbg::launch_ffn3_swiglu_small(gate_packed, gate_scale, up_packed, up_scale, down_packed, down_scale,
                                               d_model, d_ff, x, static_cast<int>(m), h, y, stream));
+}
+
+int cache_plan(const int32_t* lengths, const int32_t* added, int64_t requests, int32_t* table, int64_t table_width,
+               const int32_t* free_pages, int64_t free_capacity, const int32_t* free_count, int64_t pages,
+               int64_t page_size, const int32_t* parents, int64_t m, int32_t* row_start, int32_t* request,
+               int32_t* position, int64_t* slot, uint64_t* ancestors, int32_t* free_left, hipStream_t stream) {
+  if (!lengths || !added || !table || !free_pages || !free_count || !row_start || !request || !position || !slot ||
+      !free_left)
+    return PBG_ERR_NULL;
+  if (m < 1 || m > PBG_MAX_ROWS || bad_pages(pages, page_size) || bad_table(requests, table_width, page_size) ||
+      free_capacity < 1 || free_capacity > 0x7FFFFFFFLL)
+    return PBG_ERR_SHAPE;
+  if (misaligned(lengths, 4) || misaligned(added, 4) || misaligned(table, 4) || misaligned(free_pages, 4) ||
+      misaligned(free_count, 4) || misaligned(parents, 4) || misaligned(row_start, 4) || misaligned(request, 4) ||
+      misaligned(position, 4) || misaligned(slot, 8) || misaligned(ancestors, 8) || misaligned(free_left, 4))
+    return PBG_ERR_ALIGN;
+  if (free_left == free_count) return PBG_ERR_VALUE;
+  if (pending_error()) return PBG_ERR_HIP;
+  return finish(pbg::launch_cache_plan(lengths, added, requests, table, table_width, free_pages, free_capacity,
+                                       free_count, pages, page_size, parents, m, row_start, request, position, slot,
+                                       ancestors, free_left, stream));
+}
+
+int rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, const double* inv_freq,
+               const float* q_weight, const float* k_weight, float eps, float amplitude, int interleaved, int64_t m,
+               int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t rotary_dim, uint16_t* q, uint16_t* k_cache,
+               uint16_t* v_cache, int64_t pages, int64_t page_size, hipStream_t stream) {
+  if (!qkv || !position || !slot || !q || !k_cache || !v_cache) return PBG_ERR_NULL;
+  if (bad_heads(m, heads, kv_heads, head_dim) || rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 8 != 0 ||
+      bad_pages(pages, page_size))
+    return PBG_ERR_SHAPE;
+  if ((inv_freq == nullptr) != (rotary_dim == 0)) return PBG_ERR_NULL;
+  if (misaligned(qkv, 4) || misaligned(position, 4) || misaligned(slot, 8) || misaligned(inv_freq, 8) ||
+      misaligned(q_weight, 4) || misaligned(k_weight, 4) || misaligned(q, 16) || misaligned(k_cache, 16) ||
+      misaligned(v_cache, 16))
+    return PBG_ERR_ALIGN;
+  if (!(eps > 0.0f) || !(eps < __builtin_inff()) || !(amplitude > -__builtin_inff()) || !(amplitude < __builtin_inff()))
+    return PBG_ERR_VALUE;
+  if (pending_error()) return PBG_ERR_HIP;
+  return finish(pbg::launch_rotary_qkv(qkv, position, slot, inv_freq, q_weight, k_weight, eps, amplitude,
+                                       interleaved != 0, m, static_cast<int>(heads), static_cast<int>(kv_heads),
+                                       static_cast<int>(head_dim), static_cast<int>(rotary_dim), q, k_cache, v_cache,
+                                       pages, page_size, stream));
+}
+
+int64_t pbg_attention_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  return bad_heads(1, heads, kv_heads, head_dim) ? 0 : pbg::attention_workspace_bytes(static_cast<int>(head_dim));
+}
+
+int tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages,
+                   int64_t page_size, const int32_t* table, int64_t table_width, const int32_t* lengths,
+                   const int32_t* row_start, int64_t requests, const uint64_t* ancestors, int64_t m, int64_t heads,
+                   int64_t kv_heads, int64_t head_dim, float scale, uint16_t* out, void* workspace,
+                   int64_t workspace_bytes, hipStream_t stream) {
+  if (!q || !k_cache || !v_cache || !table || !lengths || !row_start || !out || !workspace) return PBG_ERR_NULL;
+  if (bad_heads(m, heads, kv_heads, head_dim) || bad_pages(pages, page_size) ||
+      bad_table(requests, table_width, page_size))
+    return PBG_ERR_SHAPE;
+  if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(table, 4) ||
+      misaligned(lengths, 4) || misaligned(row_start, 4) || misaligned(ancestors, 8) || misaligned(out, 16) ||
+      misaligned(workspace, 16))
+    return PBG_ERR_ALIGN;
+  // the kernels multiply by scale * log2(e)
+  if (!(scale > 0.0f) || !(scale < 0x1p127f)) return PBG_ERR_VALUE;
+  if (workspace_bytes < pbg::attention_workspace_bytes(static_cast<int>(head_dim))) return PBG_ERR_WORKSPACE;
+  if (pending_error()) return PBG_ERR_HIP;
+  return finish(pbg::launch_tree_attention(q, k_cache, v_cache, pages, page_size, table, table_width, lengths,
+                                           row_start, requests, ancestors, m, static_cast<int>(heads),
+                                           static_cast<int>(kv_heads), static_cast<int>(head_dim), scale, out,
+                                           workspace, stream));
+}
+
+int penalize_logits(const float* logits, const int32_t* request, const int32_t* tokens, int64_t tokens_width,
+                    const int32_t* prompt_length, const int32_t* length, const float* repetition,
+                    const float* frequency, const float* presence, int64_t requests, const int32_t* drafts,
+                    const int32_t* row_start, const uint64_t* ancestors, const int32_t* bias_start,
+                    const int32_t* bias_token, const float* bias_value, int64_t bias_entries, const uint32_t* grammar,
+                    const int32_t* grammar_row, int64_t states, int64_t m, int64_t n, float* out, int32_t* token,
+                    float* top, uint64_t* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (!logits || !request || !tokens || !prompt_length || !length || !repetition || !frequency || !presence || !out)
+    return PBG_ERR_NULL;
+  const bool has_drafts = drafts != nullptr, has_bias = bias_start != nullptr, has_grammar = grammar != nullptr;
+  if ((row_start != nullptr) != has_drafts || (ancestors != nullptr) != has_drafts ||
+      (bias_token != nullptr) != has_bias || (bias_value != nullptr) != has_bias ||
+      (grammar_row != nullptr) != has_grammar || (token != nullptr) != (top != nullptr) || (token && !workspace))
+    return PBG_ERR_NULL;
+  if (m < 1 || m > PBG_MAX_ROWS || n < 1 || n > PBG_MAX_N || m * n > PBG_MAX_LOGITS || requests < 1 ||
+      requests > PBG_MAX_REQUESTS || tokens_width < 1 || tokens_width > 1LL << 24 ||
+      (has_bias && (bias_entries < 1 || bias_entries > 0x7FFFFFFFLL)) || (has_grammar && (states < 1 || states > 0x7FFFFFFFLL)))
+    return PBG_ERR_SHAPE;
+  if (misaligned(logits, 4) || misaligned(request, 4) || misaligned(tokens, 4) || misaligned(prompt_length, 4) ||
+      misaligned(length, 4) || misaligned(repetition, 4) || misaligned(frequency, 4) || misaligned(presence, 4) ||
+      misaligned(drafts, 4) || misaligned(row_start, 4) || misaligned(ancestors, 8) || misaligned(bias_start, 4) ||
+      misaligned(bias_token, 4) || misaligned(bias_value, 4) || misaligned(grammar, 4) || misaligned(grammar_row, 4) ||
+      misaligned(out, 4) || misaligned(token, 4) || misaligned(top, 4) || misaligned(workspace, 8))
+    return PBG_ERR_ALIGN;
+  if (token && workspace_bytes < 8 * m * ((n + PBG_LOGITS_SLICE - 1) / PBG_LOGITS_SLICE)) return PBG_ERR_WORKSPACE;
+  if (pending_error()) return PBG_ERR_HIP;
+  return finish(pbg::launch_penalize_logits(logits, request, tokens, tokens_width, prompt_length, length, repetition,
+                                            frequency, presence, requests, drafts, row_start, ancestors, bias_start,
+                                            bias_token, bias_value, bias_entries, grammar, grammar_row, states, m, n,
+                                            out, token, top, workspace, stream));
 }
 
 }  // extern "C"

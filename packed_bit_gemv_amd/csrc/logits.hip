@@ -1,0 +1,228 @@
+// penalize_logits: penalties for repeated tokens, biases and grammar masks on logits, and the greedy token.
+#include "pbg_device.hpp"
+#include "pbg_internal.hpp"
+
+namespace pbg {
+namespace {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+
+constexpr uint32_t kGiven = 0x80000000u;  // the prompt holds the token; the low bits count the output's
+
+__device__ __forceinline__ unsigned long long max_u64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
+
+// Largest key over the workgroup's W waves, for thread 0.
+template <int W>
+__device__ __forceinline__ unsigned long long block_max(unsigned long long key) {
+  __shared__ unsigned long long part[W];
+#pragma unroll
+  for (int d = kWave / 2; d > 0; d /= 2) key = max_u64(key, __shfl_xor(key, d));
+  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = key;
+  __syncthreads();
+  key = part[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) key = max_u64(key, part[w]);
+  return key;
+}
+
+struct LogitsArgs {
+  const float* logits;
+  const int32_t* request;
+  const int32_t* tokens;
+  int64_t tokens_width;
+  const int32_t* prompt_length;
+  const int32_t* length;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  int requests;
+  const int32_t* drafts;
+  const int32_t* row_start;
+  const uint64_t* ancestors;
+  const int32_t* bias_start;
+  const int32_t* bias_token;
+  const float* bias_value;
+  int64_t bias_entries;
+  const uint32_t* grammar;
+  const int32_t* grammar_row;
+  int64_t states;
+  int64_t m, n;
+  float* out;
+  unsigned long long* best;  // [m][slices], or null
+};
+
+// A workgroup of T threads takes a slice of 4 V T tokens of one row: it counts
+// the row's tokens that fall into the slice in LDS, then makes one pass over
+// the slice's logits.
+template <int T, int V>
+__global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
+  constexpr int kSlice = 4 * V * T;
+  __shared__ __attribute__((aligned(16))) uint32_t count[kSlice];
+  const int64_t row = blockIdx.x / static_cast<unsigned>(slices);
+  const int slice = blockIdx.x % static_cast<unsigned>(slices);
+  const int i = a.request[row];
+  if (i < 0 || i >= a.requests) return;
+  const int tid = threadIdx.x;
+  const int64_t base = static_cast<int64_t>(slice) * kSlice;
+  const int len = static_cast<int>(a.n - base < kSlice ? a.n - base : kSlice);
+  const float* x = a.logits + row * a.n + base;
+  f32x4_t v[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int c = 4 * (tid + k * T);
+    v[k] = f32x4_t{};
+    if (c + 4 <= len) {
+      v[k] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any_t*>(x + c));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (c + e < len) v[k][e] = x[c + e];
+    }
+  }
+  const int64_t held = a.length[i], width = a.tokens_width;
+  const int used = static_cast<int>(held < 0 ? 0 : held < width ? held : width);
+  const uint64_t anc = a.drafts ? a.ancestors[row] : 0;
+  if (used > 0 || anc) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) *reinterpret_cast<uint4*>(&count[4 * (tid + k * T)]) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    const int prompt = a.prompt_length[i];
+    const int32_t* said = a.tokens + i * width;
+    const uint32_t lo = static_cast<uint32_t>(base);
+    for (int j = tid; j < used; j += T) {
+      const uint32_t u = static_cast<uint32_t>(said[j]) - lo;
+      if (u < static_cast<uint32_t>(len)) {
+        if (j < prompt) atomicOr(&count[u], kGiven);
+        else atomicAdd(&count[u], 1u);
+      }
+    }
+    if (tid < 64 && (anc >> tid & 1)) {
+      const int64_t r = static_cast<int64_t>(a.row_start[i]) + tid;
+      if (r >= 0 && r < a.m) {
+        const uint32_t u = static_cast<uint32_t>(a.drafts[r]) - lo;
+        if (u < static_cast<uint32_t>(len)) atomicAdd(&count[u], 1u);
+      }
+    }
+    __syncthreads();
+    const float rep = a.repetition[i], freq = a.frequency[i], pres = a.presence[i];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const uint4 n4 = *reinterpret_cast<const uint4*>(&count[4 * (tid + k * T)]);
+      const uint32_t n[4] = {n4.x, n4.y, n4.z, n4.w};
+      // few groups of four hold a token that was said
+      if (n4.x | n4.y | n4.z | n4.w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // every step a rounding of its own
+#pragma clang fp contract(off)
+        const float y = v[k][e];
+        const float z = y > 0.0f ? y / rep : y * rep;
+        const uint32_t times = n[e] & ~kGiven;
+        const float f = freq * static_cast<float>(times);
+        const float g = z - f;
+        const float h = g - pres;
+        v[k][e] = n[e] ? times ? h : z : y;
+      }
+    }
+  }
+  if (a.bias_start) {
+    int64_t from = a.bias_start[i], to = a.bias_start[i + 1];
+    if (from < 0) from = 0;
+    if (to > a.bias_entries) to = a.bias_entries;
+    if (from < to) {
+      // the last entry of a token, plus one
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < V; ++k) *reinterpret_cast<uint4*>(&count[4 * (tid + k * T)]) = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+      for (int64_t j = from + tid; j < to; j += T) {
+        const uint32_t u = static_cast<uint32_t>(a.bias_token[j]) - static_cast<uint32_t>(base);
+        if (u < static_cast<uint32_t>(len)) atomicMax(&count[u], static_cast<uint32_t>(j - from) + 1u);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t at = count[4 * (tid + k * T) + e];
+          v[k][e] = at ? v[k][e] + a.bias_value[from + (at ? at - 1 : 0)] : v[k][e];
+        }
+    }
+  }
+  const int64_t state = a.grammar ? a.grammar_row[row] : -1;
+  if (state >= 0 && state < a.states) {
+    const uint32_t* allowed = a.grammar + state * ((a.n + 31) / 32) + base / 32;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = 4 * (tid + k * T);
+      const uint32_t bits = c < len ? allowed[c / 32] >> (c % 32) : 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!(bits >> e & 1)) v[k][e] = -__builtin_inff();
+    }
+  }
+  float* o = a.out + row * a.n + base;
+  unsigned long long key = 0;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int c = 4 * (tid + k * T);
+    if (c + 4 <= len) {
+      *reinterpret_cast<f32x4_any_t*>(o + c) = v[k];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (c + e < len) o[c + e] = v[k][e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < len && v[k][e] > -__builtin_inff()) key = max_u64(key, argmax_key(v[k][e], base + c + e));
+  }
+  if (a.best) {
+    key = block_max<T / kWave>(key);
+    if (tid == 0) a.best[row * slices + slice] = key;
+  }
+}
+
+// The best of a row's slices: one wave a row.
+__global__ __launch_bounds__(kWave) void logits_best_kernel(const unsigned long long* __restrict__ best, int slices,
+                                                            const int32_t* __restrict__ request, int requests,
+                                                            int32_t* __restrict__ token, float* __restrict__ top) {
+  const int64_t row = blockIdx.x;
+  const int i = request[row];
+  if (i < 0 || i >= requests) return;
+  unsigned long long key = 0;
+  for (int s = threadIdx.x; s < slices; s += kWave) key = max_u64(key, best[row * slices + s]);
+#pragma unroll
+  for (int d = kWave / 2; d > 0; d /= 2) key = max_u64(key, __shfl_xor(key, d));
+  if (threadIdx.x == 0) {
+    token[row] = key ? argmax_key_row(key) : -1;
+    top[row] = key ? argmax_key_logit(key) : -__builtin_inff();
+  }
+}
+
+}  // namespace
+
+hipError_t launch_penalize_logits(const float* logits, const int32_t* request, const int32_t* tokens,
+                                  int64_t tokens_width, const int32_t* prompt_length, const int32_t* length,
+                                  const float* repetition, const float* frequency, const float* presence,
+                                  int64_t requests, const int32_t* drafts, const int32_t* row_start,
+                                  const uint64_t* ancestors, const int32_t* bias_start, const int32_t* bias_token,
+                                  const float* bias_value, int64_t bias_entries, const uint32_t* grammar,
+                                  const int32_t* grammar_row, int64_t states, int64_t m, int64_t n, float* out,
+                                  int32_t* token, float* top, uint64_t* workspace, hipStream_t stream) {
+  const LogitsArgs a = {logits,    request,  tokens,     tokens_width, prompt_length, length,    repetition,
+                        frequency, presence, static_cast<int>(requests), drafts, row_start, ancestors, bias_start,
+                        bias_token, bias_value, bias_entries, grammar, grammar_row, states, m, n, out,
+                        token ? reinterpret_cast<unsigned long long*>(workspace) : nullptr};
+  constexpr int kT = 512, kV = 4;
+  const int64_t slices = (n + 4 * kV * kT - 1) / (4 * kV * kT);
+  hipLaunchKernelGGL((penalize_kernel<kT, kV>), dim3(static_cast<unsigned>(m * slices)), dim3(kT), 0, stream, a,
+                     static_cast<int>(slices));
+  if (token)
+    hipLaunchKernelGGL(logits_best_kernel, dim3(static_cast<unsigned>(m)), dim3(kWave), 0, stream, a.best,
+                       static_cast<int>(slices), request, static_cast<int>(requests), token, top);
+  return hipGetLastError();
+}
+
+}  // namespace pbg

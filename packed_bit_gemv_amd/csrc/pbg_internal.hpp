@@ -87,6 +87,39 @@ hipError_t launch_lora_add(const float* y, const uint16_t* x, const int32_t* ids
                            const float* scale, int64_t m, int64_t n, int64_t k, int adapters, int rank, float* out,
                            void* ws, hipStream_t stream);
 
+// log2 of a page size (a power of two).
+int page_shift(int64_t page_size);
+
+hipError_t launch_cache_plan(const int32_t* lengths, const int32_t* added, int64_t requests, int32_t* table,
+                             int64_t table_width, const int32_t* free_pages, int64_t free_capacity,
+                             const int32_t* free_count, int64_t pages, int64_t page_size, const int32_t* parents,
+                             int64_t m, int32_t* row_start, int32_t* request, int32_t* position, int64_t* slot,
+                             uint64_t* ancestors, int32_t* free_left, hipStream_t stream);
+
+hipError_t launch_rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, const double* inv_freq,
+                             const float* q_weight, const float* k_weight, float eps, float amplitude,
+                             bool interleaved, int64_t m, int heads, int kv_heads, int head_dim, int rotary_dim,
+                             uint16_t* q, uint16_t* k_cache, uint16_t* v_cache, int64_t pages, int64_t page_size,
+                             hipStream_t stream);
+
+// Attention over the paged cache; ws holds attention_workspace_bytes(head_dim).
+int64_t attention_workspace_bytes(int head_dim);
+hipError_t launch_tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages,
+                                 int64_t page_size, const int32_t* table, int64_t table_width, const int32_t* lengths,
+                                 const int32_t* row_start, int64_t requests, const uint64_t* ancestors, int64_t m,
+                                 int heads, int kv_heads, int head_dim, float scale, uint16_t* out, void* ws,
+                                 hipStream_t stream);
+
+// Logits under a request's settings; token and workspace may be null (no greedy token).
+hipError_t launch_penalize_logits(const float* logits, const int32_t* request, const int32_t* tokens,
+                                  int64_t tokens_width, const int32_t* prompt_length, const int32_t* length,
+                                  const float* repetition, const float* frequency, const float* presence,
+                                  int64_t requests, const int32_t* drafts, const int32_t* row_start,
+                                  const uint64_t* ancestors, const int32_t* bias_start, const int32_t* bias_token,
+                                  const float* bias_value, int64_t bias_entries, const uint32_t* grammar,
+                                  const int32_t* grammar_row, int64_t states, int64_t m, int64_t n, float* out,
+                                  int32_t* token, float* top, uint64_t* workspace, hipStream_t stream);
+
 // One read of `bytes` (a multiple of 16) from 16-byte aligned src, folded into sink.
 hipError_t launch_stream_read(const void* src, int64_t bytes, uint32_t* sink, hipStream_t stream);
 
