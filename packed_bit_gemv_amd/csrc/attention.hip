@@ -9,17 +9,18 @@
 namespace pbg {
 namespace {
 
-constexpr int kTree = 64;
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
-constexpr int kStep = 32;                // tokens a wave takes at once
-constexpr int kTokens = kWaves * kStep;  // tokens of a unit of work
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -__builtin_inff();
+// A running maximum is only raised when a score passes it by this much (in powers of two): weights then reach 2^8,
+// far inside fp16, and the sums are hardly ever scaled.
+constexpr float kSlack = 8.0f;
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef short short4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) short4_t lds_short4_t;
 
 struct AttnArgs {
@@ -43,26 +44,128 @@ struct AttnArgs {
   float* states;  // [workgroups][2] tiles: outputs, then maxima and sums
 };
 
-// Request i: its rows, its tokens and its units of work.
+// Request i: its rows and tokens, and its units of work. A unit is one tile of
+// query rows over T tokens. Every tile of a tree looks at all tokens; tile n of
+// rows that follow one another needs ceil((length + (n + 1) rows) / T) units,
+// counted as first + more * ceil(n / 2^every), at most one unit too many.
 struct Request {
-  int first, rows, length, tokens;
-  int64_t tiles, steps, units;  // tiles of rows, units of a tile, units in all
+  int begin, rows, length, tokens, tiles;
+  int64_t first, units;  // units of the first tile, of all heads and tiles
+  int more, every;
 };
 
+// a / b with a short division where both fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// Units of the first n tiles of one head.
+__device__ __forceinline__ int64_t units_before(const Request& r, int n) {
+  if (n == 0) return 0;
+  const int64_t k = n - 1, q = k >> r.every, rest = k & ((1 << r.every) - 1);
+  return r.first * n + r.more * (((q * (q + 1) / 2) << r.every) + rest * (q + 1));
+}
+
+template <int T>
 __device__ __forceinline__ Request request_of(const AttnArgs& a, int i) {
   Request r;
   const int s = min(max(a.row_start[i], 0), a.m), e = min(max(a.row_start[i + 1], 0), a.m);
-  r.first = s;
+  const int64_t room = static_cast<int64_t>(a.width) << a.shift;
+  r.begin = s;
   r.rows = max(e - s, 0);
   r.length = max(a.lengths[i], 0);
-  const int64_t room = static_cast<int64_t>(a.width) << a.shift;
-  r.tokens = static_cast<int>(min(static_cast<int64_t>(r.length) + r.rows, room));
+  const int64_t tokens = min(static_cast<int64_t>(r.length) + r.rows, room);
+  r.tokens = static_cast<int>(tokens);
   r.tiles = (r.rows + a.rows - 1) / a.rows;
-  r.steps = (static_cast<int64_t>(r.tokens) + kTokens - 1) / kTokens;
+  r.more = 0;
+  r.every = 0;
+  int64_t seen = tokens;
+  if (!a.ancestors && r.tiles > 1) {
+    seen = min(static_cast<int64_t>(r.length) + a.rows, room);
+    // rows is a power of two where there is more than one tile
+    if (a.rows >= T) r.more = a.rows / T;
+    else r.more = 1, r.every = __builtin_ctz(T / a.rows);
+  }
   // a request without a token to look at still has its zeros to write
-  if (r.steps == 0) r.steps = 1;
-  r.units = r.tiles * r.steps * a.kv_heads * a.chunks;
+  r.first = max((seen + T - 1) / T, static_cast<int64_t>(1));
+  r.units = units_before(r, r.tiles) * a.kv_heads * a.chunks;
   return r;
+}
+
+// Tile n of head group v of a request, from unit `step` of it on.
+struct Place {
+  int head, tile;
+  int64_t step, steps;
+};
+
+__device__ __forceinline__ Place place_of(const Request& r, int64_t in) {
+  Place p;
+  const int64_t each = units_before(r, r.tiles);
+  p.head = static_cast<int>(quotient(in, each));
+  in -= p.head * each;
+  int lo = 0, hi = r.tiles - 1;  // the last tile that begins at `in` or before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (units_before(r, mid) <= in) lo = mid;
+    else hi = mid - 1;
+  }
+  p.tile = lo;
+  p.step = in - units_before(r, lo);
+  p.steps = units_before(r, lo + 1) - units_before(r, lo);
+  return p;
+}
+
+// The workgroup's share of the line of all requests' units: [begin, end), and
+// the request that begin lies in with the units before it.
+struct Share {
+  int64_t begin, end, share, base;
+  int request;
+};
+
+template <int T, int W>
+__device__ __forceinline__ Share share_of(const AttnArgs& a, int64_t me, int64_t groups) {
+  __shared__ int64_t scan[W];
+  __shared__ int64_t found_base;
+  __shared__ int found_request;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int per = (a.requests + (W * kWave) - 1) / (W * kWave);
+  const int i0 = min(tid * per, a.requests), i1 = min(i0 + per, a.requests);
+  int64_t mine = 0;
+  for (int i = i0; i < i1; ++i) mine += request_of<T>(a, i).units;
+  int64_t sum = mine;
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const int64_t o = __shfl_up(sum, d);
+    if (lane >= d) sum += o;
+  }
+  if (lane == kWave - 1) scan[wave] = sum;
+  if (tid == 0) found_request = 0, found_base = 0;
+  __syncthreads();
+  int64_t before = sum - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < wave) before += scan[w];
+    total += scan[w];
+  }
+  Share s;
+  s.share = quotient(total + groups - 1, groups);
+  s.begin = min(me * s.share, total);
+  s.end = min(s.begin + s.share, total);
+  if (s.begin >= before && s.begin < before + mine) {
+    int i = i0;
+    for (; i < i1; ++i) {
+      const int64_t u = request_of<T>(a, i).units;
+      if (s.begin < before + u) break;
+      before += u;
+    }
+    found_request = i;
+    found_base = before;
+  }
+  __syncthreads();
+  s.request = found_request;
+  s.base = found_base;
+  return s;
 }
 
 template <int D>
@@ -93,25 +196,61 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((w & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) | ((w & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u);
 }
 
+// x where bit n of mask is set, else -infinity.
+__device__ __forceinline__ float seen_or_none(float x, uint32_t mask, int n) {
+  const uint32_t keep = static_cast<uint32_t>(static_cast<int32_t>(mask << (31 - n)) >> 31);
+  return as_f32((as_u32(x) & keep) | (0xFF800000u & ~keep));
+}
+
 // Scale of a state with maximum m next to one with maximum `top`.
 __device__ __forceinline__ float weight_of(float m, float top) { return m == kNone ? 0.0f : exp2_of(m - top); }
+
+// Which of the 32 or 64 tokens from t0 on a query row sees, one bit each: all up to the row itself (`upto`, the last of
+// them), or with a tree those before the step and its ancestors.
+__device__ __forceinline__ uint64_t ones_below(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+__device__ __forceinline__ uint64_t seen_from(int t0, int length, int upto, uint64_t tree) {
+  const int n = t0 - length;  // tokens of the step before t0
+  const uint64_t branch = n >= 64 ? 0 : n >= 0 ? tree >> n : n > -64 ? tree << -n : 0;
+  return ones_below(upto - t0 + 1) | branch;
+}
+
+// o += y v for those of the four values at column c that are an infinity or NaN.
+__device__ __forceinline__ void add_wild(f32x4_t& o, const uint16_t* v, int c, int d, float y) {
+  __builtin_amdgcn_sched_barrier(0);  // one piece at a time: this path is rare and must not cost registers
+  if (c >= d) return;
+  const uint2 two = *reinterpret_cast<const uint2*>(v + c);
+  const uint32_t bits[4] = {two.x & 0xFFFFu, two.x >> 16, two.y & 0xFFFFu, two.y >> 16};
+#pragma unroll
+  for (int z = 0; z < 4; ++z) {
+    const float add = y * static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits[z])));
+    o[z] = (bits[z] & 0x7C00u) == 0x7C00u ? o[z] + add : o[z];
+  }
+}
+
+// ---- few query rows
+
+constexpr int kStep = 32;                // tokens a wave takes at once
+constexpr int kTokens = kWaves * kStep;  // tokens of a unit of work
+
+// Workgroups that a compute unit holds.
+constexpr int few_blocks(int d) { return d == 256 ? 1 : 2; }
 
 // D: head_dim rounded up to 64, 128 or 256. QB: blocks of 16 query rows (a
 // query row is one head of one row of the step; the heads of a key
 // head share its keys).
 //
-// The units of work (one tile of query rows over 128 tokens) of all requests
-// stand in one line, which the workgroups share evenly, so that requests
-// of any lengths fill the chip; a tile that ends up with several workgroups is
-// joined by the second kernel.
+// The units of work of all requests stand in one line, which the workgroups
+// share evenly, so that requests of any lengths fill the chip; a tile that ends
+// up with several workgroups is joined by a second kernel.
 //
 // A wave takes 32 tokens of a unit for all query rows, on its own: S^T = K Q^T
 // with keys straight from memory as the first operand, so that a lane
 // holds one query row's scores (its maximum and sum need two lane swaps), and
 // the weights are then the second operand of O^T = V^T W^T as they are. V^T comes out
-// of LDS with transposing reads.
+// of LDS with transposing reads. The loads of the next unit are issued as soon as the scores are done.
 template <int D, int QB>
-__global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(AttnArgs a) {
   constexpr int J = D / 32;       // products of 32 columns in a score
   constexpr int DB = D / 16;      // blocks of 16 columns of the output
   constexpr int kRow = D + 4;     // floats of a row where waves meet
@@ -119,85 +258,93 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
   constexpr int kMeet = 16 * kRow * 4;
   constexpr int kSlice = kStage > kMeet ? kStage : kMeet;
   __shared__ __attribute__((aligned(16))) char lds[kWaves * kSlice];
+  __shared__ __attribute__((aligned(16))) _Float16 weights[kWaves][QB][kWave][8];  // for the rare path only
   __shared__ float meet_max[kWaves][QB * 16], meet_sum[kWaves][QB * 16];
-  __shared__ int64_t scan[kWaves];
-  __shared__ int64_t found[2];
-  __shared__ int found_request;
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1), li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int64_t groups = gridDim.x;
   const int64_t me = blockIdx.x;
-
-  // ---- the share of the line
-  const int per = (a.requests + kThreads - 1) / kThreads;
-  const int i0 = min(tid * per, a.requests), i1 = min(i0 + per, a.requests);
-  int64_t mine = 0;
-  for (int i = i0; i < i1; ++i) mine += request_of(a, i).units;
-  int64_t sum = mine;
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const int64_t o = __shfl_up(sum, d);
-    if (lane >= d) sum += o;
-  }
-  if (lane == kWave - 1) scan[wave] = sum;
-  if (tid == 0) found_request = -1;
-  __syncthreads();
-  int64_t before = sum - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += scan[w];
-    total += scan[w];
-  }
-  const int64_t share = (total + groups - 1) / groups;
-  const int64_t begin = min(me * share, total), end = min(begin + share, total);
-  if (begin >= before && begin < before + mine) {
-    int i = i0;
-    for (; i < i1; ++i) {
-      const int64_t u = request_of(a, i).units;
-      if (begin < before + u) break;
-      before += u;
-    }
-    found_request = i;
-    found[0] = before;
-  }
-  __syncthreads();
+  const Share line = share_of<kTokens, kWaves>(a, me, gridDim.x);
   if (tid == 0) a.parts[me] = make_int4(0, 0, 0, 0);
-  if (begin >= end) return;
-  int request = found_request;
-  int64_t base = found[0];
-  Request r = request_of(a, request);
+  if (line.begin >= line.end) return;
+  int request = line.request;
+  int64_t base = line.base;
+  Request r = request_of<kTokens>(a, request);
 
-  for (int64_t at = begin; at < end;) {
+  for (int64_t at = line.begin; at < line.end;) {
     while (at >= base + r.units) {
       base += r.units;
-      r = request_of(a, ++request);
+      r = request_of<kTokens>(a, ++request);
     }
-    const int64_t in = at - base, tile_units = r.steps;
-    const int64_t head_units = r.tiles * tile_units;
-    const int vhead = static_cast<int>(in / head_units);
-    const int64_t in_head = in - vhead * head_units;
-    const int tile = static_cast<int>(in_head / tile_units);
-    const int64_t step0 = in_head - tile * tile_units;
-    const int64_t step1 = min(step0 + (end - at), tile_units);
-    const int kvh = vhead / a.chunks, chunk = vhead - kvh * a.chunks;
+    const Place here = place_of(r, at - base);
+    const int step0 = static_cast<int>(here.step);
+    const int step1 = static_cast<int>(min(here.step + (line.end - at), here.steps));
+    const int kvh = here.head / a.chunks, chunk = here.head - kvh * a.chunks;
     const int ratio = a.heads / a.kv_heads;
     const int head0 = kvh * ratio + chunk * a.group;
     const int tile_heads = min(a.group, ratio - chunk * a.group);
-    const int row0 = r.first + tile * a.rows;
-    const int tile_rows = min(a.rows, r.rows - tile * a.rows);
+    const int row0 = r.begin + here.tile * a.rows;
+    const int tile_rows = min(a.rows, r.rows - here.tile * a.rows);
+
+    const int32_t* table = a.table + static_cast<int64_t>(request) * a.width;
+    const int64_t page_elements = (static_cast<int64_t>(a.kv_heads) << a.shift) * a.d;
+    const int64_t head_at = (static_cast<int64_t>(kvh) << a.shift) * a.d;
+    char* slice = lds + wave * kSlice;
+    // page of a token, or -1
+    auto page_of = [&](int t) -> int {
+      const int page = t < r.tokens ? table[t >> a.shift] : -1;
+      return page >= 0 && page < a.pages ? page : -1;
+    };
+    // where a token lies in k and v (in elements)
+    auto place = [&](int page, int t) -> int64_t {
+      return page * page_elements + head_at + static_cast<int64_t>(t & ((1 << a.shift) - 1)) * a.d;
+    };
+    const int lane_t = wave * kStep + li;
+    int page[2];
+    uint4 kr[2][J], vr[2][J];
+    uint32_t held = 0, held_next = 0;  // tokens that have a place, one bit each
+    auto fetch_pages = [&](int s) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) page[b] = page_of(s * kTokens + lane_t + 16 * b);
+    };
+    int64_t from[2];
+    auto fetch_values = [&](int s) {
+      held_next = static_cast<uint32_t>(__ballot(page[0] >= 0) & 0xFFFFu) |
+                  static_cast<uint32_t>(__ballot(page[1] >= 0) & 0xFFFFu) << 16;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        from[b] = page[b] >= 0 ? place(page[b], s * kTokens + lane_t + 16 * b) : -1;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int c = 8 * (4 * j + lg);
+          vr[b][j] = make_uint4(0, 0, 0, 0);
+          if (from[b] >= 0 && c < a.d) vr[b][j] = *reinterpret_cast<const uint4*>(a.v + from[b] + c);
+        }
+      }
+    };
+    auto fetch_keys = [&]() {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int c = 8 * (4 * j + lg);
+          kr[b][j] = make_uint4(0, 0, 0, 0);
+          if (from[b] >= 0 && c < a.d) kr[b][j] = *reinterpret_cast<const uint4*>(a.k + from[b] + c);
+        }
+    };
+    fetch_pages(step0);
 
     // ---- queries: block b's row li is query row 16 b + li: row / group, head % group
     mfma_half8_t q[QB][J];
-    uint64_t sees[QB];
+    uint64_t tree[QB];
     int upto[QB];  // last token seen without a tree
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
       const int n = 16 * b + li, rr = n / a.group, hh = n - rr * a.group;
       const bool fine = rr < tile_rows && hh < tile_heads;
       const int row = row0 + rr;
-      sees[b] = fine && a.ancestors ? a.ancestors[row] : 0;
-      upto[b] = fine && !a.ancestors ? r.length + (row - r.first) : r.length - 1;
+      tree[b] = fine && a.ancestors ? a.ancestors[row] : 0;
+      upto[b] = fine && !a.ancestors ? r.length + (row - r.begin) : r.length - 1;
       const uint16_t* p = a.q + (static_cast<int64_t>(row) * a.heads + head0 + hh) * a.d;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -207,6 +354,9 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
         q[b][j] = __builtin_bit_cast(mfma_half8_t, w);
       }
     }
+    fetch_values(step0);
+    fetch_keys();
+    fetch_pages(step0 + 1);
     float top[QB], part[QB];
     f32x4_t o[QB][DB];
 #pragma unroll
@@ -217,40 +367,10 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
       for (int e = 0; e < DB; ++e) o[b][e] = f32x4_t{};
     }
 
-    const int32_t* table = a.table + static_cast<int64_t>(request) * a.width;
-    const int64_t page_bytes = (static_cast<int64_t>(a.kv_heads) << a.shift) * a.d;  // in elements
-    const int64_t head_at = (static_cast<int64_t>(kvh) << a.shift) * a.d;
-    char* slice = lds + wave * kSlice;
-    // where a token lies in k and v (in elements), or -1
-    auto place = [&](int t) -> int64_t {
-      if (t >= r.tokens) return -1;
-      const int page = table[t >> a.shift];
-      if (page < 0 || page >= a.pages) return -1;
-      return page * page_bytes + head_at + static_cast<int64_t>(t & ((1 << a.shift) - 1)) * a.d;
-    };
-
-    for (int64_t s = step0; s < step1; ++s) {
-      const int t0 = static_cast<int>(s) * kTokens + wave * kStep;
-      if (t0 >= r.tokens) continue;
-      const int64_t at0 = place(t0 + li), at1 = place(t0 + 16 + li);
-      // tokens that have a place, one bit each
-      const uint32_t held = static_cast<uint32_t>(__ballot(at0 >= 0) & 0xFFFFu) |
-                            static_cast<uint32_t>(__ballot(at1 >= 0) & 0xFFFFu) << 16;
-      uint4 kr[2][J], vr[2][J];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int64_t p = b ? at1 : at0;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const int c = 8 * (4 * j + lg);
-          kr[b][j] = make_uint4(0, 0, 0, 0);
-          vr[b][j] = make_uint4(0, 0, 0, 0);
-          if (p >= 0 && c < a.d) {
-            kr[b][j] = *reinterpret_cast<const uint4*>(a.k + p + c);
-            vr[b][j] = *reinterpret_cast<const uint4*>(a.v + p + c);
-          }
-        }
-      }
+    for (int s = step0; s < step1; ++s) {
+      const int t0 = s * kTokens + wave * kStep;
+      if (t0 >= r.tokens) break;
+      held = held_next;
       // whether any row may not see a token of these, and values that must reach only rows that see them
       const bool masked = t0 + kStep > r.length || held != 0xFFFFFFFFu;
       uint32_t wild = 0;
@@ -279,53 +399,59 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
           *reinterpret_cast<uint4*>(slice + t * (D * 2) + swizzled<D>(t, 4 * j + lg) * 16) = vr[b][j];
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      // the values' registers are free from here on, the keys' after the scores
+      if (s + 1 < step1) fetch_values(s + 1);
 
-      mfma_half8_t w[QB];
+      mfma_float4_t x[QB][2];
 #pragma unroll
-      for (int b = 0; b < QB; ++b) {
-        mfma_float4_t x[2];
+      for (int b = 0; b < QB; ++b)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          x[h] = mfma_float4_t{};
+          x[b][h] = mfma_float4_t{};
 #pragma unroll
           for (int j = 0; j < J; ++j)
-            x[h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(mfma_half8_t, kr[h][j]), q[b][j], x[h], 0, 0, 0);
+            x[b][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(mfma_half8_t, kr[h][j]), q[b][j], x[b][h],
+                                                             0, 0, 0);
         }
+      if (s + 1 < step1) {
+        fetch_keys();
+        fetch_pages(s + 2);
+      }
+      mfma_half8_t w[QB];
+      uint32_t seen[QB];
+#pragma unroll
+      for (int b = 0; b < QB; ++b) {
         if (masked) {
+          seen[b] = static_cast<uint32_t>(seen_from(t0, r.length, upto[b], tree[b])) & held;
+          const uint32_t mine = seen[b] >> (4 * lg);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int n = 16 * h + 4 * lg + e, t = t0 + n, late = t - r.length;
-              const bool seen = t <= upto[b] || (late >= 0 && late < kTree && (sees[b] >> late & 1));
-              if (!seen || !(held >> n & 1)) x[h][e] = kNone;
-            }
+            for (int e = 0; e < 4; ++e)
+              x[b][h][e] = seen_or_none(x[b][h][e], mine, 16 * h + e);
         }
         float high = kNone;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) high = fmaxf(high, x[h][e]);
+          for (int e = 0; e < 4; ++e) high = fmaxf(high, x[b][h][e]);
         high = groups_max(high) * a.scale;
-        const float now = fmaxf(top[b], high);
-        const float shift = now == kNone ? 0.0f : now;
-        const float keep = weight_of(top[b], shift);
-        top[b] = now;
-        float p[8];
+        if (__any(high > top[b] + kSlack)) {
+          const float now = fmaxf(top[b], high), keep = weight_of(top[b], now);
+          top[b] = now;
+          part[b] *= keep;
+#pragma unroll
+          for (int e = 0; e < DB; ++e) o[b][e] *= keep;
+        }
+        const float less = top[b] == kNone ? 0.0f : top[b];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[4 * h + e] = exp2_of(__builtin_fmaf(x[h][e], a.scale, -shift));
-        // the sum is that of the rounded weights, so that their rounding does not change the weights' total
-        float add = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          w[b][e] = static_cast<_Float16>(p[e]);
-          add += static_cast<float>(w[b][e]);
-        }
-        part[b] = part[b] * keep + add;
-#pragma unroll
-        for (int e = 0; e < DB; ++e) o[b][e] *= keep;
+          for (int e = 0; e < 4; ++e) {
+            const float p = exp2_of(__builtin_fmaf(x[b][h][e], a.scale, -less));
+            part[b] += p;
+            w[b][4 * h + e] = static_cast<_Float16>(p);
+          }
       }
       // ---- O^T += V^T W^T
 #pragma unroll
@@ -337,34 +463,29 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
           const auto v4 = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
               (lds_short4_t*)(slice + t * (D * 2) + swizzled<D>(t, c) * 16 + (li & 1) * 8)));
 #pragma unroll
-          for (int x = 0; x < 4; ++x) v[4 * h + x] = v4[x];
+          for (int y = 0; y < 4; ++y) v[4 * h + y] = v4[y];
         }
 #pragma unroll
         for (int b = 0; b < QB; ++b) o[b][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[b], o[b][e], 0, 0, 0);
       }
       // infinities and NaN among values that some rows may not see: added for the rows that do
+      if (wild) {
+#pragma unroll
+        for (int b = 0; b < QB; ++b) *reinterpret_cast<mfma_half8_t*>(weights[wave][b][lane]) = w[b];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
       while (wild) {
         const int n = __builtin_ctz(wild);
         wild &= wild - 1;
-        const int t = t0 + n, late = t - r.length;
-        const int64_t p = place(t);
-        const int at_lane = li + 16 * ((n & 15) >> 2), at_elem = (n >> 4) * 4 + (n & 3);
+        const int64_t p = place(page_of(t0 + n), t0 + n);
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
-          float x = 0.0f;
+          // element (n / 16) * 4 + n % 4 of the lane that holds the token
+          const float y = static_cast<float>(
+              weights[wave][b][li + 16 * ((n & 15) >> 2)][(n >> 4) * 4 + (n & 3)]);
+          if (seen[b] >> n & 1) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x = e == at_elem ? static_cast<float>(w[b][e]) : x;
-          x = __shfl(x, at_lane);
-          const bool seen = t <= upto[b] || (late >= 0 && late < kTree && (sees[b] >> late & 1));
-          if (seen && p >= 0) {
-#pragma unroll
-            for (int e = 0; e < DB; ++e)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int c = 16 * e + 4 * lg + y;
-                const uint16_t bits = c < a.d ? a.v[p + c] : 0;
-                if ((bits & 0x7C00u) == 0x7C00u) o[b][e][y] += x * static_cast<float>(__builtin_bit_cast(_Float16, bits));
-              }
+            for (int e = 0; e < DB; ++e) add_wild(o[b][e], a.v + p, 16 * e + 4 * lg, a.d, y);
           }
         }
       }
@@ -373,21 +494,21 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
     // ---- the four waves' states meet
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
-      const float s = groups_sum(part[b]);
+      const float sum = groups_sum(part[b]);
       if (lg == 0) {
         meet_max[wave][16 * b + li] = top[b];
-        meet_sum[wave][16 * b + li] = s;
+        meet_sum[wave][16 * b + li] = sum;
       }
     }
     __syncthreads();
-    const bool starts = step0 == 0, ends = step1 == tile_units;
+    const bool starts = here.step == 0, ends = step1 == here.steps;
     float* state = a.states + (me * 2 + (starts ? 1 : 0)) * (QB * 16) * (D + 2);
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
       const int n = 16 * b + li;
       float high = meet_max[0][n];
 #pragma unroll
-      for (int x = 1; x < kWaves; ++x) high = fmaxf(high, meet_max[x][n]);
+      for (int y = 1; y < kWaves; ++y) high = fmaxf(high, meet_max[y][n]);
       const float keep = weight_of(top[b], high);
       float* to = reinterpret_cast<float*>(slice) + li * kRow;
 #pragma unroll
@@ -400,17 +521,17 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
         float most = meet_max[0][qr];
 #pragma unroll
         for (int y = 1; y < kWaves; ++y) most = fmaxf(most, meet_max[y][qr]);
-        float total_w = 0.0f;
+        float sum = 0.0f;
         f32x4_t acc = {};
 #pragma unroll
         for (int y = 0; y < kWaves; ++y) {
-          total_w += meet_sum[y][qr] * weight_of(meet_max[y][qr], most);
+          sum += meet_sum[y][qr] * weight_of(meet_max[y][qr], most);
           acc += *reinterpret_cast<const f32x4_t*>(lds + y * kSlice + (nn * kRow + c) * 4);
         }
         if (starts && ends) {
           if (c < a.d) {
-            const float inv = total_w == 0.0f ? 0.0f : 1.0f / total_w;
-            if (total_w == 0.0f) acc = f32x4_t{};
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            if (sum == 0.0f) acc = f32x4_t{};
             uint16_t* to_out = a.out + (static_cast<int64_t>(row0 + rr) * a.heads + head0 + hh) * a.d + c;
             *reinterpret_cast<half4_t*>(to_out) = __builtin_convertvector(acc * inv, half4_t);
           }
@@ -418,107 +539,507 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
           *reinterpret_cast<f32x4_t*>(state + qr * D + c) = acc;
           if (c == 0) {
             state[QB * 16 * D + 2 * qr] = most;
-            state[QB * 16 * D + 2 * qr + 1] = total_w;
+            state[QB * 16 * D + 2 * qr + 1] = sum;
           }
         }
       }
       __syncthreads();
     }
-    if (starts && !ends && tid == 0) {
-      // the pieces after this one: whole shares of the workgroups that follow
-      const int64_t tile_end = at + tile_units;
-      a.parts[me] = make_int4(row0, head0, tile_heads << 16 | tile_rows, static_cast<int>((tile_end - 1) / share - me + 1));
-    }
+    // the pieces after this one: whole shares of the workgroups that follow
+    if (starts && !ends && tid == 0)
+      a.parts[me] = make_int4(row0, head0, tile_heads << 16 | tile_rows,
+                              static_cast<int>(quotient(at + here.steps - 1, line.share) - me + 1));
     at += step1 - step0;
   }
 }
 
-// Joins the pieces of a tile that several workgroups had: one workgroup for
-// four query rows, their pieces shared by the waves.
-template <int D, int QB>
+// ---- many query rows
+
+constexpr int kWide = 64;  // tokens of a unit of work
+
+// Places of a token's 16-byte pieces in LDS, such that 16 lanes that read the same piece of 16 tokens, and 32 lanes that
+// read 64 bytes of each of four tokens across, touch every bank once.
+template <int D>
+__device__ __forceinline__ int key_piece(int token, int piece) {
+  if constexpr (D == 64) return piece ^ ((token >> 1) & 7);
+  else return piece ^ (token & 15);
+}
+
+template <int D>
+__device__ __forceinline__ int value_piece(int token, int piece) {
+  if constexpr (D == 64) return piece ^ (((token >> 1) & 1) << 2);
+  else return piece ^ ((token & 3) << 2);
+}
+
+// NB: blocks of 32 query rows a wave; the W waves have rows of their own
+// and share the tokens. Keys and values go through LDS, two buffers of 64 tokens, with
+// the next 64 on their way in registers; one barrier a unit. The products are
+// turned as in the kernel for few rows (S^T = K Q^T, O^T = V^T W^T), on 32 x 32 tiles: a lane holds
+// one query row's scores, half of its tokens.
+template <int D, int NB, int W>
+__global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
+  constexpr int KS = D / 16;           // products of 16 columns in a score
+  constexpr int DB = D / 32;           // blocks of 32 columns of the output
+  constexpr int kChunks = D / 8;       // 16-byte pieces of a token's keys
+  constexpr int kPass = W * kWave / kChunks;  // tokens that the workgroup loads at once
+  constexpr int kPasses = kWide / kPass;
+  constexpr int kAhead = 4;            // pieces of keys or values read before they are needed
+  constexpr int kWeigh = 28 * NB;      // vector instructions of 16 tokens' weights
+  constexpr int kRows = W * NB * 32;
+  constexpr int kTile = kWide * D * 2;
+  __shared__ __attribute__((aligned(16))) char lds[2][2][kTile];  // buffer, keys or values
+  __shared__ __attribute__((aligned(16))) _Float16 weights[W][NB][4][kWave][8];  // for the rare path only
+  __shared__ uint32_t flags[3][4];  // tokens without a page, and with values that are infinite or NaN
+
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), li = lane & 31, lh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int64_t me = blockIdx.x;
+  const Share line = share_of<kWide, W>(a, me, gridDim.x);
+  if (tid == 0) a.parts[me] = make_int4(0, 0, 0, 0);
+  if (line.begin >= line.end) return;
+  int request = line.request;
+  int64_t base = line.base;
+  Request r = request_of<kWide>(a, request);
+
+  for (int64_t at = line.begin; at < line.end;) {
+    while (at >= base + r.units) {
+      base += r.units;
+      r = request_of<kWide>(a, ++request);
+    }
+    const Place here = place_of(r, at - base);
+    const int step0 = static_cast<int>(here.step);
+    const int step1 = static_cast<int>(min(here.step + (line.end - at), here.steps));
+    const int kvh = here.head / a.chunks, chunk = here.head - kvh * a.chunks;
+    const int ratio = a.heads / a.kv_heads;
+    const int head0 = kvh * ratio + chunk * a.group;
+    const int tile_heads = min(a.group, ratio - chunk * a.group);
+    const int row0 = r.begin + here.tile * a.rows;
+    const int tile_rows = min(a.rows, r.rows - here.tile * a.rows);
+    // the first token that some row of the tile does not see, and the end of those that any row sees
+    const int edge = a.ancestors ? r.length : r.length + here.tile * a.rows + 1;
+    const int ending = a.ancestors ? r.tokens : min(r.tokens, r.length + here.tile * a.rows + tile_rows);
+    const int last = min(step1, (ending + kWide - 1) / kWide);
+
+    const int32_t* table = a.table + static_cast<int64_t>(request) * a.width;
+    const int64_t page_elements = (static_cast<int64_t>(a.kv_heads) << a.shift) * a.d;
+    const int64_t head_at = (static_cast<int64_t>(kvh) << a.shift) * a.d;
+    const int load_t = tid / kChunks, load_c = tid % kChunks;
+    auto page_of = [&](int t) -> int {
+      const int page = t < r.tokens ? table[t >> a.shift] : -1;
+      return page >= 0 && page < a.pages ? page : -1;
+    };
+    auto place = [&](int page, int t) -> int64_t {
+      return page * page_elements + head_at + static_cast<int64_t>(t & ((1 << a.shift) - 1)) * a.d;
+    };
+    int page[kPasses], page_next[kPasses];
+    uint4 kr[kPasses], vr[kPasses];
+    auto fetch_pages = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) page_next[i] = page_of(s * kWide + load_t + i * kPass);
+    };
+    auto fetch = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        page[i] = page_next[i];
+        const int64_t p = place(page[i], s * kWide + load_t + i * kPass) + 8 * load_c;
+        kr[i] = make_uint4(0, 0, 0, 0);
+        vr[i] = make_uint4(0, 0, 0, 0);
+        if (page[i] >= 0 && 8 * load_c < a.d) {
+          kr[i] = *reinterpret_cast<const uint4*>(a.k + p);
+          vr[i] = *reinterpret_cast<const uint4*>(a.v + p);
+        }
+      }
+    };
+    // the loaded tokens of unit s to its buffer
+    auto store = [&](int s) {
+      const bool edges = (s + 1) * kWide > edge;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int t = load_t + i * kPass;
+        if (page[i] < 0 && load_c == 0) atomicOr(&flags[s % 3][t / 32], 1u << (t % 32));
+        if (edges) {
+          uint4& w = vr[i];
+          const uint4 n = make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w));
+          if (n.x | n.y | n.z | n.w) atomicOr(&flags[s % 3][2 + t / 32], 1u << (t % 32));
+          w = make_uint4(w.x & ~n.x, w.y & ~n.y, w.z & ~n.z, w.w & ~n.w);
+        }
+        *reinterpret_cast<uint4*>(&lds[s & 1][0][t * (D * 2) + key_piece<D>(t, load_c) * 16]) = kr[i];
+        *reinterpret_cast<uint4*>(&lds[s & 1][1][t * (D * 2) + value_piece<D>(t, load_c) * 16]) = vr[i];
+      }
+    };
+
+    // ---- queries: block b's row li is query row 32 (wave NB + b) + li: row / group, head % group
+    mfma_half8_t q[NB][KS];
+    uint64_t tree[NB];
+    int upto[NB];
+    const int wave_n = wave * NB * 32;
+    const bool busy = wave_n / a.group < tile_rows;
+    // the last token that any row of the wave sees
+    const int wave_end = a.ancestors ? ending : min(ending, r.length + here.tile * a.rows + (wave_n + NB * 32 - 1) / a.group + 1);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int n = wave_n + 32 * b + li, rr = n / a.group, hh = n - rr * a.group;
+      const bool fine = rr < tile_rows && hh < tile_heads;
+      const int row = row0 + rr;
+      tree[b] = fine && a.ancestors ? a.ancestors[row] : 0;
+      upto[b] = fine && !a.ancestors ? r.length + (row - r.begin) : r.length - 1;
+      const uint16_t* p = a.q + (static_cast<int64_t>(row) * a.heads + head0 + hh) * a.d;
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        const int c = 8 * (2 * j + lh);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (fine && c < a.d) w = *reinterpret_cast<const uint4*>(p + c);
+        q[b][j] = __builtin_bit_cast(mfma_half8_t, w);
+      }
+    }
+    float top[NB], part[NB];
+    f32x16_t o[NB][DB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      top[b] = kNone;
+      part[b] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < DB; ++e) o[b][e] = f32x16_t{};
+    }
+
+    __syncthreads();  // the last tile's buffers and flags
+    if (tid < 12) flags[tid / 4][tid % 4] = 0;
+    __syncthreads();
+    if (step0 < last) {
+      fetch_pages(step0);
+      fetch(step0);
+      fetch_pages(step0 + 1);
+      store(step0);
+    }
+    __syncthreads();
+
+    for (int s = step0; s < last; ++s) {
+      const int t0 = s * kWide;
+      const bool more = s + 1 < last;
+      if (more) {
+        fetch(s + 1);
+        fetch_pages(s + 2);
+      }
+      // read by unit s - 1, set from unit s + 1 on
+      if (tid < 4) flags[(s + 2) % 3][tid] = 0;
+      if (busy && t0 < wave_end) {
+        const uint64_t gaps = flags[s % 3][0] | static_cast<uint64_t>(flags[s % 3][1]) << 32;
+        const bool masked = t0 + kWide > edge || gaps != 0;
+        const char* ks = lds[s & 1][0];
+        const char* vs = lds[s & 1][1];
+        // ---- S^T = K Q^T, the keys read from LDS four products ahead
+        f32x16_t x[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) x[b][0] = f32x16_t{}, x[b][1] = f32x16_t{};
+        auto key = [&](int n) {
+          const int t = 32 * (n & 1) + li;
+          return *reinterpret_cast<const mfma_half8_t*>(ks + t * (D * 2) + key_piece<D>(t, (n & ~1) + lh) * 16);
+        };
+        mfma_half8_t kf[kAhead];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) kf[n] = key(n);
+#pragma unroll
+        for (int n = 0; n < 2 * KS; ++n) {
+          const mfma_half8_t k = kf[n % kAhead];
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            x[b][n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[b][n / 2], x[b][n & 1], 0, 0, 0);
+          if (n + kAhead < 2 * KS) kf[n % kAhead] = key(n + kAhead);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);  // LDS reads
+#pragma unroll
+        for (int n = 0; n < 2 * KS - kAhead; ++n) {
+          __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);  // matrix instructions
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, NB * kAhead, 0);
+        __builtin_amdgcn_sched_barrier(0);
+
+        uint64_t seen[NB];
+        float less[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if (masked) {
+            __builtin_amdgcn_sched_barrier(0);  // a branch, not a selection in every unit
+            seen[b] = seen_from(t0, r.length, upto[b], tree[b]) & ~gaps & ones_below(r.tokens - t0);
+            const uint64_t mine = seen[b] >> (4 * lh);
+            const uint32_t half[2] = {static_cast<uint32_t>(mine), static_cast<uint32_t>(mine >> 32)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                x[b][h][e] = seen_or_none(x[b][h][e], half[h], 8 * (e / 4) + e % 4);
+          }
+          float high = kNone;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) high = fmaxf(high, x[b][h][e]);
+          auto both = __builtin_amdgcn_permlane32_swap(as_u32(high), as_u32(high), false, false);
+          high = fmaxf(as_f32(both[0]), as_f32(both[1])) * a.scale;
+          if (__any(high > top[b] + kSlack)) {
+            const float now = fmaxf(top[b], high), keep = weight_of(top[b], now);
+            top[b] = now;
+            part[b] *= keep;
+#pragma unroll
+            for (int e = 0; e < DB; ++e) o[b][e] *= keep;
+          }
+          less[b] = top[b] == kNone ? 0.0f : top[b];
+        }
+        // ---- weights and O^T += V^T W^T, 16 tokens after 16: the exponentials of the next 16 run beside the products
+        mfma_half8_t w[NB][4];
+        auto weigh = [&](int j) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              p[e] = exp2_of(__builtin_fmaf(x[b][j / 2][8 * (j & 1) + e], a.scale, -less[b]));
+              w[b][j][e] = static_cast<_Float16>(p[e]);
+            }
+            part[b] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+          }
+        };
+        auto value = [&](int n) {  // columns 32 (n % DB) on of tokens 16 (n / DB) on
+          mfma_half8_t v;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int t = 16 * (n / DB) + 8 * y + 4 * lh + (lane & 15) / 4;
+            const int c = 4 * (n % DB) + 2 * ((lane >> 4) & 1) + (lane & 3) / 2;
+            const auto v4 = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_short4_t*)(vs + t * (D * 2) + value_piece<D>(t, c) * 16 + (lane & 1) * 8)));
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[4 * y + z] = v4[z];
+          }
+          return v;
+        };
+        mfma_half8_t vf[kAhead];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) vf[n] = value(n);
+        weigh(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j < 3) weigh(j + 1);
+#pragma unroll
+          for (int e = 0; e < DB; ++e) {
+            const int n = j * DB + e;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              o[b][e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[n % kAhead], w[b][j], o[b][e], 0, 0, 0);
+            if (n + kAhead < 4 * DB) vf[n % kAhead] = value(n + kAhead);
+          }
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, kWeigh, 0);  // vector instructions
+#pragma unroll
+        for (int n = 0; n < 4 * DB; ++n) {
+          __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);
+          if (n + kAhead < 4 * DB) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          if (n < 3 * DB) __builtin_amdgcn_sched_group_barrier(0x002, kWeigh / DB, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (masked) {
+          // infinities and NaN among values that some rows may not see: added for the rows that do
+          uint64_t wild = flags[s % 3][2] | static_cast<uint64_t>(flags[s % 3][3]) << 32;
+          if (wild) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) *reinterpret_cast<mfma_half8_t*>(weights[wave][b][j][lane]) = w[b][j];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          }
+          while (wild) {
+            const int n = __builtin_ctzll(wild);
+            wild &= wild - 1;
+            const int64_t p = place(page_of(t0 + n), t0 + n);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              // element (n / 8) * 4 + n % 4 of the lane that holds the token
+              const float y = static_cast<float>(weights[wave][b][n >> 4][li + 32 * ((n >> 2) & 1)][((n >> 3) & 1) * 4 + (n & 3)]);
+              if (seen[b] >> n & 1) {
+#pragma unroll
+                for (int e = 0; e < DB; ++e)
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) {
+                    f32x4_t part_o = {o[b][e][4 * z], o[b][e][4 * z + 1], o[b][e][4 * z + 2], o[b][e][4 * z + 3]};
+                    add_wild(part_o, a.v + p, 32 * e + 8 * z + 4 * lh, a.d, y);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) o[b][e][4 * z + u] = part_o[u];
+                  }
+              }
+            }
+          }
+        }
+      }
+      if (more) store(s + 1);
+      __syncthreads();
+    }
+
+    const bool starts = here.step == 0, ends = step1 == here.steps;
+    float* state = a.states + (me * 2 + (starts ? 1 : 0)) * kRows * (D + 2);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int n = wave_n + 32 * b + li, rr = n / a.group, hh = n - rr * a.group;
+      auto both = __builtin_amdgcn_permlane32_swap(as_u32(part[b]), as_u32(part[b]), false, false);
+      const float sum = as_f32(both[0]) + as_f32(both[1]);
+      if (rr >= tile_rows || hh >= tile_heads) continue;
+      if (starts && ends) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint16_t* to = a.out + (static_cast<int64_t>(row0 + rr) * a.heads + head0 + hh) * a.d;
+#pragma unroll
+        for (int e = 0; e < DB; ++e)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int c = 32 * e + 8 * z + 4 * lh;
+            f32x4_t y = {o[b][e][4 * z], o[b][e][4 * z + 1], o[b][e][4 * z + 2], o[b][e][4 * z + 3]};
+            if (sum == 0.0f) y = f32x4_t{};
+            if (c < a.d) *reinterpret_cast<half4_t*>(to + c) = __builtin_convertvector(y * inv, half4_t);
+          }
+      } else {
+#pragma unroll
+        for (int e = 0; e < DB; ++e)
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            *reinterpret_cast<f32x4_t*>(state + n * D + 32 * e + 8 * z + 4 * lh) =
+                f32x4_t{o[b][e][4 * z], o[b][e][4 * z + 1], o[b][e][4 * z + 2], o[b][e][4 * z + 3]};
+        if (lh == 0) {
+          state[kRows * D + 2 * n] = top[b];
+          state[kRows * D + 2 * n + 1] = sum;
+        }
+      }
+    }
+    if (starts && !ends && tid == 0)
+      a.parts[me] = make_int4(row0, head0, tile_heads << 16 | tile_rows,
+                              static_cast<int>(quotient(at + here.steps - 1, line.share) - me + 1));
+    at += step1 - step0;
+  }
+}
+
+// Joins the pieces of a tile of R query rows that several workgroups had. A wave
+// takes four query rows, 16 lanes a row, and merges pieces as they come, four
+// loads of each in flight. With SHARE the workgroup's waves share the pieces of
+// the same four rows (few rows, many pieces), otherwise each has rows of its own.
+template <int D, int R, bool SHARE>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
-  constexpr int kState = QB * 16 * (D + 2);
-  constexpr int kPer = D / kWave;  // columns a lane
-  __shared__ float acc_at[kWaves][4][D];
+  constexpr int64_t kState = R * (D + 2);
+  constexpr int V = D / 64;  // groups of four columns a lane
+  constexpr int kAhead = 4;
+  __shared__ __attribute__((aligned(16))) float acc_at[SHARE ? kWaves : 1][4][D];
   __shared__ float top_at[kWaves][4], sum_at[kWaves][4];
   const int64_t me = blockIdx.x;
   const int4 part = a.parts[me];
   if (part.w == 0) return;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int tile_rows = part.z & 0xFFFF, tile_heads = part.z >> 16;
-  const int first = blockIdx.y * 4;
-  if (first / a.group >= tile_rows) return;
-  for (int x = 0; x < 4; ++x) {
-    const int n = first + x;
-    float top = kNone, sum = 0.0f, acc[kPer] = {};
-    for (int p = wave; p < part.w; p += kWaves) {
-      const float* s = a.states + ((me + p) * 2 + (p == 0 ? 1 : 0)) * kState;
-      const float high = s[QB * 16 * D + 2 * n], w = s[QB * 16 * D + 2 * n + 1];
-      const float now = fmaxf(top, high);
-      const float keep = weight_of(top, now), add = weight_of(high, now);
-      top = now;
-      sum = sum * keep + w * add;
+  const int lane = threadIdx.x & (kWave - 1), li = lane & 15, lg = lane >> 4, wave = threadIdx.x / kWave;
+  const int n = SHARE ? blockIdx.y * 4 + lg : blockIdx.y * 4 * kWaves + 4 * wave + lg;
+  const int rr = n / a.group, hh = n - rr * a.group;
+  const bool fine = rr < (part.z & 0xFFFF) && hh < part.z >> 16;
+  // the first piece is the second state of its workgroup
+  const float* states = a.states + me * 2 * kState;
+  float top = kNone, sum = 0.0f;
+  f32x4_t acc[V] = {};
+  auto merge = [&](float high, float w, const f32x4_t (&x)[V]) {
+    const float now = fmaxf(top, high), keep = weight_of(top, now), add = weight_of(high, now);
+    top = now;
+    sum = sum * keep + w * add;
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) acc[c] = acc[c] * keep + s[n * D + lane + kWave * c] * add;
+    for (int v = 0; v < V; ++v) acc[v] = acc[v] * keep + x[v] * add;
+  };
+  const int first = SHARE ? wave : 0, by = SHARE ? kWaves : 1;
+  if (fine) {
+    for (int p = first; p < part.w; p += kAhead * by) {
+      float high[kAhead], w[kAhead];
+      f32x4_t x[kAhead][V];
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y) {
+        const int piece = min(p + y * by, part.w - 1);
+        const float* s = states + piece * 2 * kState + (piece == 0 ? kState : 0);
+        high[y] = s[R * D + 2 * n];
+        w[y] = s[R * D + 2 * n + 1];
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[y][v] = *reinterpret_cast<const f32x4_t*>(s + n * D + 64 * v + 4 * li);
+      }
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y)
+        if (p + y * by < part.w) merge(high[y], w[y], x[y]);
     }
-    if (lane == 0) {
-      top_at[wave][x] = top;
-      sum_at[wave][x] = sum;
+  }
+  if constexpr (SHARE) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) *reinterpret_cast<f32x4_t*>(&acc_at[wave][lg][64 * v + 4 * li]) = acc[v];
+    if (li == 0) {
+      top_at[wave][lg] = top;
+      sum_at[wave][lg] = sum;
     }
+    __syncthreads();
+    if (wave != 0) return;
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) acc_at[wave][x][lane + kWave * c] = acc[c];
+    for (int y = 1; y < kWaves; ++y) {
+      f32x4_t x[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = *reinterpret_cast<const f32x4_t*>(&acc_at[y][lg][64 * v + 4 * li]);
+      merge(top_at[y][lg], sum_at[y][lg], x);
+    }
   }
-  __syncthreads();
-  const int n = first + wave, rr = n / a.group, hh = n - rr * a.group;
-  if (rr >= tile_rows || hh >= tile_heads) return;
-  float top = top_at[0][wave];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) top = fmaxf(top, top_at[w][wave]);
-  float sum = 0.0f, scale[kWaves];
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    scale[w] = weight_of(top_at[w][wave], top);
-    sum += sum_at[w][wave] * scale[w];
-  }
+  if (!fine) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint16_t* to = a.out + (static_cast<int64_t>(part.x + rr) * a.heads + part.y + hh) * a.d;
 #pragma unroll
-  for (int c = 0; c < kPer; ++c) {
-    const int col = lane + kWave * c;
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += acc_at[w][wave][col] * scale[w];
-    if (sum == 0.0f) v = 0.0f;
-    if (col < a.d)
-      a.out[(static_cast<int64_t>(part.x + rr) * a.heads + part.y + hh) * a.d + col] =
-          __builtin_bit_cast(uint16_t, static_cast<_Float16>(v * inv));
+  for (int v = 0; v < V; ++v) {
+    const int c = 64 * v + 4 * li;
+    if (sum == 0.0f) acc[v] = f32x4_t{};
+    if (c < a.d) *reinterpret_cast<half4_t*>(to + c) = __builtin_convertvector(acc[v] * inv, half4_t);
   }
 }
 
 // Workgroups of a launch: as many as the chip holds at once.
-constexpr int kGroups = 768;
-constexpr int kWideGroups = 256;  // tiles of more than 16 query rows
+constexpr int kGroups = 512;
+constexpr int kWideGroups = 256;
+
+constexpr int wide_waves(int d) { return d == 256 ? 4 : 8; }
 
 template <int D, int QB>
 hipError_t launch_tiles(AttnArgs a, void* ws, hipStream_t stream) {
   const int ratio = a.heads / a.kv_heads;
   a.group = ratio < QB * 16 ? ratio : QB * 16;
   a.chunks = (ratio + a.group - 1) / a.group;
-  a.rows = QB * 16 / a.group;
-  const int groups = QB == 1 ? kGroups : kWideGroups;
+  a.rows = 1 << (31 - __builtin_clz(QB * 16 / a.group));
   a.parts = static_cast<int4*>(ws);
   a.states = reinterpret_cast<float*>(static_cast<char*>(ws) + kGroups * sizeof(int4));
+  const int groups = 256 * few_blocks(D);
   hipLaunchKernelGGL((attention_kernel<D, QB>), dim3(groups), dim3(kThreads), 0, stream, a);
-  hipLaunchKernelGGL((attention_join_kernel<D, QB>), dim3(groups, QB * 4), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attention_join_kernel<D, QB * 16, true>), dim3(groups, QB * 4), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_wide(AttnArgs a, void* ws, hipStream_t stream) {
+  constexpr int W = wide_waves(D), R = W * 32;
+  const int ratio = a.heads / a.kv_heads;
+  a.group = ratio < R ? ratio : R;
+  a.chunks = (ratio + a.group - 1) / a.group;
+  a.rows = 1 << (31 - __builtin_clz(R / a.group));
+  a.parts = static_cast<int4*>(ws);
+  a.states = reinterpret_cast<float*>(static_cast<char*>(ws) + kGroups * sizeof(int4));
+  hipLaunchKernelGGL((attention_wide_kernel<D, 1, W>), dim3(kWideGroups), dim3(W * kWave), 0, stream, a);
+  hipLaunchKernelGGL((attention_join_kernel<D, R, false>), dim3(kWideGroups, R / 16), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_rows(const AttnArgs& a, int64_t rows, void* ws, hipStream_t stream) {
+  if (rows <= 16) return launch_tiles<D, 1>(a, ws, stream);
+  if (rows <= 32) return launch_tiles<D, 2>(a, ws, stream);
+  return launch_wide<D>(a, ws, stream);
 }
 
 }  // namespace
 
 int64_t attention_workspace_bytes(int head_dim) {
   const int64_t d = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  const int64_t wide = d == 256 ? 32 : 64;
-  const int64_t narrow = kGroups * 2 * 16 * (d + 2) * 4, many = kWideGroups * 2 * wide * (d + 2) * 4;
-  return kGroups * 16 + (narrow > many ? narrow : many);
+  const int64_t few = kGroups * 2 * 32 * (d + 2) * 4, wide = kWideGroups * 2 * 32 * wide_waves(d) * (d + 2) * 4;
+  return kGroups * 16 + (few > wide ? few : wide);
 }
 
 hipError_t launch_tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages,
@@ -530,11 +1051,10 @@ hipError_t launch_tree_attention(const uint16_t* q, const uint16_t* k_cache, con
                       row_start, static_cast<int>(requests), ancestors, static_cast<int>(m), heads, kv_heads, head_dim,
                       scale * kLog2e, out, 0, 0, 0, nullptr, nullptr};
   // query rows of a key head that a request has on average
-  const bool few = m * (heads / kv_heads) <= 16 * requests;
-  if (head_dim <= 64) return few ? launch_tiles<64, 1>(a, workspace, stream) : launch_tiles<64, 4>(a, workspace, stream);
-  if (head_dim <= 128)
-    return few ? launch_tiles<128, 1>(a, workspace, stream) : launch_tiles<128, 4>(a, workspace, stream);
-  return few ? launch_tiles<256, 1>(a, workspace, stream) : launch_tiles<256, 2>(a, workspace, stream);
+  const int64_t rows = (m * (heads / kv_heads) + requests - 1) / requests;
+  if (head_dim <= 64) return launch_rows<64>(a, rows, workspace, stream);
+  if (head_dim <= 128) return launch_rows<128>(a, rows, workspace, stream);
+  return launch_rows<256>(a, rows, workspace, stream);
 }
 
 }  // namespace pbg
