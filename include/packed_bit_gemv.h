@@ -646,9 +646,12 @@ int rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, c
  *              bytes, of any content; one serves any number of rows and
  *              requests and fewer heads, and calls of many graphs that do not overlap
  *              in time
- * Heads and head_dim as for rotary_qkv. Scores, weights' sums and the output's sums are fp32; the weights enter the
+ * Heads and head_dim as for rotary_qkv; page_size at least
+ * PBG_ATTENTION_MIN_PAGE. Scores, weights' sums and the output's sums are fp32; the weights enter the
  * second product rounded to fp16 relative to the row's largest.
  */
+#define PBG_ATTENTION_MIN_PAGE 8
+
 int64_t pbg_attention_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t head_dim);
 
 int tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages,

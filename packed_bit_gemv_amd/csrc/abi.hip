@@ -442,7 +442,7 @@ int tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v
                    int64_t kv_heads, int64_t head_dim, float scale, uint16_t* out, void* workspace,
                    int64_t workspace_bytes, hipStream_t stream) {
   if (!q || !k_cache || !v_cache || !table || !lengths || !row_start || !out || !workspace) return PBG_ERR_NULL;
-  if (bad_heads(m, heads, kv_heads, head_dim) || bad_pages(pages, page_size) ||
+  if (bad_heads(m, heads, kv_heads, head_dim) || bad_pages(pages, page_size) || page_size < PBG_ATTENTION_MIN_PAGE ||
       bad_table(requests, table_width, page_size))
     return PBG_ERR_SHAPE;
   if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(table, 4) ||

@@ -11,6 +11,8 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
+constexpr int kMinPage = 8;  // tokens
+constexpr int kParts = 8;  // of the chip; workgroups go to them in turn
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -__builtin_inff();
 // A running maximum is only raised when a score passes it by this much (in powers of two): weights then reach 2^8,
@@ -22,6 +24,7 @@ typedef short short4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) short4_t lds_short4_t;
+typedef __attribute__((address_space(4))) int32_t const_int_t;  // read through the scalar cache
 
 struct AttnArgs {
   const uint16_t* q;
@@ -572,10 +575,15 @@ __device__ __forceinline__ int value_piece(int token, int piece) {
 }
 
 // NB: blocks of 32 query rows a wave; the W waves have rows of their own
-// and share the tokens. Keys and values go through LDS, two buffers of 64 tokens, with
-// the next 64 on their way in registers; one barrier a unit. The products are
+// and share the tokens, 64 at a time, through LDS, with the next 64 on their way in registers. The products are
 // turned as in the kernel for few rows (S^T = K Q^T, O^T = V^T W^T), on 32 x 32 tiles: a lane holds
 // one query row's scores, half of its tokens.
+//
+// A unit has two turns, with a barrier behind each: the matrix products
+// (O^T of the unit before, S^T of this one), then everything else (weights, loads). The two waves of a
+// SIMD are half a unit apart, so that one's products run beside the other's exponentials. The waves
+// that come second write their part of a unit's keys and values one turn early; K(s) is
+// read in turns 2 s and 2 s + 1, V(s) in 2 s + 2 and 2 s + 3, so keys need two buffers and values three.
 template <int D, int NB, int W>
 __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   constexpr int KS = D / 16;           // products of 16 columns in a score
@@ -583,17 +591,22 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   constexpr int kChunks = D / 8;       // 16-byte pieces of a token's keys
   constexpr int kPass = W * kWave / kChunks;  // tokens that the workgroup loads at once
   constexpr int kPasses = kWide / kPass;
+  constexpr int kGroup = kWave / kChunks;  // tokens that a wave loads at once
+  static_assert(kGroup <= kMinPage, "tokens of one page");
   constexpr int kAhead = 4;            // pieces of keys or values read before they are needed
-  constexpr int kWeigh = 28 * NB;      // vector instructions of 16 tokens' weights
   constexpr int kRows = W * NB * 32;
   constexpr int kTile = kWide * D * 2;
-  __shared__ __attribute__((aligned(16))) char lds[2][2][kTile];  // buffer, keys or values
+  constexpr bool kTurns = W > 4;  // two waves on a SIMD: they take turns
+  constexpr int kValueTiles = kTurns ? 3 : 2;
+  __shared__ __attribute__((aligned(16))) char keys[2][kTile];
+  __shared__ __attribute__((aligned(16))) char values[kValueTiles][kTile];
   __shared__ __attribute__((aligned(16))) _Float16 weights[W][NB][4][kWave][8];  // for the rare path only
-  __shared__ uint32_t flags[3][4];  // tokens without a page, and with values that are infinite or NaN
+  __shared__ uint32_t flags[4][4];  // tokens without a page, and with values that are infinite or NaN
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1), li = lane & 31, lh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int64_t me = blockIdx.x;
+  // neighbours in the line, which read the same keys and values, on one of the chip's eight parts, which has a cache of its own
+  const int64_t me = (blockIdx.x % kParts) * (gridDim.x / kParts) + blockIdx.x / kParts;
   const Share line = share_of<kWide, W>(a, me, gridDim.x);
   if (tid == 0) a.parts[me] = make_int4(0, 0, 0, 0);
   if (line.begin >= line.end) return;
@@ -620,51 +633,58 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
     const int ending = a.ancestors ? r.tokens : min(r.tokens, r.length + here.tile * a.rows + tile_rows);
     const int last = min(step1, (ending + kWide - 1) / kWide);
 
-    const int32_t* table = a.table + static_cast<int64_t>(request) * a.width;
+    const const_int_t* table = (const const_int_t*)(a.table + static_cast<int64_t>(request) * a.width);
     const int64_t page_elements = (static_cast<int64_t>(a.kv_heads) << a.shift) * a.d;
     const int64_t head_at = (static_cast<int64_t>(kvh) << a.shift) * a.d;
-    const int load_t = tid / kChunks, load_c = tid % kChunks;
+    const int page_mask = (1 << a.shift) - 1;
+    // a wave loads kGroup tokens at once, all of one page, so that page numbers and addresses are the wave's, not a lane's
+    const int load_t = lane / kChunks, load_c = lane % kChunks;
+    const int lane_at = load_t * a.d + 8 * load_c;
+    const bool lane_loads = 8 * load_c < a.d;
+    // page of a token that the whole wave has in common, or -1
     auto page_of = [&](int t) -> int {
-      const int page = t < r.tokens ? table[t >> a.shift] : -1;
-      return page >= 0 && page < a.pages ? page : -1;
+      const int page = table[min(t >> a.shift, a.width - 1)];
+      return t < r.tokens && page >= 0 && page < a.pages ? page : -1;
     };
     auto place = [&](int page, int t) -> int64_t {
-      return page * page_elements + head_at + static_cast<int64_t>(t & ((1 << a.shift) - 1)) * a.d;
+      return page * page_elements + head_at + static_cast<int64_t>(t & page_mask) * a.d;
     };
     int page[kPasses], page_next[kPasses];
     uint4 kr[kPasses], vr[kPasses];
     auto fetch_pages = [&](int s) {
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) page_next[i] = page_of(s * kWide + load_t + i * kPass);
+      for (int i = 0; i < kPasses; ++i) page_next[i] = page_of(s * kWide + wave * kGroup + i * kPass);
     };
     auto fetch = [&](int s) {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
         page[i] = page_next[i];
-        const int64_t p = place(page[i], s * kWide + load_t + i * kPass) + 8 * load_c;
         kr[i] = make_uint4(0, 0, 0, 0);
         vr[i] = make_uint4(0, 0, 0, 0);
-        if (page[i] >= 0 && 8 * load_c < a.d) {
-          kr[i] = *reinterpret_cast<const uint4*>(a.k + p);
-          vr[i] = *reinterpret_cast<const uint4*>(a.v + p);
+        if (page[i] >= 0) {
+          const int64_t p = place(page[i], s * kWide + wave * kGroup + i * kPass);
+          if (lane_loads) {
+            kr[i] = *reinterpret_cast<const uint4*>(a.k + p + lane_at);
+            vr[i] = *reinterpret_cast<const uint4*>(a.v + p + lane_at);
+          }
         }
       }
     };
-    // the loaded tokens of unit s to its buffer
+    // the loaded tokens of unit s to its buffers
     auto store = [&](int s) {
       const bool edges = (s + 1) * kWide > edge;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const int t = load_t + i * kPass;
-        if (page[i] < 0 && load_c == 0) atomicOr(&flags[s % 3][t / 32], 1u << (t % 32));
+        const int t = wave * kGroup + load_t + i * kPass;
+        if (page[i] < 0 && load_c == 0) atomicOr(&flags[s & 3][t / 32], 1u << (t % 32));
         if (edges) {
           uint4& w = vr[i];
           const uint4 n = make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w));
-          if (n.x | n.y | n.z | n.w) atomicOr(&flags[s % 3][2 + t / 32], 1u << (t % 32));
+          if (n.x | n.y | n.z | n.w) atomicOr(&flags[s & 3][2 + t / 32], 1u << (t % 32));
           w = make_uint4(w.x & ~n.x, w.y & ~n.y, w.z & ~n.z, w.w & ~n.w);
         }
-        *reinterpret_cast<uint4*>(&lds[s & 1][0][t * (D * 2) + key_piece<D>(t, load_c) * 16]) = kr[i];
-        *reinterpret_cast<uint4*>(&lds[s & 1][1][t * (D * 2) + value_piece<D>(t, load_c) * 16]) = vr[i];
+        *reinterpret_cast<uint4*>(&keys[s & 1][t * (D * 2) + key_piece<D>(t, load_c) * 16]) = kr[i];
+        *reinterpret_cast<uint4*>(&values[s % kValueTiles][t * (D * 2) + value_piece<D>(t, load_c) * 16]) = vr[i];
       }
     };
 
@@ -702,105 +722,36 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
       for (int e = 0; e < DB; ++e) o[b][e] = f32x16_t{};
     }
 
+    const int turn = kTurns ? wave / (W / 2) : 0;
     __syncthreads();  // the last tile's buffers and flags
-    if (tid < 12) flags[tid / 4][tid % 4] = 0;
+    if (tid < 16) flags[tid / 4][tid % 4] = 0;
     __syncthreads();
-    if (step0 < last) {
-      fetch_pages(step0);
-      fetch(step0);
-      fetch_pages(step0 + 1);
-      store(step0);
+    fetch_pages(step0);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      if (n <= turn && step0 + n < last) {
+        fetch(step0 + n);
+        fetch_pages(step0 + n + 1);
+        store(step0 + n);
+      }
+    if (step0 + 1 + turn < last) {
+      fetch(step0 + 1 + turn);
+      fetch_pages(step0 + 2 + turn);
     }
     __syncthreads();
+    if (turn) __syncthreads();
 
-    for (int s = step0; s < last; ++s) {
-      const int t0 = s * kWide;
-      const bool more = s + 1 < last;
-      if (more) {
-        fetch(s + 1);
-        fetch_pages(s + 2);
-      }
-      // read by unit s - 1, set from unit s + 1 on
-      if (tid < 4) flags[(s + 2) % 3][tid] = 0;
-      if (busy && t0 < wave_end) {
-        const uint64_t gaps = flags[s % 3][0] | static_cast<uint64_t>(flags[s % 3][1]) << 32;
-        const bool masked = t0 + kWide > edge || gaps != 0;
-        const char* ks = lds[s & 1][0];
-        const char* vs = lds[s & 1][1];
-        // ---- S^T = K Q^T, the keys read from LDS four products ahead
-        f32x16_t x[NB][2];
+    mfma_half8_t w[NB][4];
+    f32x16_t x[NB][2];
+    uint64_t seen[NB];
+    bool masked = false;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) x[b][0] = f32x16_t{}, x[b][1] = f32x16_t{};
-        auto key = [&](int n) {
-          const int t = 32 * (n & 1) + li;
-          return *reinterpret_cast<const mfma_half8_t*>(ks + t * (D * 2) + key_piece<D>(t, (n & ~1) + lh) * 16);
-        };
-        mfma_half8_t kf[kAhead];
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int n = 0; n < kAhead; ++n) kf[n] = key(n);
-#pragma unroll
-        for (int n = 0; n < 2 * KS; ++n) {
-          const mfma_half8_t k = kf[n % kAhead];
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            x[b][n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[b][n / 2], x[b][n & 1], 0, 0, 0);
-          if (n + kAhead < 2 * KS) kf[n % kAhead] = key(n + kAhead);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);  // LDS reads
-#pragma unroll
-        for (int n = 0; n < 2 * KS - kAhead; ++n) {
-          __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);  // matrix instructions
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, NB * kAhead, 0);
-        __builtin_amdgcn_sched_barrier(0);
-
-        uint64_t seen[NB];
-        float less[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          if (masked) {
-            __builtin_amdgcn_sched_barrier(0);  // a branch, not a selection in every unit
-            seen[b] = seen_from(t0, r.length, upto[b], tree[b]) & ~gaps & ones_below(r.tokens - t0);
-            const uint64_t mine = seen[b] >> (4 * lh);
-            const uint32_t half[2] = {static_cast<uint32_t>(mine), static_cast<uint32_t>(mine >> 32)};
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                x[b][h][e] = seen_or_none(x[b][h][e], half[h], 8 * (e / 4) + e % 4);
-          }
-          float high = kNone;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) high = fmaxf(high, x[b][h][e]);
-          auto both = __builtin_amdgcn_permlane32_swap(as_u32(high), as_u32(high), false, false);
-          high = fmaxf(as_f32(both[0]), as_f32(both[1])) * a.scale;
-          if (__any(high > top[b] + kSlack)) {
-            const float now = fmaxf(top[b], high), keep = weight_of(top[b], now);
-            top[b] = now;
-            part[b] *= keep;
-#pragma unroll
-            for (int e = 0; e < DB; ++e) o[b][e] *= keep;
-          }
-          less[b] = top[b] == kNone ? 0.0f : top[b];
-        }
-        // ---- weights and O^T += V^T W^T, 16 tokens after 16: the exponentials of the next 16 run beside the products
-        mfma_half8_t w[NB][4];
-        auto weigh = [&](int j) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            float p[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              p[e] = exp2_of(__builtin_fmaf(x[b][j / 2][8 * (j & 1) + e], a.scale, -less[b]));
-              w[b][j][e] = static_cast<_Float16>(p[e]);
-            }
-            part[b] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-          }
-        };
+    for (int b = 0; b < NB; ++b) seen[b] = 0;
+    for (int s = step0; s <= last; ++s) {
+      // ---- the matrix products' turn: O^T += V^T W^T of unit s - 1, S^T = K Q^T of unit s
+      const bool scores = busy && s < last && s * kWide < wave_end;
+      if (busy && s > step0 && (s - 1) * kWide < wave_end) {
+        const char* vs = values[(s - 1) % kValueTiles];
         auto value = [&](int n) {  // columns 32 (n % DB) on of tokens 16 (n / DB) on
           mfma_half8_t v;
 #pragma unroll
@@ -818,31 +769,26 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < kAhead; ++n) vf[n] = value(n);
-        weigh(0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j < 3) weigh(j + 1);
-#pragma unroll
-          for (int e = 0; e < DB; ++e) {
-            const int n = j * DB + e;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-              o[b][e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[n % kAhead], w[b][j], o[b][e], 0, 0, 0);
-            if (n + kAhead < 4 * DB) vf[n % kAhead] = value(n + kAhead);
-          }
-        }
-        __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, kWeigh, 0);  // vector instructions
 #pragma unroll
         for (int n = 0; n < 4 * DB; ++n) {
-          __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);
-          if (n + kAhead < 4 * DB) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-          if (n < 3 * DB) __builtin_amdgcn_sched_group_barrier(0x002, kWeigh / DB, 0);
+          const mfma_half8_t v = vf[n % kAhead];
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            o[b][n % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[b][n / DB], o[b][n % DB], 0, 0, 0);
+          if (n + kAhead < 4 * DB) vf[n % kAhead] = value(n + kAhead);
         }
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);  // LDS reads
+#pragma unroll
+        for (int n = 0; n < 4 * DB - kAhead; ++n) {
+          __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);  // matrix instructions
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, NB * kAhead, 0);
         __builtin_amdgcn_sched_barrier(0);
         if (masked) {
           // infinities and NaN among values that some rows may not see: added for the rows that do
-          uint64_t wild = flags[s % 3][2] | static_cast<uint64_t>(flags[s % 3][3]) << 32;
+          const int t0 = (s - 1) * kWide;
+          uint64_t wild = flags[(s - 1) & 3][2] | static_cast<uint64_t>(flags[(s - 1) & 3][3]) << 32;
           if (wild) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
@@ -873,9 +819,91 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
           }
         }
       }
-      if (more) store(s + 1);
+      if (scores) {
+        const char* ks = keys[s & 1];
+        auto key = [&](int n) {
+          const int t = 32 * (n & 1) + li;
+          return *reinterpret_cast<const mfma_half8_t*>(ks + t * (D * 2) + key_piece<D>(t, (n & ~1) + lh) * 16);
+        };
+        mfma_half8_t kf[kAhead];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) kf[n] = key(n);
+#pragma unroll
+        for (int n = 0; n < 2 * KS; ++n) {
+          const mfma_half8_t k = kf[n % kAhead];
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            x[b][n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[b][n / 2], n < 2 ? f32x16_t{} : x[b][n & 1], 0, 0, 0);
+          if (n + kAhead < 2 * KS) kf[n % kAhead] = key(n + kAhead);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int n = 0; n < 2 * KS - kAhead; ++n) {
+          __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, NB * kAhead, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __syncthreads();
+
+      // ---- the other instructions' turn: loads, and the weights of unit s
+      const int next = s + 1 + turn;
+      if (next < last) store(next);
+      if (next + 1 < last) {
+        fetch(next + 1);
+        fetch_pages(next + 2);
+      }
+      // last read two units before it, written from the next turn on
+      if (tid < 4) flags[(s + 2) & 3][tid] = 0;
+      if (scores) {
+        const int t0 = s * kWide;
+        const uint64_t gaps = flags[s & 3][0] | static_cast<uint64_t>(flags[s & 3][1]) << 32;
+        masked = t0 + kWide > edge || gaps != 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if (masked) {
+            __builtin_amdgcn_sched_barrier(0);  // a branch, not a selection in every unit
+            seen[b] = seen_from(t0, r.length, upto[b], tree[b]) & ~gaps & ones_below(r.tokens - t0);
+            const uint64_t mine = seen[b] >> (4 * lh);
+            const uint32_t half[2] = {static_cast<uint32_t>(mine), static_cast<uint32_t>(mine >> 32)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                x[b][h][e] = seen_or_none(x[b][h][e], half[h], 8 * (e / 4) + e % 4);
+          }
+          float high = kNone;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) high = fmaxf(high, x[b][h][e]);
+          auto both = __builtin_amdgcn_permlane32_swap(as_u32(high), as_u32(high), false, false);
+          high = fmaxf(as_f32(both[0]), as_f32(both[1])) * a.scale;
+          if (__any(high > top[b] + kSlack)) {
+            const float now = fmaxf(top[b], high), keep = weight_of(top[b], now);
+            top[b] = now;
+            part[b] *= keep;
+#pragma unroll
+            for (int e = 0; e < DB; ++e) o[b][e] *= keep;
+          }
+          const float less = top[b] == kNone ? 0.0f : top[b];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              p[e] = exp2_of(__builtin_fmaf(x[b][j / 2][8 * (j & 1) + e], a.scale, -less));
+              w[b][j][e] = static_cast<_Float16>(p[e]);
+            }
+            part[b] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+          }
+        }
+      }
       __syncthreads();
     }
+    if (kTurns && !turn) __syncthreads();
 
     const bool starts = here.step == 0, ends = step1 == here.steps;
     float* state = a.states + (me * 2 + (starts ? 1 : 0)) * kRows * (D + 2);

@@ -74,7 +74,7 @@ def test_attention_refusals():
     refusals("tree_attention", ATTENTION, ["q", "k_cache", "v_cache", "table", "lengths", "row_start", "out", "workspace"], ["ancestors"],
              dict(q=16, k_cache=16, v_cache=16, ancestors=8, out=16, workspace=16),
              [("m", 0), ("m", 2 ** 20 + 1), ("requests", 0), ("requests", 4097), ("heads", 3), ("heads", 1026), ("kv_heads", 0),
-              ("head_dim", 4), ("head_dim", 65), ("head_dim", 512), ("pages", 0), ("page_size", 48), ("table_width", 0),
+              ("head_dim", 4), ("head_dim", 65), ("head_dim", 512), ("pages", 0), ("page_size", 48), ("page_size", 4), ("table_width", 0),
               ("table_width", 2 ** 28)],
              [("scale", 0.0), ("scale", -1.0), ("scale", math.nan), ("scale", math.inf), ("scale", 3e38)])
     size = lib().pbg_attention_workspace_bytes(4, 2, 64)
