@@ -589,10 +589,11 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   constexpr int KS = D / 16;           // products of 16 columns in a score
   constexpr int DB = D / 32;           // blocks of 32 columns of the output
   constexpr int kChunks = D / 8;       // 16-byte pieces of a token's keys
-  constexpr int kPass = W * kWave / kChunks;  // tokens that the workgroup loads at once
-  constexpr int kPasses = kWide / kPass;
   constexpr int kGroup = kWave / kChunks;  // tokens that a wave loads at once
-  static_assert(kGroup <= kMinPage, "tokens of one page");
+  constexpr int kMine = kWide / W;         // tokens of a unit that it loads
+  constexpr int kPasses = kMine / kGroup;
+  constexpr int kPages = kMine / kMinPage;
+  static_assert(kPages * kMinPage == kMine && kMinPage % kGroup == 0, "whole pages");
   constexpr int kAhead = 4;            // pieces of keys or values read before they are needed
   constexpr int kRows = W * NB * 32;
   constexpr int kTile = kWide * D * 2;
@@ -637,54 +638,58 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
     const int64_t page_elements = (static_cast<int64_t>(a.kv_heads) << a.shift) * a.d;
     const int64_t head_at = (static_cast<int64_t>(kvh) << a.shift) * a.d;
     const int page_mask = (1 << a.shift) - 1;
-    // a wave loads kGroup tokens at once, all of one page, so that page numbers and addresses are the wave's, not a lane's
+    // A wave loads kMine tokens of a unit that follow one another, eight of them always of one page, so that page
+    // numbers and addresses are the wave's, not a lane's. Columns past head_dim are loaded as column 0 and
+    // made zero in the keys; tokens without a page are loaded from the first page and made zero.
     const int load_t = lane / kChunks, load_c = lane % kChunks;
-    const int lane_at = load_t * a.d + 8 * load_c;
-    const bool lane_loads = 8 * load_c < a.d;
-    // page of a token that the whole wave has in common, or -1
-    auto page_of = [&](int t) -> int {
-      const int page = table[min(t >> a.shift, a.width - 1)];
-      return t < r.tokens && page >= 0 && page < a.pages ? page : -1;
-    };
-    auto place = [&](int page, int t) -> int64_t {
-      return page * page_elements + head_at + static_cast<int64_t>(t & page_mask) * a.d;
-    };
-    int page[kPasses], page_next[kPasses];
+    const uint32_t lane_at = load_t * a.d + (8 * load_c < a.d ? 8 * load_c : 0);
+    int page[kPages], page_next[kPages];
     uint4 kr[kPasses], vr[kPasses];
     auto fetch_pages = [&](int s) {
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) page_next[i] = page_of(s * kWide + wave * kGroup + i * kPass);
+      for (int g = 0; g < kPages; ++g) {
+        const int t = s * kWide + wave * kMine + g * kMinPage;
+        const int found = table[static_cast<uint32_t>(min(t >> a.shift, a.width - 1))];
+        page_next[g] = t < r.tokens && static_cast<uint32_t>(found) < static_cast<uint32_t>(a.pages) ? found : -1;
+      }
     };
     auto fetch = [&](int s) {
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        page[i] = page_next[i];
-        kr[i] = make_uint4(0, 0, 0, 0);
-        vr[i] = make_uint4(0, 0, 0, 0);
-        if (page[i] >= 0) {
-          const int64_t p = place(page[i], s * kWide + wave * kGroup + i * kPass);
-          if (lane_loads) {
-            kr[i] = *reinterpret_cast<const uint4*>(a.k + p + lane_at);
-            vr[i] = *reinterpret_cast<const uint4*>(a.v + p + lane_at);
-          }
+      for (int g = 0; g < kPages; ++g) {
+        page[g] = page_next[g];
+        const int t = s * kWide + wave * kMine + g * kMinPage;
+        const int64_t from = max(page[g], 0) * page_elements + head_at + (t & page_mask) * a.d;
+        const uint16_t* k = a.k + from;
+        const uint16_t* v = a.v + from;
+#pragma unroll
+        for (int i = 0; i < kPasses / kPages; ++i) {
+          kr[g * (kPasses / kPages) + i] = *reinterpret_cast<const uint4*>(k + (lane_at + i * kGroup * a.d));
+          vr[g * (kPasses / kPages) + i] = *reinterpret_cast<const uint4*>(v + (lane_at + i * kGroup * a.d));
         }
       }
     };
     // the loaded tokens of unit s to its buffers
-    auto store = [&](int s) {
+    auto store = [&](int s, char* key_to, char* value_to) {
       const bool edges = (s + 1) * kWide > edge;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const int t = wave * kGroup + load_t + i * kPass;
-        if (page[i] < 0 && load_c == 0) atomicOr(&flags[s & 3][t / 32], 1u << (t % 32));
+        const int t = wave * kMine + i * kGroup + load_t;
+        uint32_t* flag = &flags[s & 3][t / 32];
+        if (page[i / (kPasses / kPages)] < 0) {
+          __builtin_amdgcn_sched_barrier(0);  // a branch
+          kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+          if (load_c == 0) atomicOr(flag, 1u << (t % 32));
+        }
+        if (a.d != D && 8 * load_c >= a.d) kr[i] = make_uint4(0, 0, 0, 0);
         if (edges) {
+          __builtin_amdgcn_sched_barrier(0);
           uint4& w = vr[i];
           const uint4 n = make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w));
-          if (n.x | n.y | n.z | n.w) atomicOr(&flags[s & 3][2 + t / 32], 1u << (t % 32));
+          if (n.x | n.y | n.z | n.w) atomicOr(flag + 2, 1u << (t % 32));
           w = make_uint4(w.x & ~n.x, w.y & ~n.y, w.z & ~n.z, w.w & ~n.w);
         }
-        *reinterpret_cast<uint4*>(&keys[s & 1][t * (D * 2) + key_piece<D>(t, load_c) * 16]) = kr[i];
-        *reinterpret_cast<uint4*>(&values[s % kValueTiles][t * (D * 2) + value_piece<D>(t, load_c) * 16]) = vr[i];
+        *reinterpret_cast<uint4*>(key_to + t * (D * 2) + key_piece<D>(t, load_c) * 16) = kr[i];
+        *reinterpret_cast<uint4*>(value_to + t * (D * 2) + value_piece<D>(t, load_c) * 16) = vr[i];
       }
     };
 
@@ -732,7 +737,7 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
       if (n <= turn && step0 + n < last) {
         fetch(step0 + n);
         fetch_pages(step0 + n + 1);
-        store(step0 + n);
+        store(step0 + n, keys[(step0 + n) & 1], values[n]);
       }
     if (step0 + 1 + turn < last) {
       fetch(step0 + 1 + turn);
@@ -747,11 +752,14 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
     bool masked = false;
 #pragma unroll
     for (int b = 0; b < NB; ++b) seen[b] = 0;
+    // values of units s - 1 and of the one that is stored next
+    int value_read = (kValueTiles - 1) * kTile, value_store = (1 + turn) * kTile;
     for (int s = step0; s <= last; ++s) {
+      const uint64_t gaps = flags[s & 3][0] | static_cast<uint64_t>(flags[s & 3][1]) << 32;
       // ---- the matrix products' turn: O^T += V^T W^T of unit s - 1, S^T = K Q^T of unit s
       const bool scores = busy && s < last && s * kWide < wave_end;
       if (busy && s > step0 && (s - 1) * kWide < wave_end) {
-        const char* vs = values[(s - 1) % kValueTiles];
+        const char* vs = values[0] + value_read;
         auto value = [&](int n) {  // columns 32 (n % DB) on of tokens 16 (n / DB) on
           mfma_half8_t v;
 #pragma unroll
@@ -799,7 +807,7 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
           while (wild) {
             const int n = __builtin_ctzll(wild);
             wild &= wild - 1;
-            const int64_t p = place(page_of(t0 + n), t0 + n);
+            const int64_t p = table[static_cast<uint32_t>((t0 + n) >> a.shift)] * page_elements + head_at + ((t0 + n) & page_mask) * a.d;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               // element (n / 8) * 4 + n % 4 of the lane that holds the token
@@ -850,7 +858,9 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
 
       // ---- the other instructions' turn: loads, and the weights of unit s
       const int next = s + 1 + turn;
-      if (next < last) store(next);
+      if (next < last) store(next, keys[next & 1], values[0] + value_store);
+      value_store = value_store == (kValueTiles - 1) * kTile ? 0 : value_store + kTile;
+      value_read = value_read == (kValueTiles - 1) * kTile ? 0 : value_read + kTile;
       if (next + 1 < last) {
         fetch(next + 1);
         fetch_pages(next + 2);
@@ -859,7 +869,6 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
       if (tid < 4) flags[(s + 2) & 3][tid] = 0;
       if (scores) {
         const int t0 = s * kWide;
-        const uint64_t gaps = flags[s & 3][0] | static_cast<uint64_t>(flags[s & 3][1]) << 32;
         masked = t0 + kWide > edge || gaps != 0;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
