@@ -73,11 +73,13 @@ __device__ __forceinline__ int64_t units_before(const Request& r, int n) {
 template <int T>
 __device__ __forceinline__ Request request_of(const AttnArgs& a, int i) {
   Request r;
-  const int s = min(max(a.row_start[i], 0), a.m), e = min(max(a.row_start[i + 1], 0), a.m);
+  const const_int_t* row_start = (const const_int_t*)a.row_start;
+  const const_int_t* lengths = (const const_int_t*)a.lengths;
+  const int s = min(max(row_start[i], 0), a.m), e = min(max(row_start[i + 1], 0), a.m);
   const int64_t room = static_cast<int64_t>(a.width) << a.shift;
   r.begin = s;
   r.rows = max(e - s, 0);
-  r.length = max(a.lengths[i], 0);
+  r.length = max(lengths[i], 0);
   const int64_t tokens = min(static_cast<int64_t>(r.length) + r.rows, room);
   r.tokens = static_cast<int>(tokens);
   r.tiles = (r.rows + a.rows - 1) / a.rows;
@@ -104,6 +106,13 @@ struct Place {
 
 __device__ __forceinline__ Place place_of(const Request& r, int64_t in) {
   Place p;
+  if (r.tiles == 1) {
+    p.head = static_cast<int>(quotient(in, r.first));
+    p.tile = 0;
+    p.step = in - p.head * r.first;
+    p.steps = r.first;
+    return p;
+  }
   const int64_t each = units_before(r, r.tiles);
   p.head = static_cast<int>(quotient(in, each));
   in -= p.head * each;
@@ -119,20 +128,57 @@ __device__ __forceinline__ Place place_of(const Request& r, int64_t in) {
   return p;
 }
 
-// The workgroup's share of the line of all requests' units: [begin, end), and
-// the request that begin lies in with the units before it.
+// The workgroup's share of the line of all requests' units, [begin, end), and
+// the request r that begin lies in, with the units before it. 2^G workgroups of W waves.
 struct Share {
   int64_t begin, end, share, base;
   int request;
 };
 
-template <int T, int W>
-__device__ __forceinline__ Share share_of(const AttnArgs& a, int64_t me, int64_t groups) {
+__device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+__device__ __forceinline__ int64_t from_lane(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), lane);
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+template <int T, int W, int G>
+__device__ __forceinline__ Share share_of(const AttnArgs& a, int64_t me, Request& r) {
   __shared__ int64_t scan[W];
   __shared__ int64_t found_base;
   __shared__ int found_request;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  const int per = (a.requests + (W * kWave) - 1) / (W * kWave);
+  Share s;
+  if (a.requests <= kWave) {
+    // every wave by itself, a request a lane
+    const Request mine = request_of<T>(a, min(lane, a.requests - 1));
+    const int64_t units = lane < a.requests ? mine.units : 0;
+    int64_t sum = units;
+    for (int d = 1; d < a.requests; d *= 2) {
+      const int64_t o = __shfl_up(sum, d);
+      if (lane >= d) sum += o;
+    }
+    const int64_t total = from_lane(sum, a.requests - 1), before = sum - units;
+    s.share = (total + ((1 << G) - 1)) >> G;
+    s.begin = min(me * s.share, total);
+    s.end = min(s.begin + s.share, total);
+    const uint64_t where = __ballot(s.begin >= before && s.begin < before + units);
+    const int at = where ? __builtin_ctzll(where) : 0;
+    s.request = at;
+    s.base = from_lane(before, at);
+    r.begin = from_lane(mine.begin, at);
+    r.rows = from_lane(mine.rows, at);
+    r.length = from_lane(mine.length, at);
+    r.tokens = from_lane(mine.tokens, at);
+    r.tiles = from_lane(mine.tiles, at);
+    r.first = from_lane(mine.first, at);
+    r.units = from_lane(mine.units, at);
+    r.more = from_lane(mine.more, at);
+    r.every = from_lane(mine.every, at);
+    return s;
+  }
+  const int per = (a.requests + W * kWave - 1) / (W * kWave);
   const int i0 = min(tid * per, a.requests), i1 = min(i0 + per, a.requests);
   int64_t mine = 0;
   for (int i = i0; i < i1; ++i) mine += request_of<T>(a, i).units;
@@ -151,8 +197,7 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, int64_t me, int64_t
     if (w < wave) before += scan[w];
     total += scan[w];
   }
-  Share s;
-  s.share = quotient(total + groups - 1, groups);
+  s.share = (total + ((1 << G) - 1)) >> G;
   s.begin = min(me * s.share, total);
   s.end = min(s.begin + s.share, total);
   if (s.begin >= before && s.begin < before + mine) {
@@ -166,8 +211,9 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, int64_t me, int64_t
     found_base = before;
   }
   __syncthreads();
-  s.request = found_request;
-  s.base = found_base;
+  s.request = __builtin_amdgcn_readfirstlane(found_request);
+  s.base = from_lane(found_base, 0);
+  r = request_of<T>(a, s.request);
   return s;
 }
 
@@ -236,8 +282,9 @@ __device__ __forceinline__ void add_wild(f32x4_t& o, const uint16_t* v, int c, i
 constexpr int kStep = 32;                // tokens a wave takes at once
 constexpr int kTokens = kWaves * kStep;  // tokens of a unit of work
 
-// Workgroups that a compute unit holds.
+// Workgroups that a compute unit holds, and the launch's (as many as the chip holds), a power of two.
 constexpr int few_blocks(int d) { return d == 256 ? 1 : 2; }
+constexpr int few_bits(int d) { return d == 256 ? 8 : 9; }
 
 // D: head_dim rounded up to 64, 128 or 256. QB: blocks of 16 query rows (a
 // query row is one head of one row of the step; the heads of a key
@@ -267,12 +314,12 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
   const int tid = threadIdx.x, lane = tid & (kWave - 1), li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int64_t me = blockIdx.x;
-  const Share line = share_of<kTokens, kWaves>(a, me, gridDim.x);
+  Request r;
+  const Share line = share_of<kTokens, kWaves, few_bits(D)>(a, me, r);
   if (tid == 0) a.parts[me] = make_int4(0, 0, 0, 0);
   if (line.begin >= line.end) return;
   int request = line.request;
   int64_t base = line.base;
-  Request r = request_of<kTokens>(a, request);
 
   for (int64_t at = line.begin; at < line.end;) {
     while (at >= base + r.units) {
@@ -559,6 +606,7 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
 // ---- many query rows
 
 constexpr int kWide = 64;  // tokens of a unit of work
+constexpr int kWideBits = 8;  // one workgroup on each compute unit
 
 // Places of a token's 16-byte pieces in LDS, such that 16 lanes that read the same piece of 16 tokens, and 32 lanes that
 // read 64 bytes of each of four tokens across, touch every bank once.
@@ -608,12 +656,12 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   // neighbours in the line, which read the same keys and values, on one of the chip's eight parts, which has a cache of its own
   const int64_t me = (blockIdx.x % kParts) * (gridDim.x / kParts) + blockIdx.x / kParts;
-  const Share line = share_of<kWide, W>(a, me, gridDim.x);
+  Request r;
+  const Share line = share_of<kWide, W, kWideBits>(a, me, r);
   if (tid == 0) a.parts[me] = make_int4(0, 0, 0, 0);
   if (line.begin >= line.end) return;
   int request = line.request;
   int64_t base = line.base;
-  Request r = request_of<kWide>(a, request);
 
   for (int64_t at = line.begin; at < line.end;) {
     while (at >= base + r.units) {
@@ -954,85 +1002,126 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   }
 }
 
-// Joins the pieces of a tile of R query rows that several workgroups had. A wave
-// takes four query rows, 16 lanes a row, and merges pieces as they come, four
-// loads of each in flight. With SHARE the workgroup's waves share the pieces of
-// the same four rows (few rows, many pieces), otherwise each has rows of its own.
-template <int D, int R, bool SHARE>
+// Joins the pieces of the tiles of R query rows that several of N workgroups had. Every
+// workgroup counts the jobs, four query rows of a tile each, and takes its
+// share of them (a workgroup for each that could be, most of them with nothing to do, took 9 us for 4,096). A wave has 16 lanes
+// a row and merges pieces as they come, the loads of several in flight. With SHARE the
+// workgroup's waves share the pieces of the same four rows (few rows, many
+// pieces), otherwise each has rows of its own.
+template <int D, int R, int N, bool SHARE>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
   constexpr int64_t kState = R * (D + 2);
   constexpr int V = D / 64;  // groups of four columns a lane
-  constexpr int kAhead = 4;
+  constexpr int kAhead = SHARE ? 16 / V : 4;
+  constexpr int kEach = N / kThreads;
   __shared__ __attribute__((aligned(16))) float acc_at[SHARE ? kWaves : 1][4][D];
   __shared__ float top_at[kWaves][4], sum_at[kWaves][4];
-  const int64_t me = blockIdx.x;
-  const int4 part = a.parts[me];
-  if (part.w == 0) return;
-  const int lane = threadIdx.x & (kWave - 1), li = lane & 15, lg = lane >> 4, wave = threadIdx.x / kWave;
-  const int n = SHARE ? blockIdx.y * 4 + lg : blockIdx.y * 4 * kWaves + 4 * wave + lg;
-  const int rr = n / a.group, hh = n - rr * a.group;
-  const bool fine = rr < (part.z & 0xFFFF) && hh < part.z >> 16;
-  // the first piece is the second state of its workgroup
-  const float* states = a.states + me * 2 * kState;
-  float top = kNone, sum = 0.0f;
-  f32x4_t acc[V] = {};
-  auto merge = [&](float high, float w, const f32x4_t (&x)[V]) {
-    const float now = fmaxf(top, high), keep = weight_of(top, now), add = weight_of(high, now);
-    top = now;
-    sum = sum * keep + w * add;
+  // tiles of 16 query rows have a job or two each: a workgroup each, with no need to count
+  constexpr bool kCounts = R > 16;
+  __shared__ int ends[kCounts ? N : 1], waves[kWaves];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), li = lane & 15, lg = lane >> 4, wave = tid / kWave;
+  auto jobs_of = [&](const int4& part) { return part.w == 0 ? 0 : ((part.z & 0xFFFF) * a.group + 3) / 4; };
+  int jobs;
+  if constexpr (kCounts) {
+    int count[kEach], mine = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = acc[v] * keep + x[v] * add;
-  };
-  const int first = SHARE ? wave : 0, by = SHARE ? kWaves : 1;
-  if (fine) {
-    for (int p = first; p < part.w; p += kAhead * by) {
-      float high[kAhead], w[kAhead];
-      f32x4_t x[kAhead][V];
-#pragma unroll
-      for (int y = 0; y < kAhead; ++y) {
-        const int piece = min(p + y * by, part.w - 1);
-        const float* s = states + piece * 2 * kState + (piece == 0 ? kState : 0);
-        high[y] = s[R * D + 2 * n];
-        w[y] = s[R * D + 2 * n + 1];
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[y][v] = *reinterpret_cast<const f32x4_t*>(s + n * D + 64 * v + 4 * li);
-      }
-#pragma unroll
-      for (int y = 0; y < kAhead; ++y)
-        if (p + y * by < part.w) merge(high[y], w[y], x[y]);
+    for (int i = 0; i < kEach; ++i) {
+      count[i] = jobs_of(a.parts[tid * kEach + i]);
+      mine += count[i];
     }
-  }
-  if constexpr (SHARE) {
+    int before = block_scan<kWaves>(mine, waves, jobs);
 #pragma unroll
-    for (int v = 0; v < V; ++v) *reinterpret_cast<f32x4_t*>(&acc_at[wave][lg][64 * v + 4 * li]) = acc[v];
-    if (li == 0) {
-      top_at[wave][lg] = top;
-      sum_at[wave][lg] = sum;
+    for (int i = 0; i < kEach; ++i) {
+      before += count[i];
+      ends[tid * kEach + i] = before;
     }
     __syncthreads();
-    if (wave != 0) return;
-#pragma unroll
-    for (int y = 1; y < kWaves; ++y) {
-      f32x4_t x[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = *reinterpret_cast<const f32x4_t*>(&acc_at[y][lg][64 * v + 4 * li]);
-      merge(top_at[y][lg], sum_at[y][lg], x);
-    }
+  } else {
+    jobs = jobs_of(a.parts[blockIdx.x]);
   }
-  if (!fine) return;
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint16_t* to = a.out + (static_cast<int64_t>(part.x + rr) * a.heads + part.y + hh) * a.d;
+  const int step = !kCounts ? 1 : SHARE ? gridDim.x : gridDim.x * kWaves;
+  for (int job = !kCounts ? 0 : SHARE ? blockIdx.x : blockIdx.x * kWaves + wave; job < jobs; job += step) {
+    int64_t me = blockIdx.x;
+    int n = job * 4 + lg;
+    if constexpr (kCounts) {
+      int lo = 0, hi = N - 1;  // the first workgroup whose jobs end behind this one
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (ends[mid] > job) hi = mid;
+        else lo = mid + 1;
+      }
+      me = __builtin_amdgcn_readfirstlane(lo);
+      n -= me == 0 ? 0 : ends[me - 1] * 4;
+    }
+    const int4 part = a.parts[me];
+    const int rr = n / a.group, hh = n - rr * a.group;
+    const bool fine = rr < (part.z & 0xFFFF) && hh < part.z >> 16;
+    // the first piece is the second state of its workgroup
+    const float* states = a.states + me * 2 * kState;
+    float top = kNone, sum = 0.0f;
+    f32x4_t acc[V] = {};
+    auto merge = [&](float high, float w, const f32x4_t (&x)[V]) {
+      const float now = fmaxf(top, high), keep = weight_of(top, now), add = weight_of(high, now);
+      top = now;
+      sum = sum * keep + w * add;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = 64 * v + 4 * li;
-    if (sum == 0.0f) acc[v] = f32x4_t{};
-    if (c < a.d) *reinterpret_cast<half4_t*>(to + c) = __builtin_convertvector(acc[v] * inv, half4_t);
+      for (int v = 0; v < V; ++v) acc[v] = acc[v] * keep + x[v] * add;
+    };
+    const int first = SHARE ? wave : 0, by = SHARE ? kWaves : 1;
+    if (fine) {
+      for (int p = first; p < part.w; p += kAhead * by) {
+        float high[kAhead], w[kAhead];
+        f32x4_t x[kAhead][V];
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+          const int piece = min(p + y * by, part.w - 1);
+          const float* s = states + piece * 2 * kState + (piece == 0 ? kState : 0);
+          high[y] = s[R * D + 2 * n];
+          w[y] = s[R * D + 2 * n + 1];
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[y][v] = *reinterpret_cast<const f32x4_t*>(s + n * D + 64 * v + 4 * li);
+        }
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y)
+          if (p + y * by < part.w) merge(high[y], w[y], x[y]);
+      }
+    }
+    if constexpr (SHARE) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) *reinterpret_cast<f32x4_t*>(&acc_at[wave][lg][64 * v + 4 * li]) = acc[v];
+      if (li == 0) {
+        top_at[wave][lg] = top;
+        sum_at[wave][lg] = sum;
+      }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int y = 1; y < kWaves; ++y) {
+          f32x4_t x[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[v] = *reinterpret_cast<const f32x4_t*>(&acc_at[y][lg][64 * v + 4 * li]);
+          merge(top_at[y][lg], sum_at[y][lg], x);
+        }
+      }
+      __syncthreads();
+    }
+    if (fine && (!SHARE || wave == 0)) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      uint16_t* to = a.out + (static_cast<int64_t>(part.x + rr) * a.heads + part.y + hh) * a.d;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = 64 * v + 4 * li;
+        if (sum == 0.0f) acc[v] = f32x4_t{};
+        if (c < a.d) *reinterpret_cast<half4_t*>(to + c) = __builtin_convertvector(acc[v] * inv, half4_t);
+      }
+    }
   }
 }
 
 // Workgroups of a launch: as many as the chip holds at once.
-constexpr int kGroups = 512;
-constexpr int kWideGroups = 256;
+constexpr int kGroups = 1 << few_bits(64);
+constexpr int kWideGroups = 1 << kWideBits;
+constexpr int kJoinGroups = 256;
 
 constexpr int wide_waves(int d) { return d == 256 ? 4 : 8; }
 
@@ -1044,9 +1133,9 @@ hipError_t launch_tiles(AttnArgs a, void* ws, hipStream_t stream) {
   a.rows = 1 << (31 - __builtin_clz(QB * 16 / a.group));
   a.parts = static_cast<int4*>(ws);
   a.states = reinterpret_cast<float*>(static_cast<char*>(ws) + kGroups * sizeof(int4));
-  const int groups = 256 * few_blocks(D);
+  constexpr int groups = 1 << few_bits(D);
   hipLaunchKernelGGL((attention_kernel<D, QB>), dim3(groups), dim3(kThreads), 0, stream, a);
-  hipLaunchKernelGGL((attention_join_kernel<D, QB * 16, true>), dim3(groups, QB * 4), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attention_join_kernel<D, QB * 16, groups, true>), dim3(QB == 1 ? groups : kJoinGroups), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -1060,7 +1149,7 @@ hipError_t launch_wide(AttnArgs a, void* ws, hipStream_t stream) {
   a.parts = static_cast<int4*>(ws);
   a.states = reinterpret_cast<float*>(static_cast<char*>(ws) + kGroups * sizeof(int4));
   hipLaunchKernelGGL((attention_wide_kernel<D, 1, W>), dim3(kWideGroups), dim3(W * kWave), 0, stream, a);
-  hipLaunchKernelGGL((attention_join_kernel<D, R, false>), dim3(kWideGroups, R / 16), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attention_join_kernel<D, R, kWideGroups, false>), dim3(8 * kJoinGroups), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
