@@ -52,16 +52,29 @@ struct LogitsArgs {
   unsigned long long* best;  // [m][slices], or null
 };
 
+typedef __attribute__((address_space(4))) int32_t const_int_t;  // read through the scalar cache
+typedef __attribute__((address_space(4))) float const_float_t;
+typedef __attribute__((address_space(4))) uint64_t const_u64_t;
+
+template <typename C, typename P>
+__device__ __forceinline__ C* scalars(P* p) {
+  return (C*)p;
+}
+
 // A workgroup of T threads takes a slice of 4 V T tokens of one row: it counts
 // the row's tokens that fall into the slice in LDS, then makes one pass over
-// the slice's logits.
+// the slice's logits, which were loaded before. Everything that the row's request says is
+// loaded together, and the history several loads at a time.
 template <int T, int V>
 __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
   constexpr int kSlice = 4 * V * T;
+  constexpr int kAhead = 8;
   __shared__ __attribute__((aligned(16))) uint32_t count[kSlice];
   const int64_t row = blockIdx.x / static_cast<unsigned>(slices);
   const int slice = blockIdx.x % static_cast<unsigned>(slices);
-  const int i = a.request[row];
+  const int i = scalars<const const_int_t>(a.request)[row];
+  const uint64_t anc = a.drafts ? scalars<const const_u64_t>(a.ancestors)[row] : 0;
+  const int64_t state = a.grammar ? scalars<const const_int_t>(a.grammar_row)[row] : -1;
   if (i < 0 || i >= a.requests) return;
   const int tid = threadIdx.x;
   const int64_t base = static_cast<int64_t>(slice) * kSlice;
@@ -80,32 +93,60 @@ __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
         if (c + e < len) v[k][e] = x[c + e];
     }
   }
-  const int64_t held = a.length[i], width = a.tokens_width;
+  const int64_t held = scalars<const const_int_t>(a.length)[i], width = a.tokens_width;
   const int used = static_cast<int>(held < 0 ? 0 : held < width ? held : width);
-  const uint64_t anc = a.drafts ? a.ancestors[row] : 0;
-  if (used > 0 || anc) {
+  const int prompt = scalars<const const_int_t>(a.prompt_length)[i];
+  const float rep = scalars<const const_float_t>(a.repetition)[i], freq = scalars<const const_float_t>(a.frequency)[i];
+  const float pres = scalars<const const_float_t>(a.presence)[i];
+  const int64_t draft_at = a.drafts ? scalars<const const_int_t>(a.row_start)[i] : 0;
+  int64_t from = 0, to = 0;
+  if (a.bias_start) {
+    from = scalars<const const_int_t>(a.bias_start)[i];
+    to = scalars<const const_int_t>(a.bias_start)[i + 1];
+    if (from < 0) from = 0;
+    if (to > a.bias_entries) to = a.bias_entries;
+  }
+  const bool masks = state >= 0 && state < a.states;
+  uint32_t allowed[V];
+  if (masks) {
+    const uint32_t* words = a.grammar + state * ((a.n + 31) / 32) + base / 32;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = 4 * (tid + k * T);
+      allowed[k] = c < len ? words[c / 32] >> (c % 32) : 0u;
+    }
+  }
+  auto clear = [&]() {
 #pragma unroll
     for (int k = 0; k < V; ++k) *reinterpret_cast<uint4*>(&count[4 * (tid + k * T)]) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    const int prompt = a.prompt_length[i];
+  };
+  if (used > 0 || anc) {
+    clear();
     const int32_t* said = a.tokens + i * width;
     const uint32_t lo = static_cast<uint32_t>(base);
-    for (int j = tid; j < used; j += T) {
-      const uint32_t u = static_cast<uint32_t>(said[j]) - lo;
-      if (u < static_cast<uint32_t>(len)) {
-        if (j < prompt) atomicOr(&count[u], kGiven);
-        else atomicAdd(&count[u], 1u);
+    for (int j0 = 0; j0 < used; j0 += kAhead * T) {
+      int32_t token[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) token[k] = said[min(j0 + k * T + tid, used - 1)];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int j = j0 + k * T + tid;
+        const uint32_t u = static_cast<uint32_t>(token[k]) - lo;
+        if (j < used && u < static_cast<uint32_t>(len)) {
+          if (j < prompt) atomicOr(&count[u], kGiven);
+          else atomicAdd(&count[u], 1u);
+        }
       }
     }
     if (tid < 64 && (anc >> tid & 1)) {
-      const int64_t r = static_cast<int64_t>(a.row_start[i]) + tid;
+      const int64_t r = draft_at + tid;
       if (r >= 0 && r < a.m) {
         const uint32_t u = static_cast<uint32_t>(a.drafts[r]) - lo;
         if (u < static_cast<uint32_t>(len)) atomicAdd(&count[u], 1u);
       }
     }
     __syncthreads();
-    const float rep = a.repetition[i], freq = a.frequency[i], pres = a.presence[i];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const uint4 n4 = *reinterpret_cast<const uint4*>(&count[4 * (tid + k * T)]);
@@ -114,7 +155,7 @@ __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
       if (n4.x | n4.y | n4.z | n4.w)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // every step a rounding of its own
+        // every step a rounding of its own, selected afterwards: branches around single elements cost 200 registers here
 #pragma clang fp contract(off)
         const float y = v[k][e];
         const float z = y > 0.0f ? y / rep : y * rep;
@@ -126,41 +167,32 @@ __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
       }
     }
   }
-  if (a.bias_start) {
-    int64_t from = a.bias_start[i], to = a.bias_start[i + 1];
-    if (from < 0) from = 0;
-    if (to > a.bias_entries) to = a.bias_entries;
-    if (from < to) {
-      // the last entry of a token, plus one
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < V; ++k) *reinterpret_cast<uint4*>(&count[4 * (tid + k * T)]) = make_uint4(0, 0, 0, 0);
-      __syncthreads();
-      for (int64_t j = from + tid; j < to; j += T) {
-        const uint32_t u = static_cast<uint32_t>(a.bias_token[j]) - static_cast<uint32_t>(base);
-        if (u < static_cast<uint32_t>(len)) atomicMax(&count[u], static_cast<uint32_t>(j - from) + 1u);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t at = count[4 * (tid + k * T) + e];
-          v[k][e] = at ? v[k][e] + a.bias_value[from + (at ? at - 1 : 0)] : v[k][e];
-        }
+  if (from < to) {
+    // the last entry of a token, plus one
+    __syncthreads();
+    clear();
+    for (int64_t j = from + tid; j < to; j += T) {
+      const uint32_t u = static_cast<uint32_t>(a.bias_token[j]) - static_cast<uint32_t>(base);
+      if (u < static_cast<uint32_t>(len)) atomicMax(&count[u], static_cast<uint32_t>(j - from) + 1u);
     }
-  }
-  const int64_t state = a.grammar ? a.grammar_row[row] : -1;
-  if (state >= 0 && state < a.states) {
-    const uint32_t* allowed = a.grammar + state * ((a.n + 31) / 32) + base / 32;
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c = 4 * (tid + k * T);
-      const uint32_t bits = c < len ? allowed[c / 32] >> (c % 32) : 0u;
+      const uint4 n4 = *reinterpret_cast<const uint4*>(&count[4 * (tid + k * T)]);
+      const uint32_t n[4] = {n4.x, n4.y, n4.z, n4.w};
+      if (n4.x | n4.y | n4.z | n4.w)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (!(bits >> e & 1)) v[k][e] = -__builtin_inff();
+      for (int e = 0; e < 4; ++e) {
+        const float add = a.bias_value[from + (n[e] ? n[e] - 1 : 0)];
+        v[k][e] = n[e] ? v[k][e] + add : v[k][e];
+      }
     }
+  }
+  if (masks) {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[k][e] = allowed[k] >> e & 1 ? v[k][e] : -__builtin_inff();
   }
   float* o = a.out + row * a.n + base;
   unsigned long long key = 0;
@@ -174,11 +206,21 @@ __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
       for (int e = 0; e < 3; ++e)
         if (c + e < len) o[c + e] = v[k][e];
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < len && v[k][e] > -__builtin_inff()) key = max_u64(key, argmax_key(v[k][e], base + c + e));
   }
   if (a.best) {
+    // the thread's largest value, the first of equal ones: its elements' places grow with k and e
+    float high = -__builtin_inff();
+    int at = -1;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = 4 * (tid + k * T) + e;
+        const bool more = c < len && v[k][e] > high;
+        high = more ? v[k][e] : high;
+        at = more ? c : at;
+      }
+    if (at >= 0) key = argmax_key(high, base + at);
     key = block_max<T / kWave>(key);
     if (tid == 0) a.best[row * slices + slice] = key;
   }
@@ -215,7 +257,10 @@ hipError_t launch_penalize_logits(const float* logits, const int32_t* request, c
                         frequency, presence, static_cast<int>(requests), drafts, row_start, ancestors, bias_start,
                         bias_token, bias_value, bias_entries, grammar, grammar_row, states, m, n, out,
                         token ? reinterpret_cast<unsigned long long*>(workspace) : nullptr};
-  constexpr int kT = 512, kV = 4;
+  // 4,096 tokens a workgroup: 64 rows of 151,936 (histories of 2,000, biases, grammars) take 25.9 us and one row (8,000)
+  // 7.2; with 8,192 of 512 threads 26.2 and 8.5, of 256 threads 32.6 and 12.9, with 2,048 of 256 threads 25.3 and 7.7,
+  // of 1,024 threads 36.5 and 7.0
+  constexpr int kT = 512, kV = 2;
   const int64_t slices = (n + 4 * kV * kT - 1) / (4 * kV * kT);
   hipLaunchKernelGGL((penalize_kernel<kT, kV>), dim3(static_cast<unsigned>(m * slices)), dim3(kT), 0, stream, a,
                      static_cast<int>(slices));
