@@ -568,7 +568,7 @@ int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16
  *   row_start   [requests + 1] int32 out
  *   request     [m] int32 out: the row's request
  *   position    [m] int32 out: the length plus the number of rows between the
- *               cached tokens and the row
+ *               cached tokens and the row (at most 2^31 - 1)
  *   slot        [m] int64 out: row c of request i is its token lengths[i] + c;
  *               -1 where its page is missing (the stack ran out, the table
  *               ended, or it held no page)
@@ -580,7 +580,7 @@ int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16
  * ancestors. So do, but for their request, the rows of a tree from the 64th
  * on. Calling it again on the same inputs gives the same tables: nothing is
  * taken from the stack until free_count is set to free_left.
- * table_width * page_size and pages * page_size stay below 2^31 and 2^40.
+ * table_width * page_size is at most 2^30, pages * page_size below 2^40.
  */
 int cache_plan(const int32_t* lengths, const int32_t* added, int64_t requests, int32_t* table, int64_t table_width,
                const int32_t* free_pages, int64_t free_capacity, const int32_t* free_count, int64_t pages,

@@ -27,7 +27,7 @@ bool bad_pages(int64_t pages, int64_t page_size) {
 }
 
 bool bad_table(int64_t requests, int64_t table_width, int64_t page_size) {
-  return requests < 1 || requests > PBG_MAX_REQUESTS || table_width < 1 || table_width > 0x7FFFFFFFLL / page_size;
+  return requests < 1 || requests > PBG_MAX_REQUESTS || table_width < 1 || table_width > (1LL << 30) / page_size;
 }
 
 // Heads of a step's m rows; the elements of a key head's page stay below 2^31.

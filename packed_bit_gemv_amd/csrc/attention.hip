@@ -43,6 +43,7 @@ struct AttnArgs {
   uint16_t* out;
   // heads of a key head that a tile takes, such groups of a key head, rows of a tile
   int group, chunks, rows;
+  int least, most;  // requests with fewer or more rows are not this launch's
   int4* parts;    // [workgroups]: first row, first head, rows and pieces of the work that a workgroup leaves to others
   float* states;  // [workgroups][2] tiles: outputs, then maxima and sums
 };
@@ -79,6 +80,7 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int i) {
   const int64_t room = static_cast<int64_t>(a.width) << a.shift;
   r.begin = s;
   r.rows = max(e - s, 0);
+  if (r.rows < a.least || r.rows > a.most) r.rows = 0;
   r.length = max(lengths[i], 0);
   const int64_t tokens = min(static_cast<int64_t>(r.length) + r.rows, room);
   r.tokens = static_cast<int>(tokens);
@@ -217,10 +219,25 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, int64_t me, Request
   return s;
 }
 
+// Places of a token's 16-byte pieces in LDS, such that 16 lanes that read the same piece of 16 tokens, and 32 lanes that
+// read 64 bytes of each of four tokens across, touch every bank once.
 template <int D>
-__device__ __forceinline__ int swizzled(int token, int chunk) {
-  if constexpr (D == 64) return chunk ^ (((token >> 1) & 3) << 1);
-  else return chunk ^ ((token & 7) << 1);
+__device__ __forceinline__ int key_piece(int token, int piece) {
+  if constexpr (D == 64) return piece ^ ((token >> 1) & 7);
+  else return piece ^ (token & 15);
+}
+
+template <int D>
+__device__ __forceinline__ int value_piece(int token, int piece) {
+  if constexpr (D == 64) return piece ^ (((token >> 1) & 1) << 2);
+  else return piece ^ ((token & 3) << 2);
+}
+
+// The same for 32 bytes of each of eight tokens.
+template <int D>
+__device__ __forceinline__ int narrow_piece(int token, int piece) {
+  if constexpr (D == 64) return piece ^ (((token >> 1) & 3) << 1);
+  else return piece ^ ((token & 7) << 1);
 }
 
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
@@ -249,6 +266,11 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 __device__ __forceinline__ float seen_or_none(float x, uint32_t mask, int n) {
   const uint32_t keep = static_cast<uint32_t>(static_cast<int32_t>(mask << (31 - n)) >> 31);
   return as_f32((as_u32(x) & keep) | (0xFF800000u & ~keep));
+}
+
+// 16 bytes at a wave's address and a lane's offset.
+__device__ __forceinline__ uint4 load16(const uint16_t* p, uint32_t bytes) {
+  return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) + bytes);
 }
 
 // Scale of a state with maximum m next to one with maximum `top`.
@@ -283,8 +305,8 @@ constexpr int kStep = 32;                // tokens a wave takes at once
 constexpr int kTokens = kWaves * kStep;  // tokens of a unit of work
 
 // Workgroups that a compute unit holds, and the launch's (as many as the chip holds), a power of two.
-constexpr int few_blocks(int d) { return d == 256 ? 1 : 2; }
-constexpr int few_bits(int d) { return d == 256 ? 8 : 9; }
+constexpr int few_blocks(int d, int qb) { return d == 256 || (d == 128 && qb > 1) ? 1 : 2; }
+constexpr int few_bits(int d, int qb) { return few_blocks(d, qb) == 1 ? 8 : 9; }
 
 // D: head_dim rounded up to 64, 128 or 256. QB: blocks of 16 query rows (a
 // query row is one head of one row of the step; the heads of a key
@@ -294,19 +316,23 @@ constexpr int few_bits(int d) { return d == 256 ? 8 : 9; }
 // share evenly, so that requests of any lengths fill the chip; a tile that ends
 // up with several workgroups is joined by a second kernel.
 //
-// A wave takes 32 tokens of a unit for all query rows, on its own: S^T = K Q^T
-// with keys straight from memory as the first operand, so that a lane
+// A wave takes 32 tokens of a unit for all query rows, on its own: S^T = K Q^T, so that a lane
 // holds one query row's scores (its maximum and sum need two lane swaps), and
-// the weights are then the second operand of O^T = V^T W^T as they are. V^T comes out
-// of LDS with transposing reads. The loads of the next unit are issued as soon as the scores are done.
+// the weights are then the second operand of O^T = V^T W^T as they are; V^T comes out
+// of LDS with transposing reads. Keys and values are loaded 1 KiB of consecutive bytes at a time and pass
+// through LDS that only the wave uses; the loads of the next unit are issued before the products of this one.
 template <int D, int QB>
-__global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, few_blocks(D, QB)) void attention_kernel(AttnArgs a) {
   constexpr int J = D / 32;       // products of 32 columns in a score
   constexpr int DB = D / 16;      // blocks of 16 columns of the output
   constexpr int kRow = D + 4;     // floats of a row where waves meet
+  constexpr int kChunks = D / 8;             // 16-byte pieces of a token's keys
+  constexpr int kGroup = kWave / kChunks;    // tokens that a wave loads at once
+  constexpr int kLoads = kStep / kGroup, kPages = kStep / kMinPage;
   constexpr int kStage = kStep * D * 2;
   constexpr int kMeet = 16 * kRow * 4;
-  constexpr int kSlice = kStage > kMeet ? kStage : kMeet;
+  constexpr int kSlice = 2 * kStage;
+  static_assert(kSlice >= kMeet && kMinPage % kGroup == 0, "room for a state, whole pages");
   __shared__ __attribute__((aligned(16))) char lds[kWaves * kSlice];
   __shared__ __attribute__((aligned(16))) _Float16 weights[kWaves][QB][kWave][8];  // for the rare path only
   __shared__ float meet_max[kWaves][QB * 16], meet_sum[kWaves][QB * 16];
@@ -315,7 +341,7 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int64_t me = blockIdx.x;
   Request r;
-  const Share line = share_of<kTokens, kWaves, few_bits(D)>(a, me, r);
+  const Share line = share_of<kTokens, kWaves, few_bits(D, QB)>(a, me, r);
   if (tid == 0) a.parts[me] = make_int4(0, 0, 0, 0);
   if (line.begin >= line.end) return;
   int request = line.request;
@@ -336,51 +362,40 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
     const int row0 = r.begin + here.tile * a.rows;
     const int tile_rows = min(a.rows, r.rows - here.tile * a.rows);
 
-    const int32_t* table = a.table + static_cast<int64_t>(request) * a.width;
+    const const_int_t* table = (const const_int_t*)(a.table + static_cast<int64_t>(request) * a.width);
     const int64_t page_elements = (static_cast<int64_t>(a.kv_heads) << a.shift) * a.d;
     const int64_t head_at = (static_cast<int64_t>(kvh) << a.shift) * a.d;
-    char* slice = lds + wave * kSlice;
-    // page of a token, or -1
-    auto page_of = [&](int t) -> int {
-      const int page = t < r.tokens ? table[t >> a.shift] : -1;
-      return page >= 0 && page < a.pages ? page : -1;
-    };
-    // where a token lies in k and v (in elements)
-    auto place = [&](int page, int t) -> int64_t {
-      return page * page_elements + head_at + static_cast<int64_t>(t & ((1 << a.shift) - 1)) * a.d;
-    };
-    const int lane_t = wave * kStep + li;
-    int page[2];
-    uint4 kr[2][J], vr[2][J];
-    uint32_t held = 0, held_next = 0;  // tokens that have a place, one bit each
+    const int page_mask = (1 << a.shift) - 1;
+    char* key_slice = lds + wave * kSlice;
+    char* value_slice = key_slice + kStage;
+    // Eight tokens that follow one another are of one page, so that page numbers and addresses are the wave's, not a
+    // lane's. Columns past head_dim are loaded as column 0 and made zero in the keys; tokens without a page are loaded
+    // from the first page and made zero.
+    const int load_t = lane / kChunks, load_c = lane % kChunks;
+    const uint32_t lane_at = 2 * (load_t * a.d + (8 * load_c < a.d ? 8 * load_c : 0));  // in bytes
+    int page[kPages], page_next[kPages];
+    uint4 kr[kLoads], vr[kLoads];
     auto fetch_pages = [&](int s) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) page[b] = page_of(s * kTokens + lane_t + 16 * b);
-    };
-    int64_t from[2];
-    auto fetch_values = [&](int s) {
-      held_next = static_cast<uint32_t>(__ballot(page[0] >= 0) & 0xFFFFu) |
-                  static_cast<uint32_t>(__ballot(page[1] >= 0) & 0xFFFFu) << 16;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        from[b] = page[b] >= 0 ? place(page[b], s * kTokens + lane_t + 16 * b) : -1;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const int c = 8 * (4 * j + lg);
-          vr[b][j] = make_uint4(0, 0, 0, 0);
-          if (from[b] >= 0 && c < a.d) vr[b][j] = *reinterpret_cast<const uint4*>(a.v + from[b] + c);
-        }
+      for (int g = 0; g < kPages; ++g) {
+        const int t = s * kTokens + wave * kStep + g * kMinPage;
+        const int found = table[static_cast<uint32_t>(min(t >> a.shift, a.width - 1))];
+        page_next[g] = t < r.tokens && static_cast<uint32_t>(found) < static_cast<uint32_t>(a.pages) ? found : -1;
       }
     };
-    auto fetch_keys = [&]() {
+    auto fetch = [&](int s) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int g = 0; g < kPages; ++g) {
+        page[g] = page_next[g];
+        const int t = s * kTokens + wave * kStep + g * kMinPage;
+        const int64_t from = max(page[g], 0) * page_elements + head_at + (t & page_mask) * a.d;
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const int c = 8 * (4 * j + lg);
-          kr[b][j] = make_uint4(0, 0, 0, 0);
-          if (from[b] >= 0 && c < a.d) kr[b][j] = *reinterpret_cast<const uint4*>(a.k + from[b] + c);
+        for (int i = 0; i < kLoads / kPages; ++i) {
+          const int64_t at = from + i * kGroup * a.d;
+          kr[g * (kLoads / kPages) + i] = load16(a.k + at, lane_at);
+          vr[g * (kLoads / kPages) + i] = load16(a.v + at, lane_at);
         }
+      }
     };
     fetch_pages(step0);
 
@@ -404,8 +419,7 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
         q[b][j] = __builtin_bit_cast(mfma_half8_t, w);
       }
     }
-    fetch_values(step0);
-    fetch_keys();
+    fetch(step0);
     fetch_pages(step0 + 1);
     float top[QB], part[QB];
     f32x4_t o[QB][DB];
@@ -420,53 +434,54 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
     for (int s = step0; s < step1; ++s) {
       const int t0 = s * kTokens + wave * kStep;
       if (t0 >= r.tokens) break;
-      held = held_next;
+      uint32_t held = 0;  // tokens that have a place, one bit each
+#pragma unroll
+      for (int g = 0; g < kPages; ++g) held |= page[g] >= 0 ? 0xFFu << (8 * g) : 0u;
       // whether any row may not see a token of these, and values that must reach only rows that see them
       const bool masked = t0 + kStep > r.length || held != 0xFFFFFFFFu;
       uint32_t wild = 0;
       if (masked) {
+        held &= static_cast<uint32_t>(ones_below(r.tokens - t0));
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint32_t any = 0;
+        for (int n = 0; n < kLoads; ++n) {
+          __builtin_amdgcn_sched_barrier(0);  // one after the other, for the registers' sake
+          uint4& w = vr[n];
+          if (page[n / (kLoads / kPages)] < 0) kr[n] = w = make_uint4(0, 0, 0, 0);
+          const uint4 x = make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w));
+          const uint64_t lanes = __ballot((x.x | x.y | x.z | x.w) != 0);
+          w = make_uint4(w.x & ~x.x, w.y & ~x.y, w.z & ~x.z, w.w & ~x.w);
 #pragma unroll
-          for (int j = 0; j < J; ++j) {
-            uint4& w = vr[b][j];
-            const uint4 n = make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w));
-            any |= n.x | n.y | n.z | n.w;
-            w = make_uint4(w.x & ~n.x, w.y & ~n.y, w.z & ~n.z, w.w & ~n.w);
-          }
-          const uint64_t lanes = __ballot(any != 0);
-          const uint32_t tokens = static_cast<uint32_t>((lanes | lanes >> 16 | lanes >> 32 | lanes >> 48) & 0xFFFFu);
-          wild |= tokens << (16 * b);
+          for (int t = 0; t < kGroup; ++t)
+            if (lanes >> (t * kChunks) & ones_below(kChunks)) wild |= 1u << (n * kGroup + t);
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int t = 16 * b + li;
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-          *reinterpret_cast<uint4*>(slice + t * (D * 2) + swizzled<D>(t, 4 * j + lg) * 16) = vr[b][j];
+      for (int n = 0; n < kLoads; ++n) {
+        const int t = n * kGroup + load_t;
+        if (a.d != D && 8 * load_c >= a.d) kr[n] = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(key_slice + t * (D * 2) + key_piece<D>(t, load_c) * 16) = kr[n];
+        *reinterpret_cast<uint4*>(value_slice + t * (D * 2) + narrow_piece<D>(t, load_c) * 16) = vr[n];
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      // the values' registers are free from here on, the keys' after the scores
-      if (s + 1 < step1) fetch_values(s + 1);
+      // the registers are free from here on
+      if (s + 1 < step1) {
+        fetch(s + 1);
+        fetch_pages(s + 2);
+      }
 
       mfma_float4_t x[QB][2];
 #pragma unroll
-      for (int b = 0; b < QB; ++b)
+      for (int b = 0; b < QB; ++b) x[b][0] = x[b][1] = mfma_float4_t{};
+#pragma unroll
+      for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          x[b][h] = mfma_float4_t{};
+          const int t = 16 * h + li;
+          const auto k = *reinterpret_cast<const mfma_half8_t*>(key_slice + t * (D * 2) + key_piece<D>(t, 4 * j + lg) * 16);
 #pragma unroll
-          for (int j = 0; j < J; ++j)
-            x[b][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(mfma_half8_t, kr[h][j]), q[b][j], x[b][h],
-                                                             0, 0, 0);
+          for (int b = 0; b < QB; ++b) x[b][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[b][j], x[b][h], 0, 0, 0);
         }
-      if (s + 1 < step1) {
-        fetch_keys();
-        fetch_pages(s + 2);
-      }
       mfma_half8_t w[QB];
       uint32_t seen[QB];
 #pragma unroll
@@ -511,7 +526,7 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
         for (int h = 0; h < 2; ++h) {
           const int t = 16 * h + 4 * lg + li / 4, c = 2 * e + (li & 3) / 2;
           const auto v4 = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_short4_t*)(slice + t * (D * 2) + swizzled<D>(t, c) * 16 + (li & 1) * 8)));
+              (lds_short4_t*)(value_slice + t * (D * 2) + narrow_piece<D>(t, c) * 16 + (li & 1) * 8)));
 #pragma unroll
           for (int y = 0; y < 4; ++y) v[4 * h + y] = v4[y];
         }
@@ -527,7 +542,7 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
       while (wild) {
         const int n = __builtin_ctz(wild);
         wild &= wild - 1;
-        const int64_t p = place(page_of(t0 + n), t0 + n);
+        const int64_t p = table[static_cast<uint32_t>((t0 + n) >> a.shift)] * page_elements + head_at + ((t0 + n) & page_mask) * a.d;
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
           // element (n / 16) * 4 + n % 4 of the lane that holds the token
@@ -560,7 +575,7 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
 #pragma unroll
       for (int y = 1; y < kWaves; ++y) high = fmaxf(high, meet_max[y][n]);
       const float keep = weight_of(top[b], high);
-      float* to = reinterpret_cast<float*>(slice) + li * kRow;
+      float* to = reinterpret_cast<float*>(key_slice) + li * kRow;
 #pragma unroll
       for (int e = 0; e < DB; ++e) *reinterpret_cast<f32x4_t*>(to + 16 * e + 4 * lg) = o[b][e] * keep;
       __syncthreads();
@@ -607,20 +622,6 @@ __global__ __launch_bounds__(kThreads, few_blocks(D)) void attention_kernel(Attn
 
 constexpr int kWide = 64;  // tokens of a unit of work
 constexpr int kWideBits = 8;  // one workgroup on each compute unit
-
-// Places of a token's 16-byte pieces in LDS, such that 16 lanes that read the same piece of 16 tokens, and 32 lanes that
-// read 64 bytes of each of four tokens across, touch every bank once.
-template <int D>
-__device__ __forceinline__ int key_piece(int token, int piece) {
-  if constexpr (D == 64) return piece ^ ((token >> 1) & 7);
-  else return piece ^ (token & 15);
-}
-
-template <int D>
-__device__ __forceinline__ int value_piece(int token, int piece) {
-  if constexpr (D == 64) return piece ^ (((token >> 1) & 1) << 2);
-  else return piece ^ ((token & 3) << 2);
-}
 
 // NB: blocks of 32 query rows a wave; the W waves have rows of their own
 // and share the tokens, 64 at a time, through LDS, with the next 64 on their way in registers. The products are
@@ -690,7 +691,7 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
     // numbers and addresses are the wave's, not a lane's. Columns past head_dim are loaded as column 0 and
     // made zero in the keys; tokens without a page are loaded from the first page and made zero.
     const int load_t = lane / kChunks, load_c = lane % kChunks;
-    const uint32_t lane_at = load_t * a.d + (8 * load_c < a.d ? 8 * load_c : 0);
+    const uint32_t lane_at = 2 * (load_t * a.d + (8 * load_c < a.d ? 8 * load_c : 0));  // in bytes
     int page[kPages], page_next[kPages];
     uint4 kr[kPasses], vr[kPasses];
     auto fetch_pages = [&](int s) {
@@ -707,12 +708,11 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
         page[g] = page_next[g];
         const int t = s * kWide + wave * kMine + g * kMinPage;
         const int64_t from = max(page[g], 0) * page_elements + head_at + (t & page_mask) * a.d;
-        const uint16_t* k = a.k + from;
-        const uint16_t* v = a.v + from;
 #pragma unroll
         for (int i = 0; i < kPasses / kPages; ++i) {
-          kr[g * (kPasses / kPages) + i] = *reinterpret_cast<const uint4*>(k + (lane_at + i * kGroup * a.d));
-          vr[g * (kPasses / kPages) + i] = *reinterpret_cast<const uint4*>(v + (lane_at + i * kGroup * a.d));
+          const int64_t at = from + i * kGroup * a.d;
+          kr[g * (kPasses / kPages) + i] = load16(a.k + at, lane_at);
+          vr[g * (kPasses / kPages) + i] = load16(a.v + at, lane_at);
         }
       }
     };
@@ -1005,14 +1005,14 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
 // Joins the pieces of the tiles of R query rows that several of N workgroups had. Every
 // workgroup counts the jobs, four query rows of a tile each, and takes its
 // share of them (a workgroup for each that could be, most of them with nothing to do, took 9 us for 4,096). A wave has 16 lanes
-// a row and merges pieces as they come, the loads of several in flight. With SHARE the
+// a row and merges pieces as they come, the loads of AHEAD in flight. With SHARE the
 // workgroup's waves share the pieces of the same four rows (few rows, many
 // pieces), otherwise each has rows of its own.
-template <int D, int R, int N, bool SHARE>
-__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
+template <int D, int R, int N, bool SHARE, int AHEAD>
+__device__ __forceinline__ void join(const AttnArgs& a, int block, int blocks) {
   constexpr int64_t kState = R * (D + 2);
   constexpr int V = D / 64;  // groups of four columns a lane
-  constexpr int kAhead = SHARE ? 16 / V : 4;
+  constexpr int kAhead = AHEAD;
   constexpr int kEach = N / kThreads;
   __shared__ __attribute__((aligned(16))) float acc_at[SHARE ? kWaves : 1][4][D];
   __shared__ float top_at[kWaves][4], sum_at[kWaves][4];
@@ -1037,11 +1037,11 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
     }
     __syncthreads();
   } else {
-    jobs = jobs_of(a.parts[blockIdx.x]);
+    jobs = jobs_of(a.parts[block]);
   }
-  const int step = !kCounts ? 1 : SHARE ? gridDim.x : gridDim.x * kWaves;
-  for (int job = !kCounts ? 0 : SHARE ? blockIdx.x : blockIdx.x * kWaves + wave; job < jobs; job += step) {
-    int64_t me = blockIdx.x;
+  const int step = !kCounts ? 1 : SHARE ? blocks : blocks * kWaves;
+  for (int job = !kCounts ? 0 : SHARE ? block : block * kWaves + wave; job < jobs; job += step) {
+    int64_t me = block;
     int n = job * 4 + lg;
     if constexpr (kCounts) {
       int lo = 0, hi = N - 1;  // the first workgroup whose jobs end behind this one
@@ -1118,54 +1118,96 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
   }
 }
 
+template <int D, int R, int N, bool SHARE>
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
+  join<D, R, N, SHARE, SHARE ? 1024 / D : 4>(a, blockIdx.x, gridDim.x);
+}
+
+// For both kernels at once: the first N workgroups join tiles of 16 query rows, the others those of R.
+template <int D, int N, int R, int M>
+__global__ __launch_bounds__(kThreads) void attention_join_both_kernel(AttnArgs few, AttnArgs wide) {
+  if (blockIdx.x < N) join<D, 16, N, true, 4>(few, blockIdx.x, N);
+  else join<D, R, M, false, 4>(wide, blockIdx.x - N, gridDim.x - N);
+}
+
 // Workgroups of a launch: as many as the chip holds at once.
-constexpr int kGroups = 1 << few_bits(64);
+constexpr int kGroups = 1 << few_bits(64, 1);
 constexpr int kWideGroups = 1 << kWideBits;
 constexpr int kJoinGroups = 256;
 
 constexpr int wide_waves(int d) { return d == 256 ? 4 : 8; }
 
+// The sizes of tiles of R query rows, and their part of the workspace.
+AttnArgs with_tiles(AttnArgs a, int r, void* ws) {
+  const int ratio = a.heads / a.kv_heads;
+  a.group = ratio < r ? ratio : r;
+  a.chunks = (ratio + a.group - 1) / a.group;
+  a.rows = 1 << (31 - __builtin_clz(r / a.group));
+  a.parts = static_cast<int4*>(ws);
+  a.states = reinterpret_cast<float*>(static_cast<char*>(ws) + kGroups * sizeof(int4));
+  return a;
+}
+
+constexpr int64_t workspace_of(int groups, int r, int d) {
+  return kGroups * sizeof(int4) + static_cast<int64_t>(groups) * 2 * r * (d + 2) * sizeof(float);
+}
+
 template <int D, int QB>
-hipError_t launch_tiles(AttnArgs a, void* ws, hipStream_t stream) {
-  const int ratio = a.heads / a.kv_heads;
-  a.group = ratio < QB * 16 ? ratio : QB * 16;
-  a.chunks = (ratio + a.group - 1) / a.group;
-  a.rows = 1 << (31 - __builtin_clz(QB * 16 / a.group));
-  a.parts = static_cast<int4*>(ws);
-  a.states = reinterpret_cast<float*>(static_cast<char*>(ws) + kGroups * sizeof(int4));
-  constexpr int groups = 1 << few_bits(D);
+hipError_t launch_few(const AttnArgs& args, void* ws, hipStream_t stream) {
+  constexpr int groups = 1 << few_bits(D, QB);
+  const AttnArgs a = with_tiles(args, QB * 16, ws);
   hipLaunchKernelGGL((attention_kernel<D, QB>), dim3(groups), dim3(kThreads), 0, stream, a);
-  hipLaunchKernelGGL((attention_join_kernel<D, QB * 16, groups, true>), dim3(QB == 1 ? groups : kJoinGroups), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attention_join_kernel<D, QB * 16, groups, true>), dim3(QB == 1 ? groups : kJoinGroups),
+                     dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
+// Without a tree, requests with at most 16 query rows a key head go through the kernel for few rows, also here: single
+// tokens beside a prompt. 63 tokens of requests of 4,096 beside a prompt of 1,024 rows take 256 us, all through the wide
+// kernel 422. Where there are none the launch costs 7 us with its part of the join (of 771 for 4,096 rows over 8,192
+// tokens), which trees, whose sizes are alike, do not pay (16 trees of 30 to 61 rows: 87 us, 94 with it), nor does one request.
 template <int D>
-hipError_t launch_wide(AttnArgs a, void* ws, hipStream_t stream) {
-  constexpr int W = wide_waves(D), R = W * 32;
-  const int ratio = a.heads / a.kv_heads;
-  a.group = ratio < R ? ratio : R;
-  a.chunks = (ratio + a.group - 1) / a.group;
-  a.rows = 1 << (31 - __builtin_clz(R / a.group));
-  a.parts = static_cast<int4*>(ws);
-  a.states = reinterpret_cast<float*>(static_cast<char*>(ws) + kGroups * sizeof(int4));
-  hipLaunchKernelGGL((attention_wide_kernel<D, 1, W>), dim3(kWideGroups), dim3(W * kWave), 0, stream, a);
-  hipLaunchKernelGGL((attention_join_kernel<D, R, kWideGroups, false>), dim3(8 * kJoinGroups), dim3(kThreads), 0, stream, a);
+hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
+  constexpr int W = wide_waves(D), R = W * 32, groups = 1 << few_bits(D, 1);
+  AttnArgs few = with_tiles(args, 16, ws);
+  AttnArgs wide = with_tiles(args, R, static_cast<char*>(ws) + workspace_of(groups, 16, D));
+  const bool both = !args.ancestors && args.requests > 1;
+  if (both) {
+    few.most = 16 / (args.heads / args.kv_heads);
+    wide.least = few.most + 1;
+    hipLaunchKernelGGL((attention_kernel<D, 1>), dim3(groups), dim3(kThreads), 0, stream, few);
+  }
+  hipLaunchKernelGGL((attention_wide_kernel<D, 1, W>), dim3(kWideGroups), dim3(W * kWave), 0, stream, wide);
+  if (both)
+    hipLaunchKernelGGL((attention_join_both_kernel<D, groups, R, kWideGroups>), dim3(groups + 8 * kJoinGroups),
+                       dim3(kThreads), 0, stream, few, wide);
+  else
+    hipLaunchKernelGGL((attention_join_kernel<D, R, kWideGroups, false>), dim3(8 * kJoinGroups), dim3(kThreads), 0,
+                       stream, wide);
   return hipGetLastError();
 }
 
+// Which kernel, by the query rows of a key head that a request has on average. Eight requests of up to 8,192 tokens at
+// head_dim 128: 20 rows take 74.5 us in tiles of 16, 61.7 in tiles of 32 and 62.5 in the wide kernel; 28 rows 90.1, 62.4 and
+// 63.0; 48 rows 93.9 in tiles of 48, 128.6 in tiles of 64 and 67.4 in the wide kernel. One row each of 64 requests: 217 us in
+// tiles of 16, 291 in tiles of 32, 829 wide. At head_dim 256, where a tile of 32 does not fit the registers, 32 rows take 45 us
+// in tiles of 16, 66 in tiles of 32 and 68 wide.
 template <int D>
 hipError_t launch_rows(const AttnArgs& a, int64_t rows, void* ws, hipStream_t stream) {
-  if (rows <= 16) return launch_tiles<D, 1>(a, ws, stream);
-  if (rows <= 32) return launch_tiles<D, 2>(a, ws, stream);
+  if (rows <= (D == 256 ? 32 : 16)) return launch_few<D, 1>(a, ws, stream);
+  if constexpr (D < 256) {
+    if (rows <= 32) return launch_few<D, 2>(a, ws, stream);
+  }
   return launch_wide<D>(a, ws, stream);
 }
 
 }  // namespace
 
 int64_t attention_workspace_bytes(int head_dim) {
-  const int64_t d = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  const int64_t few = kGroups * 2 * 32 * (d + 2) * 4, wide = kWideGroups * 2 * 32 * wide_waves(d) * (d + 2) * 4;
-  return kGroups * 16 + (few > wide ? few : wide);
+  const int d = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+  const int64_t two = d == 256 ? 0 : workspace_of(1 << few_bits(d, 2), 32, d);
+  const int64_t both = workspace_of(1 << few_bits(d, 1), 16, d) + workspace_of(kWideGroups, 32 * wide_waves(d), d);
+  return two > both ? two : both;
 }
 
 hipError_t launch_tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages,
@@ -1175,7 +1217,7 @@ hipError_t launch_tree_attention(const uint16_t* q, const uint16_t* k_cache, con
                                  hipStream_t stream) {
   const AttnArgs a = {q, k_cache, v_cache, pages, page_shift(page_size), table, static_cast<int>(table_width), lengths,
                       row_start, static_cast<int>(requests), ancestors, static_cast<int>(m), heads, kv_heads, head_dim,
-                      scale * kLog2e, out, 0, 0, 0, nullptr, nullptr};
+                      scale * kLog2e, out, 0, 0, 0, 0, 0x7FFFFFFF, nullptr, nullptr};
   // query rows of a key head that a request has on average
   const int64_t rows = (m * (heads / kv_heads) + requests - 1) / requests;
   if (head_dim <= 64) return launch_rows<64>(a, rows, workspace, stream);
