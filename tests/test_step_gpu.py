@@ -379,6 +379,36 @@ def test_attention_long_context_in_pieces(pbg, heads, kv, d, rows):
     check_attention(pbg, attention_case(d, [9000, 12, 14001], [rows, 2, 1], heads, kv, d, 64))
 
 
+def test_attention_pieces_of_both_kernels(pbg):
+    """Single tokens of long requests beside prompts, each in several pieces, with up to and with more than 64 requests."""
+    check_attention(pbg, attention_case(4, [9000, 700, 0, 12001], [1, 250, 130, 2], 4, 1, 64, 16, pad=4))
+    check_attention(pbg, attention_case(5, [6000, 300], [1, 140], 6, 1, 128, 32))
+    check_attention(pbg, attention_case(6, [6000, 300], [1, 140], 8, 1, 256, 32))
+    many = [int(x) for x in np.random.default_rng(7).integers(0, 300, 90)]
+    check_attention(pbg, attention_case(7, many, [700 if i == 50 else 40 if i % 30 == 0 else i % 3 for i in range(90)], 8, 1, 64, 16))
+
+
+def test_attention_trees_with_more_rows_than_a_tree_has(pbg):
+    """Of a request's rows from the 64th on none is seen; those rows themselves see what their masks say."""
+    c = attention_case(8, [20, 7], [100, 3], 4, 2, 64, 16, tree=True)
+    c["ancestors"][64:100] = np.random.default_rng(1).integers(0, 2 ** 63, 36).astype(np.uint64)
+    check_attention(pbg, c)
+    c["ancestors"][:] = np.uint64(2 ** 64 - 1)
+    check_attention(pbg, c)
+
+
+def test_attention_refusals_of_the_binding(pbg):
+    c = {k: dev(v) for k, v in attention_case(9, [20, 7], [2, 3], 4, 2, 64, 16).items()}
+    for bad in (dict(q=c["q"][:, :, :32]), dict(q=c["q"].transpose(0, 1)), dict(lengths=c["lengths"][:1]), dict(lengths=c["lengths"].long()),
+                dict(row_start=c["row_start"][:2]), dict(table=c["table"].cpu()), dict(v_cache=c["v_cache"][:1]), dict(ancestors=c["lengths"]),
+                dict(out=torch.empty_like(c["q"]).float()), dict(workspace=torch.empty(4))):
+        with pytest.raises(ValueError):
+            pbg.tree_attention(**{**c, **bad})
+    for bad in (dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda:0")), dict(scale=0.0), dict(scale=NAN)):
+        with pytest.raises(pbg.PbgError):
+            pbg.tree_attention(**{**c, **bad})
+
+
 def test_attention_sharp_scores(pbg):
     """A few tokens hold all the weight, the largest score comes late or early, and weights fall below fp16's range."""
     for scale in (0.01, 1.0, 30.0):
