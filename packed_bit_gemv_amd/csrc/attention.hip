@@ -664,14 +664,29 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   int request = line.request;
   int64_t base = line.base;
 
-  for (int64_t at = line.begin; at < line.end;) {
+  // The end of a tile that another workgroup began comes last: all then walk the tokens from the first on at about the same
+  // time, and find the keys that they share in the cache.
+  const Place begun = place_of(r, line.begin - base);
+  const int64_t begun_end = begun.step == 0 ? line.begin : min(line.begin + begun.steps - begun.step, line.end);
+  int64_t stop = line.end;
+  bool done = begun_end == line.begin;  // with that end
+  for (int64_t at = begun_end;;) {
+    if (at == stop) {
+      if (done) break;
+      done = true;
+      at = line.begin;
+      stop = begun_end;
+      request = line.request;
+      base = line.base;
+      r = request_of<kWide>(a, request);
+    }
     while (at >= base + r.units) {
       base += r.units;
       r = request_of<kWide>(a, ++request);
     }
     const Place here = place_of(r, at - base);
     const int step0 = static_cast<int>(here.step);
-    const int step1 = static_cast<int>(min(here.step + (line.end - at), here.steps));
+    const int step1 = static_cast<int>(min(here.step + (stop - at), here.steps));
     const int kvh = here.head / a.chunks, chunk = here.head - kvh * a.chunks;
     const int ratio = a.heads / a.kv_heads;
     const int head0 = kvh * ratio + chunk * a.group;
