@@ -16,7 +16,10 @@ constexpr int kParts = 8;  // of the chip; workgroups go to them in turn
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -__builtin_inff();
 // A running maximum is only raised when a score passes it by this much (in powers of two): weights then reach 2^8,
-// far inside fp16, and the sums are hardly ever scaled.
+// far inside fp16, and the sums are hardly ever scaled. Weights are rounded to fp16 for the second product, to half a
+// step each (2^-11), independent of one another and no more than the output's own rounding: against 64 bits both together
+// are 1.38 times the latter alone (1.07 with a maximum that is always raised, whose largest weights are exactly 1). The sum
+// of the weights is that of the unrounded ones: of the rounded ones the wide kernel is 13 % slower, and 1.30 times.
 constexpr float kSlack = 8.0f;
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
