@@ -643,9 +643,9 @@ int rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, c
  *   scale      > 0, and finite also times log2(e)
  *   out        [m][heads][head_dim] fp16 bits out, 16-byte aligned
  *   workspace  device, 16-byte aligned, pbg_attention_workspace_bytes(...)
- *              bytes, of any content; one serves any number of rows and
- *              requests and fewer heads, and calls of many graphs that do not overlap
- *              in time
+ *              bytes, of any content; one serves any number of rows,
+ *              requests and heads and narrower heads, and any calls that do
+ *              not overlap in time
  * Heads and head_dim as for rotary_qkv; page_size at least
  * PBG_ATTENTION_MIN_PAGE. Scores, weights' sums and the output's sums are fp32; the weights enter the
  * second product rounded to fp16 relative to the row's largest.

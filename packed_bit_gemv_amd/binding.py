@@ -697,14 +697,10 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, ids: torch.Tensor, a: torch.Tenso
     return out
 
 
-def _given(index: int, t, name: str, dtype: torch.dtype, shape: tuple):
-    """Address of t as _on has it, or None for None."""
-    return None if t is None else _on(index, t, name, dtype, shape)
-
-
-def _masks(index: int, t, name: str, m: int):
-    """Address of an int64 or uint64 [m] tensor of bit masks, or None."""
-    return _given(index, t, name, t.dtype if t is not None and t.dtype is torch.uint64 else torch.int64, (m,))
+def _masks(index: int, t, m: int) -> int:
+    """Address of ancestors, an int64 or uint64 [m] tensor of bit masks."""
+    unsigned = isinstance(t, torch.Tensor) and t.dtype is torch.uint64
+    return _on(index, t, "ancestors", torch.uint64 if unsigned else torch.int64, (m,))
 
 
 def _cache(k_cache, v_cache):
@@ -732,9 +728,9 @@ def cache_plan(lengths: torch.Tensor, added: torch.Tensor, table: torch.Tensor, 
     lengths, added int32 [requests]: the tokens that each request has in the cache and the rows that it adds. table
     int32 [requests, width] is read and, for pages that the step opens, written; free_pages int32 [n] is a stack of
     free pages with free_count int32 [1] of them left, free_left int32 [1] what the step leaves. parents int32 [rows]
-    makes each request's rows a tree of drafted tokens (of at most 64). The step has as many rows as the outputs that are given, or
-    `rows`: request, position int32 [rows], slot int64 [rows] (-1 for rows behind the last request), row_start int32
-    [requests + 1], ancestors int64 [rows] (bit masks over the request's rows; allocated for a tree).
+    makes each request's rows a tree of drafted tokens (of at most 64). The step has as many rows as the outputs that
+    are given, or `rows`: request, position int32 [rows], slot int64 [rows] (-1 for rows behind the last request),
+    row_start int32 [requests + 1], ancestors int64 [rows] (bit masks over the request's rows; allocated for a tree).
     """
     i32, i64 = torch.int32, torch.int64
     requests, width, dev = _matrix(table, "table", i32)
@@ -758,20 +754,23 @@ def cache_plan(lengths: torch.Tensor, added: torch.Tensor, table: torch.Tensor, 
     _call("cache_plan", lib().cache_plan, dev, _on(dev, lengths, "lengths", i32, (requests,)),
           _on(dev, added, "added", i32, (requests,)), requests, table.data_ptr(), width,
           _on(dev, free_pages, "free_pages", i32, (capacity,)), capacity,
-          _on(dev, free_count, "free_count", i32, (1,)), pages, page_size, _given(dev, parents, "parents", i32, (m,)), m,
+          _on(dev, free_count, "free_count", i32, (1,)), pages, page_size,
+          None if parents is None else _on(dev, parents, "parents", i32, (m,)), m,
           _on(dev, row_start, "row_start", i32, (requests + 1,)), _on(dev, request, "request", i32, (m,)),
           _on(dev, position, "position", i32, (m,)), _on(dev, slot, "slot", i64, (m,)),
-          _masks(dev, ancestors, "ancestors", m), _on(dev, free_left, "free_left", i32, (1,)))
+          None if ancestors is None else _masks(dev, ancestors, m), _on(dev, free_left, "free_left", i32, (1,)))
     return row_start, request, position, slot, ancestors, free_left
 
 
 def rotary_frequencies(rotary_dim: int, base: float = 1e6, scaling: str | None = None, factor: float = 1.0,
                        original_length: int = 32768, device="cuda"):
-    """(inv_freq fp64 [rotary_dim / 2], amplitude) of rotary_qkv: base ** (-2 j / rotary_dim), scaled for contexts `factor` times as long.
+    """(inv_freq fp64 [rotary_dim / 2], amplitude) of rotary_qkv: base ** (-2 j / rotary_dim), scaled for contexts
+    `factor` times as long.
 
     scaling: None; "linear", positions divided by the factor; "ntk", the base raised so that the slowest pair turns
-    factor times slower and the fastest is kept; "yarn", pairs that turn more than 32 times over original_length tokens kept, those
-    that turn less than once divided by the factor, a ramp over the pair's number in between, and an amplitude of 1 + 0.1 ln(factor).
+    factor times slower and the fastest is kept; "yarn", pairs that turn more than 32 times over original_length tokens
+    kept, those that turn less than once divided by the factor, a ramp over the pair's number in between, and an
+    amplitude of 1 + 0.1 ln(factor).
     """
     if rotary_dim < 0 or rotary_dim % 2 or not factor >= 1.0:
         raise ValueError("rotary_dim must be even and factor at least 1")
@@ -818,10 +817,10 @@ def rotary_qkv(qkv: torch.Tensor, position: torch.Tensor, slot: torch.Tensor, in
     _call("rotary_qkv", lib().rotary_qkv, dev, _on(dev, qkv, "qkv", torch.float32, (m, columns)),
           _on(dev, position, "position", torch.int32, (m,)), _on(dev, slot, "slot", torch.int64, (m,)),
           _on(dev, inv_freq, "inv_freq", torch.float64, (half,)) if half else None,
-          _given(dev, q_weight, "q_weight", torch.float32, (head_dim,)),
-          _given(dev, k_weight, "k_weight", torch.float32, (head_dim,)), eps, amplitude, int(interleaved), m, heads,
-          kv_heads, head_dim, 2 * half, _on(dev, q, "q", torch.float16, (m, heads, head_dim)), k_cache.data_ptr(),
-          v_cache.data_ptr(), pages, page_size)
+          None if q_weight is None else _on(dev, q_weight, "q_weight", torch.float32, (head_dim,)),
+          None if k_weight is None else _on(dev, k_weight, "k_weight", torch.float32, (head_dim,)), eps, amplitude,
+          int(interleaved), m, heads, kv_heads, head_dim, 2 * half,
+          _on(dev, q, "q", torch.float16, (m, heads, head_dim)), k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size)
     return q
 
 
@@ -839,9 +838,9 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
 
     q as rotary_qkv leaves it; k_cache, v_cache fp16 [pages, kv_heads, page_size, head_dim], which hold the step's own
     keys and values already; table int32 [requests, width]; lengths int32 [requests], the tokens before the step;
-    row_start int32 [requests + 1] and ancestors int64 [m] from cache_plan. Each row sees its request's tokens from before the
-    step, and of the step's own those of its ancestors, or without ancestors those up to itself. scale defaults
-    to 1 / sqrt(head_dim). A row that sees nothing is zero; rows behind the last request are left as they were.
+    row_start int32 [requests + 1] and ancestors int64 [m] from cache_plan. Each row sees its request's tokens from
+    before the step, and of the step's own those of its ancestors, or without ancestors those up to itself. scale
+    defaults to 1 / sqrt(head_dim). A row that sees nothing is zero; rows behind the last request are left as they were.
     """
     pages, kv_heads, page_size, head_dim, dev = _cache(k_cache, v_cache)
     try:
@@ -860,7 +859,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
           _on(dev, table, "table", torch.int32, (requests, width)), width,
           _on(dev, lengths, "lengths", torch.int32, (requests,)),
           _on(dev, row_start, "row_start", torch.int32, (requests + 1,)), requests,
-          _masks(dev, ancestors, "ancestors", m), m, heads, kv_heads, head_dim,
+          None if ancestors is None else _masks(dev, ancestors, m), m, heads, kv_heads, head_dim,
           head_dim ** -0.5 if scale is None else scale, _on(dev, out, "out", torch.float16, (m, heads, head_dim)),
           workspace.data_ptr(), workspace.nbytes)
     return out
@@ -913,13 +912,17 @@ def penalize_logits(logits: torch.Tensor, request: torch.Tensor, tokens: torch.T
           _on(dev, tokens, "tokens", i32, (requests, width)), width,
           _on(dev, prompt_length, "prompt_length", i32, (requests,)), _on(dev, length, "length", i32, (requests,)),
           _on(dev, repetition, "repetition", f32, (requests,)), _on(dev, frequency, "frequency", f32, (requests,)),
-          _on(dev, presence, "presence", f32, (requests,)), requests, _given(dev, drafts, "drafts", i32, (m,)),
-          _given(dev, row_start, "row_start", i32, (requests + 1,)), _masks(dev, ancestors, "ancestors", m),
-          _given(dev, bias_start, "bias_start", i32, (requests + 1,)), _given(dev, bias_token, "bias_token", i32, (entries,)),
-          _given(dev, bias_value, "bias_value", f32, (entries,)), entries,
-          _given(dev, grammar, "grammar", i32, (states, (n + 31) // 32)),
-          _given(dev, grammar_row, "grammar_row", i32, (m,)), states, m, n, _on(dev, out, "out", f32, (m, n)),
-          _given(dev, token, "token", i32, (m,)), _given(dev, top, "top", f32, (m,)),
+          _on(dev, presence, "presence", f32, (requests,)), requests,
+          None if drafts is None else _on(dev, drafts, "drafts", i32, (m,)),
+          None if row_start is None else _on(dev, row_start, "row_start", i32, (requests + 1,)),
+          None if ancestors is None else _masks(dev, ancestors, m),
+          None if bias_start is None else _on(dev, bias_start, "bias_start", i32, (requests + 1,)),
+          None if bias_token is None else _on(dev, bias_token, "bias_token", i32, (entries,)),
+          None if bias_value is None else _on(dev, bias_value, "bias_value", f32, (entries,)), entries,
+          None if grammar is None else _on(dev, grammar, "grammar", i32, (states, (n + 31) // 32)),
+          None if grammar_row is None else _on(dev, grammar_row, "grammar_row", i32, (m,)), states, m, n,
+          _on(dev, out, "out", f32, (m, n)), None if token is None else _on(dev, token, "token", i32, (m,)),
+          None if top is None else _on(dev, top, "top", f32, (m,)),
           None if token is None else workspace.data_ptr(), 0 if token is None else workspace.nbytes)
     return out, token, top
 

@@ -1221,11 +1221,16 @@ hipError_t launch_rows(const AttnArgs& a, int64_t rows, void* ws, hipStream_t st
 
 }  // namespace
 
+// For heads of this width and narrower ones.
 int64_t attention_workspace_bytes(int head_dim) {
-  const int d = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  const int64_t two = d == 256 ? 0 : workspace_of(1 << few_bits(d, 2), 32, d);
-  const int64_t both = workspace_of(1 << few_bits(d, 1), 16, d) + workspace_of(kWideGroups, 32 * wide_waves(d), d);
-  return two > both ? two : both;
+  int64_t most = 0;
+  for (int d = 64; d <= 256 && (d == 64 || d < 2 * head_dim); d *= 2) {
+    const int64_t two = d == 256 ? 0 : workspace_of(1 << few_bits(d, 2), 32, d);
+    const int64_t both = workspace_of(1 << few_bits(d, 1), 16, d) + workspace_of(kWideGroups, 32 * wide_waves(d), d);
+    most = most > two ? most : two;
+    most = most > both ? most : both;
+  }
+  return most;
 }
 
 hipError_t launch_tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages,
