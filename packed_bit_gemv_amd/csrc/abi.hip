@@ -475,7 +475,8 @@ int penalize_logits(const float* logits, const int32_t* request, const int32_t* 
     return PBG_ERR_NULL;
   if (m < 1 || m > PBG_MAX_ROWS || n < 1 || n > PBG_MAX_N || m * n > PBG_MAX_LOGITS || requests < 1 ||
       requests > PBG_MAX_REQUESTS || tokens_width < 1 || tokens_width > 1LL << 24 ||
-      (has_bias && (bias_entries < 1 || bias_entries > 0x7FFFFFFFLL)) || (has_grammar && (states < 1 || states > 0x7FFFFFFFLL)))
+      (has_bias && (bias_entries < 1 || bias_entries > 0x7FFFFFFFLL)) ||
+      (has_grammar && (states < 1 || states > 0x7FFFFFFFLL)))
     return PBG_ERR_SHAPE;
   if (misaligned(logits, 4) || misaligned(request, 4) || misaligned(tokens, 4) || misaligned(prompt_length, 4) ||
       misaligned(length, 4) || misaligned(repetition, 4) || misaligned(frequency, 4) || misaligned(presence, 4) ||

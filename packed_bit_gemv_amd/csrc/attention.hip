@@ -17,9 +17,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -__builtin_inff();
 // A running maximum is only raised when a score passes it by this much (in powers of two): weights then reach 2^8,
 // far inside fp16, and the sums are hardly ever scaled. Weights are rounded to fp16 for the second product, to half a
-// step each (2^-11), independent of one another and no more than the output's own rounding: against 64 bits both together
-// are 1.38 times the latter alone (1.07 with a maximum that is always raised, whose largest weights are exactly 1). The sum
-// of the weights is that of the unrounded ones: of the rounded ones the wide kernel is 13 % slower, and 1.30 times.
+// step each (2^-11), independent of one another and no more than the output's own rounding: against 64 bits both
+// together are 1.38 times the latter alone (1.07 with a maximum that is always raised, whose largest weights are
+// exactly 1). The sum of the weights is that of the unrounded ones: of the rounded ones the wide kernel is 13 %
+// slower, and 1.30 times.
 constexpr float kSlack = 8.0f;
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
@@ -84,7 +85,8 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int i) {
   r.begin = s;
   r.rows = max(e - s, 0);
   if (r.rows < a.least || r.rows > a.most) r.rows = 0;
-  r.length = max(lengths[i], 0);
+  // tokens past the table have no place, so that no sum of these leaves 32 bits
+  r.length = static_cast<int>(min(static_cast<int64_t>(max(lengths[i], 0)), room));
   const int64_t tokens = min(static_cast<int64_t>(r.length) + r.rows, room);
   r.tokens = static_cast<int>(tokens);
   r.tiles = (r.rows + a.rows - 1) / a.rows;
@@ -134,7 +136,10 @@ __device__ __forceinline__ Place place_of(const Request& r, int64_t in) {
 }
 
 // The workgroup's share of the line of all requests' units, [begin, end), and
-// the request r that begin lies in, with the units before it. 2^G workgroups of W waves.
+// the request r that begin lies in, with the units before it, for 2^G
+// workgroups of W waves. The lengths are on the GPU only: every workgroup adds
+// them up, which takes it about 1 us for up to 64 requests (2 us with a scan
+// by the whole workgroup).
 struct Share {
   int64_t begin, end, share, base;
   int request;
@@ -222,8 +227,8 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, int64_t me, Request
   return s;
 }
 
-// Places of a token's 16-byte pieces in LDS, such that 16 lanes that read the same piece of 16 tokens, and 32 lanes that
-// read 64 bytes of each of four tokens across, touch every bank once.
+// Places of a token's 16-byte pieces in LDS, such that 16 lanes that read the same piece of 16 tokens, and 32 lanes
+// that read 64 bytes of each of four tokens across, touch every bank once.
 template <int D>
 __device__ __forceinline__ int key_piece(int token, int piece) {
   if constexpr (D == 64) return piece ^ ((token >> 1) & 7);
@@ -319,11 +324,20 @@ constexpr int few_bits(int d, int qb) { return few_blocks(d, qb) == 1 ? 8 : 9; }
 // share evenly, so that requests of any lengths fill the chip; a tile that ends
 // up with several workgroups is joined by a second kernel.
 //
-// A wave takes 32 tokens of a unit for all query rows, on its own: S^T = K Q^T, so that a lane
-// holds one query row's scores (its maximum and sum need two lane swaps), and
-// the weights are then the second operand of O^T = V^T W^T as they are; V^T comes out
-// of LDS with transposing reads. Keys and values are loaded 1 KiB of consecutive bytes at a time and pass
-// through LDS that only the wave uses; the loads of the next unit are issued before the products of this one.
+// A wave takes 32 tokens of a unit for all query rows, on its own: S^T = K Q^T,
+// so that a lane holds one query row's scores (its maximum and sum need two
+// lane swaps), and the weights are then the second operand of O^T = V^T W^T as
+// they are; V^T comes out of LDS with transposing reads. Keys and values are
+// loaded 1 KiB of consecutive bytes at a time and pass through LDS that only
+// the wave uses; the loads of the next unit are issued before the products of
+// this one.
+//
+// Bound by the reads of the cache: 64 requests of 820 to 8,192 tokens, one row
+// each (32 heads over 8 of 128, 1.18 GB), take 217 us, 5.4 TB/s; the loads
+// alone take as long, a pure read of as many consecutive bytes 174. 7 rows over
+// 40,953 tokens (168 MB) take 38 us and 5 for the join, of which the reads are
+// 28. One token over 1,000 takes 8 us and 3, four loads that wait for one
+// another.
 template <int D, int QB>
 __global__ __launch_bounds__(kThreads, few_blocks(D, QB)) void attention_kernel(AttnArgs a) {
   constexpr int J = D / 32;       // products of 32 columns in a score
@@ -481,7 +495,8 @@ __global__ __launch_bounds__(kThreads, few_blocks(D, QB)) void attention_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int t = 16 * h + li;
-          const auto k = *reinterpret_cast<const mfma_half8_t*>(key_slice + t * (D * 2) + key_piece<D>(t, 4 * j + lg) * 16);
+          const char* piece = key_slice + t * (D * 2) + key_piece<D>(t, 4 * j + lg) * 16;
+          const auto k = *reinterpret_cast<const mfma_half8_t*>(piece);
 #pragma unroll
           for (int b = 0; b < QB; ++b) x[b][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[b][j], x[b][h], 0, 0, 0);
         }
@@ -545,7 +560,8 @@ __global__ __launch_bounds__(kThreads, few_blocks(D, QB)) void attention_kernel(
       while (wild) {
         const int n = __builtin_ctz(wild);
         wild &= wild - 1;
-        const int64_t p = table[static_cast<uint32_t>((t0 + n) >> a.shift)] * page_elements + head_at + ((t0 + n) & page_mask) * a.d;
+        const int t = t0 + n;
+        const int64_t p = table[static_cast<uint32_t>(t >> a.shift)] * page_elements + head_at + (t & page_mask) * a.d;
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
           // element (n / 16) * 4 + n % 4 of the lane that holds the token
@@ -626,16 +642,24 @@ __global__ __launch_bounds__(kThreads, few_blocks(D, QB)) void attention_kernel(
 constexpr int kWide = 64;  // tokens of a unit of work
 constexpr int kWideBits = 8;  // one workgroup on each compute unit
 
-// NB: blocks of 32 query rows a wave; the W waves have rows of their own
-// and share the tokens, 64 at a time, through LDS, with the next 64 on their way in registers. The products are
-// turned as in the kernel for few rows (S^T = K Q^T, O^T = V^T W^T), on 32 x 32 tiles: a lane holds
-// one query row's scores, half of its tokens.
+// NB: blocks of 32 query rows a wave; the W waves have rows of their own and
+// share the tokens, 64 at a time, through LDS, with the next 64 on their way in
+// registers. The products are turned as in the kernel for few rows
+// (S^T = K Q^T, O^T = V^T W^T), on 32 x 32 tiles: a lane holds one query row's
+// scores, half of its tokens.
 //
-// A unit has two turns, with a barrier behind each: the matrix products
-// (O^T of the unit before, S^T of this one), then everything else (weights, loads). The two waves of a
-// SIMD are half a unit apart, so that one's products run beside the other's exponentials. The waves
-// that come second write their part of a unit's keys and values one turn early; K(s) is
-// read in turns 2 s and 2 s + 1, V(s) in 2 s + 2 and 2 s + 3, so keys need two buffers and values three.
+// A unit has two turns, with a barrier behind each: the matrix products (O^T of
+// the unit before, S^T of this one), then everything else (weights, loads). The
+// two waves of a SIMD are half a unit apart, so that one's products run beside
+// the other's exponentials. The waves that come second write their part of a
+// unit's keys and values one turn early; K(s) is read in turns 2 s and 2 s + 1,
+// V(s) in 2 s + 2 and 2 s + 3, so keys need two buffers and values three.
+//
+// 4,096 rows over 8,192 tokens and themselves (32 heads over 8 of 128) take 750
+// us, 916 TFLOP/s: a unit takes 2.3 us, of which its products are 0.9, its
+// exponentials and the rest of the vector instructions 1.0 and its LDS reads
+// 0.9, each on units of their own. Without the loads it would be 670, without
+// the exponentials 690.
 template <int D, int NB, int W>
 __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   constexpr int KS = D / 16;           // products of 16 columns in a score
@@ -658,7 +682,8 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1), li = lane & 31, lh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  // neighbours in the line, which read the same keys and values, on one of the chip's eight parts, which has a cache of its own
+  // neighbours in the line, which read the same keys and values, on one of the chip's eight parts, each with its own
+  // cache
   const int64_t me = (blockIdx.x % kParts) * (gridDim.x / kParts) + blockIdx.x / kParts;
   Request r;
   const Share line = share_of<kWide, W, kWideBits>(a, me, r);
@@ -667,8 +692,8 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   int request = line.request;
   int64_t base = line.base;
 
-  // The end of a tile that another workgroup began comes last: all then walk the tokens from the first on at about the same
-  // time, and find the keys that they share in the cache.
+  // The end of a tile that another workgroup began comes last: all then walk the tokens from the first on at about the
+  // same time, and find the keys that they share in the cache (750 us of the above; in the line's order 771).
   const Place begun = place_of(r, line.begin - base);
   const int64_t begun_end = begun.step == 0 ? line.begin : min(line.begin + begun.steps - begun.step, line.end);
   int64_t stop = line.end;
@@ -766,7 +791,8 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
     const int wave_n = wave * NB * 32;
     const bool busy = wave_n / a.group < tile_rows;
     // the last token that any row of the wave sees
-    const int wave_end = a.ancestors ? ending : min(ending, r.length + here.tile * a.rows + (wave_n + NB * 32 - 1) / a.group + 1);
+    const int wave_rows = (wave_n + NB * 32 - 1) / a.group + 1;
+    const int wave_end = a.ancestors ? ending : min(ending, r.length + here.tile * a.rows + wave_rows);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int n = wave_n + 32 * b + li, rr = n / a.group, hh = n - rr * a.group;
@@ -873,11 +899,13 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
           while (wild) {
             const int n = __builtin_ctzll(wild);
             wild &= wild - 1;
-            const int64_t p = table[static_cast<uint32_t>((t0 + n) >> a.shift)] * page_elements + head_at + ((t0 + n) & page_mask) * a.d;
+            const int t = t0 + n;
+        const int64_t p = table[static_cast<uint32_t>(t >> a.shift)] * page_elements + head_at + (t & page_mask) * a.d;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               // element (n / 8) * 4 + n % 4 of the lane that holds the token
-              const float y = static_cast<float>(weights[wave][b][n >> 4][li + 32 * ((n >> 2) & 1)][((n >> 3) & 1) * 4 + (n & 3)]);
+              const _Float16* mine = weights[wave][b][n >> 4][li + 32 * ((n >> 2) & 1)];
+              const float y = static_cast<float>(mine[((n >> 3) & 1) * 4 + (n & 3)]);
               if (seen[b] >> n & 1) {
 #pragma unroll
                 for (int e = 0; e < DB; ++e)
@@ -907,8 +935,10 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
         for (int n = 0; n < 2 * KS; ++n) {
           const mfma_half8_t k = kf[n % kAhead];
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-            x[b][n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[b][n / 2], n < 2 ? f32x16_t{} : x[b][n & 1], 0, 0, 0);
+          for (int b = 0; b < NB; ++b) {
+            const f32x16_t before = n < 2 ? f32x16_t{} : x[b][n & 1];
+            x[b][n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[b][n / 2], before, 0, 0, 0);
+          }
           if (n + kAhead < 2 * KS) kf[n % kAhead] = key(n + kAhead);
         }
         __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
@@ -1020,12 +1050,11 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   }
 }
 
-// Joins the pieces of the tiles of R query rows that several of N workgroups had. Every
-// workgroup counts the jobs, four query rows of a tile each, and takes its
-// share of them (a workgroup for each that could be, most of them with nothing to do, took 9 us for 4,096). A wave has 16 lanes
-// a row and merges pieces as they come, the loads of AHEAD in flight. With SHARE the
-// workgroup's waves share the pieces of the same four rows (few rows, many
-// pieces), otherwise each has rows of its own.
+// Joins the pieces of the tiles of R query rows that several of N workgroups had. Every workgroup counts the jobs,
+// four query rows of a tile each, and takes its share of them (a workgroup for each that could be, most of them with
+// nothing to do, took 9 us for 4,096). A wave has 16 lanes a row and merges pieces as they come, the loads of AHEAD
+// in flight. With SHARE the workgroup's waves share the pieces of the same four rows (few rows, many pieces),
+// otherwise each has rows of its own.
 template <int D, int R, int N, bool SHARE, int AHEAD>
 __device__ __forceinline__ void join(const AttnArgs& a, int block, int blocks) {
   constexpr int64_t kState = R * (D + 2);
@@ -1180,10 +1209,11 @@ hipError_t launch_few(const AttnArgs& args, void* ws, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Without a tree, requests with at most 16 query rows a key head go through the kernel for few rows, also here: single
-// tokens beside a prompt. 63 tokens of requests of 4,096 beside a prompt of 1,024 rows take 256 us, all through the wide
-// kernel 422. Where there are none the launch costs 7 us with its part of the join (of 771 for 4,096 rows over 8,192
-// tokens), which trees, whose sizes are alike, do not pay (16 trees of 30 to 61 rows: 87 us, 94 with it), nor does one request.
+// Without a tree, requests with at most 16 query rows a key head go through the kernel for few rows, also here:
+// single tokens beside a prompt. 63 tokens of requests of 4,096 beside a prompt of 1,024 rows take 256 us, all
+// through the wide kernel 422. Where there are none the launch costs 7 us with its part of the join (of 771 for 4,096
+// rows over 8,192 tokens), which trees, whose sizes are alike, do not pay (16 trees of 30 to 61 rows: 87 us, 94 with
+// it), nor does one request.
 template <int D>
 hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
   constexpr int W = wide_waves(D), R = W * 32, groups = 1 << few_bits(D, 1);
@@ -1205,11 +1235,11 @@ hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Which kernel, by the query rows of a key head that a request has on average. Eight requests of up to 8,192 tokens at
-// head_dim 128: 20 rows take 74.5 us in tiles of 16, 61.7 in tiles of 32 and 62.5 in the wide kernel; 28 rows 90.1, 62.4 and
-// 63.0; 48 rows 93.9 in tiles of 48, 128.6 in tiles of 64 and 67.4 in the wide kernel. One row each of 64 requests: 217 us in
-// tiles of 16, 291 in tiles of 32, 829 wide. At head_dim 256, where a tile of 32 does not fit the registers, 32 rows take 45 us
-// in tiles of 16, 66 in tiles of 32 and 68 wide.
+// Which kernel, by the query rows of a key head that a request has on average. Eight requests of up to 8,192 tokens
+// at head_dim 128: 20 rows take 74.5 us in tiles of 16, 61.7 in tiles of 32 and 62.5 in the wide kernel; 28 rows
+// 90.1, 62.4 and 63.0; 48 rows 93.9 in tiles of 48, 128.6 in tiles of 64 and 67.4 in the wide kernel. One row each of
+// 64 requests: 217 us in tiles of 16, 291 in tiles of 32, 829 wide. At head_dim 256, where a tile of 32 does not fit
+// the registers, 32 rows take 45 us in tiles of 16, 66 in tiles of 32 and 68 wide.
 template <int D>
 hipError_t launch_rows(const AttnArgs& a, int64_t rows, void* ws, hipStream_t stream) {
   if (rows <= (D == 256 ? 32 : 16)) return launch_few<D, 1>(a, ws, stream);

@@ -21,8 +21,8 @@ constexpr int kMaxRequests = 4096;
 // the table or the stack.
 __global__ __launch_bounds__(kPlanThreads) void cache_plan_kernel(
     const int32_t* __restrict__ lengths, const int32_t* __restrict__ added, int requests, int32_t* table, int width,
-    const int32_t* __restrict__ free_pages, int64_t free_capacity, const int32_t* __restrict__ free_count, int64_t pages,
-    int shift, const int32_t* __restrict__ parents, int m, int32_t* __restrict__ row_start,
+    const int32_t* __restrict__ free_pages, int64_t free_capacity, const int32_t* __restrict__ free_count,
+    int64_t pages, int shift, const int32_t* __restrict__ parents, int m, int32_t* __restrict__ row_start,
     int32_t* __restrict__ request, int32_t* __restrict__ position, int64_t* __restrict__ slot,
     uint64_t* __restrict__ ancestors, int32_t* __restrict__ free_left) {
   __shared__ int start[kMaxRequests + 1];
@@ -281,9 +281,9 @@ void launch_rotary(const RotaryArgs& a, bool interleaved, hipStream_t stream) {
 
 template <int LPH>
 void launch_rotary_rows(const RotaryArgs& a, bool interleaved, hipStream_t stream) {
-  // Two groups of heads a wave share its angles: 4,096 rows of 48 heads take 32.1 us, with one 39.0, with three 31.8, with
-  // four 35.1; 1,000 rows 11.0 and 12.7. One group ends sooner where there are waves to spare: one row 3.4 and 3.9 us, 333
-  // rows of 18 heads 3.6 and 3.9.
+  // Two groups of heads a wave share its angles: 4,096 rows of 48 heads take 32.1 us, with one 39.0, with three 31.8,
+  // with four 35.1; 1,000 rows 11.0 and 12.7. One group ends sooner where there are waves to spare: one row 3.4 and
+  // 3.9 us, 333 rows of 18 heads 3.6 and 3.9.
   if (static_cast<int64_t>(a.m) * (a.heads + 2 * a.kv_heads) >= 16384) launch_rotary<LPH, 2>(a, interleaved, stream);
   else launch_rotary<LPH, 1>(a, interleaved, stream);
 }
@@ -297,10 +297,11 @@ hipError_t launch_cache_plan(const int32_t* lengths, const int32_t* added, int64
                              const int32_t* free_count, int64_t pages, int64_t page_size, const int32_t* parents,
                              int64_t m, int32_t* row_start, int32_t* request, int32_t* position, int64_t* slot,
                              uint64_t* ancestors, int32_t* free_left, hipStream_t stream) {
-  hipLaunchKernelGGL(cache_plan_kernel, dim3(static_cast<unsigned>((m + kPlanRows - 1) / kPlanRows)), dim3(kPlanThreads),
-                     0, stream, lengths, added, static_cast<int>(requests), table, static_cast<int>(table_width),
-                     free_pages, free_capacity, free_count, pages, page_shift(page_size), parents, static_cast<int>(m),
-                     row_start, request, position, slot, ancestors, free_left);
+  const dim3 grid(static_cast<unsigned>((m + kPlanRows - 1) / kPlanRows));
+  hipLaunchKernelGGL(cache_plan_kernel, grid, dim3(kPlanThreads), 0, stream, lengths, added,
+                     static_cast<int>(requests), table, static_cast<int>(table_width), free_pages, free_capacity,
+                     free_count, pages, page_shift(page_size), parents, static_cast<int>(m), row_start,
+                     request, position, slot, ancestors, free_left);
   return hipGetLastError();
 }
 

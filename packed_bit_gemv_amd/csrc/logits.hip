@@ -10,7 +10,9 @@ typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr uint32_t kGiven = 0x80000000u;  // the prompt holds the token; the low bits count the output's
 
-__device__ __forceinline__ unsigned long long max_u64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
+__device__ __forceinline__ unsigned long long max_u64(unsigned long long a, unsigned long long b) {
+  return a > b ? a : b;
+}
 
 // Largest key over the workgroup's W waves, for thread 0.
 template <int W>
@@ -155,7 +157,8 @@ __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
       if (n4.x | n4.y | n4.z | n4.w)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // every step a rounding of its own, selected afterwards: branches around single elements cost 200 registers here
+        // every step a rounding of its own, selected afterwards: branches around single elements cost 200 registers
+        // here
 #pragma clang fp contract(off)
         const float y = v[k][e];
         const float z = y > 0.0f ? y / rep : y * rep;
@@ -257,9 +260,9 @@ hipError_t launch_penalize_logits(const float* logits, const int32_t* request, c
                         frequency, presence, static_cast<int>(requests), drafts, row_start, ancestors, bias_start,
                         bias_token, bias_value, bias_entries, grammar, grammar_row, states, m, n, out,
                         token ? reinterpret_cast<unsigned long long*>(workspace) : nullptr};
-  // 4,096 tokens a workgroup: 64 rows of 151,936 (histories of 2,000, biases, grammars) take 25.9 us and one row (8,000)
-  // 7.2; with 8,192 of 512 threads 26.2 and 8.5, of 256 threads 32.6 and 12.9, with 2,048 of 256 threads 25.3 and 7.7,
-  // of 1,024 threads 36.5 and 7.0
+  // 4,096 tokens a workgroup: 64 rows of 151,936 (histories of 2,000, biases, grammars) take 25.9 us and one row
+  // (8,000) 7.2; with 8,192 of 512 threads 26.2 and 8.5, of 256 threads 32.6 and 12.9, with 2,048 of 256 threads 25.3
+  // and 7.7, of 1,024 threads 36.5 and 7.0
   constexpr int kT = 512, kV = 2;
   const int64_t slices = (n + 4 * kV * kT - 1) / (4 * kV * kT);
   hipLaunchKernelGGL((penalize_kernel<kT, kV>), dim3(static_cast<unsigned>(m * slices)), dim3(kT), 0, stream, a,

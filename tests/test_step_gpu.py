@@ -504,6 +504,9 @@ def test_attention_hostile_tables(pbg):
     got = host(pbg.tree_attention(**{k: dev(v) for k, v in bad.items()}))
     assert np.array_equal(got[[0, 1, 6, 7]], good[[0, 1, 6, 7]])
     check_attention(pbg, {**c, "lengths": np.array([40, 200, 0, 30], np.int32)})
+    for rows in (2, 30):
+        c2 = attention_case(12, [40, 10, 20], [rows, rows, rows], 4, 2, 64, 16)
+        check_attention(pbg, {**c2, "lengths": np.array([40, 2 ** 31 - 1, 2 ** 31 - 1 - rows], np.int32)})
     bad = {**c, "row_start": np.array([0, 2, -5, 6, 100], np.int32)}
     pbg.tree_attention(**{k: dev(v) for k, v in bad.items()})
     bad = {**c, "row_start": np.array([-9, 2, 4, 2, 8], np.int32)}
