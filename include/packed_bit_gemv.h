@@ -647,8 +647,10 @@ int rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, c
  *              requests and heads and narrower heads, and any calls that do
  *              not overlap in time
  * Heads and head_dim as for rotary_qkv; page_size at least
- * PBG_ATTENTION_MIN_PAGE. Scores, weights' sums and the output's sums are fp32; the weights enter the
- * second product rounded to fp16 relative to the row's largest.
+ * PBG_ATTENTION_MIN_PAGE. Scores, weights' sums and the output's sums are
+ * fp32 (a row with a score times scale * log2(e) beyond fp32 is not
+ * specified); the weights enter the second product rounded to fp16 relative to
+ * the row's largest.
  */
 #define PBG_ATTENTION_MIN_PAGE 8
 

@@ -5,6 +5,7 @@
 // down whenever it grows.
 #include "pbg_device.hpp"
 #include "pbg_internal.hpp"
+#include "pbg_scan.hpp"
 
 namespace pbg {
 namespace {
@@ -1213,15 +1214,16 @@ hipError_t launch_few(const AttnArgs& args, void* ws, hipStream_t stream) {
 // single tokens beside a prompt. 63 tokens of requests of 4,096 beside a prompt of 1,024 rows take 256 us, all
 // through the wide kernel 422. Where there are none the launch costs 7 us with its part of the join (of 771 for 4,096
 // rows over 8,192 tokens), which trees, whose sizes are alike, do not pay (16 trees of 30 to 61 rows: 87 us, 94 with
-// it), nor does one request.
+// it), nor does one request, nor heads of which more than 16 share a key head.
 template <int D>
 hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
   constexpr int W = wide_waves(D), R = W * 32, groups = 1 << few_bits(D, 1);
   AttnArgs few = with_tiles(args, 16, ws);
   AttnArgs wide = with_tiles(args, R, static_cast<char*>(ws) + workspace_of(groups, 16, D));
-  const bool both = !args.ancestors && args.requests > 1;
+  const int ratio = args.heads / args.kv_heads;
+  const bool both = !args.ancestors && args.requests > 1 && ratio <= 16;
   if (both) {
-    few.most = 16 / (args.heads / args.kv_heads);
+    few.most = 16 / ratio;
     wide.least = few.most + 1;
     hipLaunchKernelGGL((attention_kernel<D, 1>), dim3(groups), dim3(kThreads), 0, stream, few);
   }

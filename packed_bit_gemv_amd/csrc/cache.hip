@@ -2,6 +2,7 @@
 // step's queries, keys and values from the q|k|v linear's output.
 #include "pbg_device.hpp"
 #include "pbg_internal.hpp"
+#include "pbg_scan.hpp"
 
 namespace pbg {
 namespace {

@@ -211,29 +211,6 @@ __device__ __forceinline__ int reduce4_slot(int lane) {
   return lane == 0 ? 0 : lane == 32 ? 1 : lane == 16 ? 2 : lane == 48 ? 3 : -1;
 }
 
-// Sum of v over the threads before this one, and over all threads (W whole waves).
-template <int W, typename V>
-__device__ __forceinline__ V block_scan(V v, V* waves, V& total) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  V s = v;
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const V o = __shfl_up(s, d);
-    if (lane >= d) s += o;
-  }
-  __syncthreads();  // the last use of waves
-  if (lane == kWave - 1) waves[wave] = s;
-  __syncthreads();
-  V before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < wave) before += waves[w];
-    total += waves[w];
-  }
-  return before + s - v;
-}
-
 // Greedy-argmax key of a logit: the order-preserving image of the fp32 bits
 // in the high half and (2^32 - 1 - row) in the low half, so that the largest
 // key is the largest logit and, among equal logits, the lowest row. -0 is
