@@ -14,15 +14,39 @@ __device__ __forceinline__ unsigned long long max_u64(unsigned long long a, unsi
   return a > b ? a : b;
 }
 
-// Largest key over the workgroup's W waves, for thread 0.
+__device__ __forceinline__ uint32_t min_u32(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
+// Key of the largest value over the workgroup's W waves, for every thread: each brings its own largest and the place
+// of the first that is as large, kNowhere where it has none above -infinity. Inside a wave the value first and then
+// the lowest place of it, by row rotates and lane swaps (as 64-bit keys through shuffles one row takes 7.2 us, so 7.0,
+// and 64 rows 25.8 and 25.2).
+constexpr uint32_t kNowhere = 0xFFFFFFFFu;
+
 template <int W>
-__device__ __forceinline__ unsigned long long block_max(unsigned long long key) {
+__device__ __forceinline__ unsigned long long block_best(float high, uint32_t at, int64_t base) {
+  float top = high;
+  top = fmaxf(top, row_ror<8>(top));
+  top = fmaxf(top, row_ror<4>(top));
+  top = fmaxf(top, row_ror<2>(top));
+  top = fmaxf(top, row_ror<1>(top));
+  const auto t16 = __builtin_amdgcn_permlane16_swap(as_u32(top), as_u32(top), false, false);
+  top = fmaxf(as_f32(t16[0]), as_f32(t16[1]));
+  const auto t32 = __builtin_amdgcn_permlane32_swap(as_u32(top), as_u32(top), false, false);
+  top = fmaxf(as_f32(t32[0]), as_f32(t32[1]));
+  uint32_t place = high == top ? at : kNowhere;
+  place = min_u32(place, as_u32(row_ror<8>(as_f32(place))));
+  place = min_u32(place, as_u32(row_ror<4>(as_f32(place))));
+  place = min_u32(place, as_u32(row_ror<2>(as_f32(place))));
+  place = min_u32(place, as_u32(row_ror<1>(as_f32(place))));
+  const auto p16 = __builtin_amdgcn_permlane16_swap(place, place, false, false);
+  place = min_u32(p16[0], p16[1]);
+  const auto p32 = __builtin_amdgcn_permlane32_swap(place, place, false, false);
+  place = min_u32(p32[0], p32[1]);
   __shared__ unsigned long long part[W];
-#pragma unroll
-  for (int d = kWave / 2; d > 0; d /= 2) key = max_u64(key, __shfl_xor(key, d));
-  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = key;
+  if ((threadIdx.x & (kWave - 1)) == 0)
+    part[threadIdx.x / kWave] = place == kNowhere ? 0 : argmax_key(top, base + place);
   __syncthreads();
-  key = part[0];
+  unsigned long long key = part[0];
 #pragma unroll
   for (int w = 1; w < W; ++w) key = max_u64(key, part[w]);
   return key;
@@ -65,8 +89,11 @@ __device__ __forceinline__ C* scalars(P* p) {
 
 // A workgroup of T threads takes a slice of 4 V T tokens of one row: it counts
 // the row's tokens that fall into the slice in LDS, then makes one pass over
-// the slice's logits, which were loaded before. Everything that the row's request says is
-// loaded together, and the history several loads at a time.
+// the slice's logits, which were loaded before. Everything that the row's
+// request says is loaded together, and the history several loads at a time.
+// The results are stored past the caches, the logits, which the head has just
+// written, are read through them (64 rows: 22.2 us; 23.5 with ordinary stores, 22.6
+// with loads past the caches too).
 template <int T, int V>
 __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
   constexpr int kSlice = 4 * V * T;
@@ -88,7 +115,7 @@ __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
     const int c = 4 * (tid + k * T);
     v[k] = f32x4_t{};
     if (c + 4 <= len) {
-      v[k] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any_t*>(x + c));
+      v[k] = *reinterpret_cast<const f32x4_any_t*>(x + c);
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
@@ -198,12 +225,11 @@ __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
       for (int e = 0; e < 4; ++e) v[k][e] = allowed[k] >> e & 1 ? v[k][e] : -__builtin_inff();
   }
   float* o = a.out + row * a.n + base;
-  unsigned long long key = 0;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = 4 * (tid + k * T);
     if (c + 4 <= len) {
-      *reinterpret_cast<f32x4_any_t*>(o + c) = v[k];
+      __builtin_nontemporal_store(v[k], reinterpret_cast<f32x4_any_t*>(o + c));
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
@@ -213,7 +239,7 @@ __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
   if (a.best) {
     // the thread's largest value, the first of equal ones: its elements' places grow with k and e
     float high = -__builtin_inff();
-    int at = -1;
+    uint32_t at = kNowhere;
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
@@ -221,10 +247,9 @@ __global__ __launch_bounds__(T) void penalize_kernel(LogitsArgs a, int slices) {
         const int c = 4 * (tid + k * T) + e;
         const bool more = c < len && v[k][e] > high;
         high = more ? v[k][e] : high;
-        at = more ? c : at;
+        at = more ? static_cast<uint32_t>(c) : at;
       }
-    if (at >= 0) key = argmax_key(high, base + at);
-    key = block_max<T / kWave>(key);
+    const unsigned long long key = block_best<T / kWave>(high, at, base);
     if (tid == 0) a.best[row * slices + slice] = key;
   }
 }
@@ -260,9 +285,9 @@ hipError_t launch_penalize_logits(const float* logits, const int32_t* request, c
                         frequency, presence, static_cast<int>(requests), drafts, row_start, ancestors, bias_start,
                         bias_token, bias_value, bias_entries, grammar, grammar_row, states, m, n, out,
                         token ? reinterpret_cast<unsigned long long*>(workspace) : nullptr};
-  // 4,096 tokens a workgroup: 64 rows of 151,936 (histories of 2,000, biases, grammars) take 25.9 us and one row
-  // (8,000) 7.2; with 8,192 of 512 threads 26.2 and 8.5, of 256 threads 32.6 and 12.9, with 2,048 of 256 threads 25.3
-  // and 7.7, of 1,024 threads 36.5 and 7.0
+  // 4,096 tokens a workgroup: 64 rows of 151,936 (histories of 2,000, biases, grammars) take 22.2 us and one row
+  // (8,000) 7.0; with 2,048 of 256 threads 21.8 and 7.5, of 512 30.2 and 6.7, with 4,096 of 1,024 threads 32.4 and
+  // 6.8, of 256 threads 22.6 and 9.4, with 8,192 of 512 threads 23.3 and 8.3
   constexpr int kT = 512, kV = 2;
   const int64_t slices = (n + 4 * kV * kT - 1) / (4 * kV * kT);
   hipLaunchKernelGGL((penalize_kernel<kT, kV>), dim3(static_cast<unsigned>(m * slices)), dim3(kT), 0, stream, a,
