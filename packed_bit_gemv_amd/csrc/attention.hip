@@ -900,8 +900,8 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
           while (wild) {
             const int n = __builtin_ctzll(wild);
             wild &= wild - 1;
-            const int t = t0 + n;
-        const int64_t p = table[static_cast<uint32_t>(t >> a.shift)] * page_elements + head_at + (t & page_mask) * a.d;
+            const int t = t0 + n, number = table[static_cast<uint32_t>(t >> a.shift)];
+            const int64_t p = number * page_elements + head_at + (t & page_mask) * a.d;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               // element (n / 8) * 4 + n % 4 of the lane that holds the token
@@ -1051,6 +1051,370 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   }
 }
 
+// ---- many query rows of wide heads
+
+// The same for heads of 256 columns, whose outputs and queries would not fit the registers of two waves on a SIMD
+// (one wave with all of them spills, and nothing runs beside its products: 4,096 rows over 8,192 tokens, 16 heads over
+// 4, take 2,144 us): two waves share 32 query rows. Each makes the scores of half of a unit's tokens and the output of
+// half of the columns, so that both read keys and values once between them. They meet in LDS: each half's largest
+// scores at the end of the products' turn, the weights at the end of the other. Both then raise the same maximum.
+//
+// There is room for two buffers of values, so that a wave stores its values one unit after its keys: in the turn behind
+// the products of unit s the waves that come first store K(s + 1) and V(s), the others K(s + 2) and V(s + 1). K(s) is
+// read in turns 2 s and 2 s + 1, V(s) in 2 s + 2 and 2 s + 3.
+constexpr int kPairRows = 128;  // query rows of a tile: four pairs of waves
+
+__global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
+  constexpr int D = 256, W = 8;
+  constexpr int KS = D / 16;           // products of 16 columns in a score
+  constexpr int DB = D / 64;           // blocks of 32 columns of a wave's half of the output
+  constexpr int kChunks = D / 8;       // 16-byte pieces of a token's keys
+  constexpr int kGroup = kWave / kChunks;  // tokens that a wave loads at once
+  constexpr int kMine = kWide / W;         // tokens of a unit that it loads, of one page
+  constexpr int kPasses = kMine / kGroup;
+  static_assert(kMine == kMinPage, "whole pages");
+  constexpr int kAhead = 4;            // pieces of keys or values read before they are needed
+  constexpr int kTile = kWide * D * 2;
+  __shared__ __attribute__((aligned(16))) char keys[2][kTile];
+  __shared__ __attribute__((aligned(16))) char values[2][kTile];
+  __shared__ __attribute__((aligned(16))) _Float16 weights[W / 2][4][kWave][8];
+  __shared__ float meet[W / 2][2][32];  // largest scores, at the end the sums of weights
+  __shared__ uint32_t flags[4][4];      // tokens without a page, and with values that are infinite or NaN
+
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), li = lane & 31, lh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), pair = wave / 2, half = wave % 2;
+  const int turn = wave / (W / 2);  // a SIMD has a wave of either
+  const int64_t me = (blockIdx.x % kParts) * (gridDim.x / kParts) + blockIdx.x / kParts;
+  Request r;
+  const Share line = share_of<kWide, W, kWideBits>(a, me, r);
+  if (tid == 0) a.parts[me] = make_int4(0, 0, 0, 0);
+  if (line.begin >= line.end) return;
+  int request = line.request;
+  int64_t base = line.base;
+
+  const Place begun = place_of(r, line.begin - base);
+  const int64_t begun_end = begun.step == 0 ? line.begin : min(line.begin + begun.steps - begun.step, line.end);
+  int64_t stop = line.end;
+  bool done = begun_end == line.begin;
+  for (int64_t at = begun_end;;) {
+    if (at == stop) {
+      if (done) break;
+      done = true;
+      at = line.begin;
+      stop = begun_end;
+      request = line.request;
+      base = line.base;
+      r = request_of<kWide>(a, request);
+    }
+    while (at >= base + r.units) {
+      base += r.units;
+      r = request_of<kWide>(a, ++request);
+    }
+    const Place here = place_of(r, at - base);
+    const int step0 = static_cast<int>(here.step);
+    const int step1 = static_cast<int>(min(here.step + (stop - at), here.steps));
+    const int kvh = here.head / a.chunks, chunk = here.head - kvh * a.chunks;
+    const int ratio = a.heads / a.kv_heads;
+    const int head0 = kvh * ratio + chunk * a.group;
+    const int tile_heads = min(a.group, ratio - chunk * a.group);
+    const int row0 = r.begin + here.tile * a.rows;
+    const int tile_rows = min(a.rows, r.rows - here.tile * a.rows);
+    const int edge = a.ancestors ? r.length : r.length + here.tile * a.rows + 1;
+    const int ending = a.ancestors ? r.tokens : min(r.tokens, r.length + here.tile * a.rows + tile_rows);
+    const int last = min(step1, (ending + kWide - 1) / kWide);
+
+    const const_int_t* table = (const const_int_t*)(a.table + static_cast<int64_t>(request) * a.width);
+    const int64_t page_elements = (static_cast<int64_t>(a.kv_heads) << a.shift) * a.d;
+    const int64_t head_at = (static_cast<int64_t>(kvh) << a.shift) * a.d;
+    const int page_mask = (1 << a.shift) - 1;
+    const int load_t = lane / kChunks, load_c = lane % kChunks;
+    const uint32_t lane_at = 2 * (load_t * a.d + (8 * load_c < a.d ? 8 * load_c : 0));  // in bytes
+    int key_page = -1, value_page = -1, page_next = -1;
+    uint4 kr[kPasses], vr[kPasses];
+    auto fetch_page = [&](int s) {
+      const int t = s * kWide + wave * kMine;
+      const int found = table[static_cast<uint32_t>(min(t >> a.shift, a.width - 1))];
+      page_next = t < r.tokens && static_cast<uint32_t>(found) < static_cast<uint32_t>(a.pages) ? found : -1;
+    };
+    auto place = [&](int s, int page) {
+      return max(page, 0) * page_elements + head_at + ((s * kWide + wave * kMine) & page_mask) * a.d;
+    };
+    // keys of unit s, and the page of the next
+    auto fetch_keys = [&](int s) {
+      key_page = page_next;
+      const int64_t from = place(s, key_page);
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) kr[i] = load16(a.k + from + i * kGroup * a.d, lane_at);
+      fetch_page(s + 1);
+    };
+    // values of unit s, whose keys were the last to be loaded, and the keys after those
+    auto fetch = [&](int s) {
+      if (s < last) {
+        value_page = key_page;
+        const int64_t from = place(s, value_page);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) vr[i] = load16(a.v + from + i * kGroup * a.d, lane_at);
+      }
+      if (s + 1 < last) fetch_keys(s + 1);
+    };
+    auto store_keys = [&](int s) {
+      char* to = keys[s & 1];
+      if (key_page < 0) {
+        __builtin_amdgcn_sched_barrier(0);  // a branch
+        if (lane == 0) atomicOr(&flags[s & 3][wave / 4], 0xFFu << (wave % 4 * 8));
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) kr[i] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int t = wave * kMine + i * kGroup + load_t;
+        if (a.d != D && 8 * load_c >= a.d) kr[i] = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(to + t * (D * 2) + key_piece<D>(t, load_c) * 16) = kr[i];
+      }
+    };
+    auto store_values = [&](int s) {
+      char* to = values[s & 1];
+      const bool edges = (s + 1) * kWide > edge;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int t = wave * kMine + i * kGroup + load_t;
+        if (value_page < 0) {
+          __builtin_amdgcn_sched_barrier(0);
+          vr[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (edges) {
+          __builtin_amdgcn_sched_barrier(0);
+          uint4& w = vr[i];
+          const uint4 n = make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w));
+          if (n.x | n.y | n.z | n.w) atomicOr(&flags[s & 3][2 + t / 32], 1u << (t % 32));
+          w = make_uint4(w.x & ~n.x, w.y & ~n.y, w.z & ~n.z, w.w & ~n.w);
+        }
+        *reinterpret_cast<uint4*>(to + t * (D * 2) + value_piece<D>(t, load_c) * 16) = vr[i];
+      }
+    };
+
+    // ---- queries: row li is query row 32 pair + li: row / group, head % group
+    const int n = 32 * pair + li, rr = n / a.group, hh = n - rr * a.group;
+    const bool fine = rr < tile_rows && hh < tile_heads;
+    const bool busy = 32 * pair / a.group < tile_rows;
+    // the last token that any row of the pair sees
+    const int pair_rows = (32 * pair + 31) / a.group + 1;
+    const int pair_end = a.ancestors ? ending : min(ending, r.length + here.tile * a.rows + pair_rows);
+    const uint64_t tree = fine && a.ancestors ? a.ancestors[row0 + rr] : 0;
+    const int upto = fine && !a.ancestors ? r.length + (row0 + rr - r.begin) : r.length - 1;
+    mfma_half8_t q[KS];
+    {
+      const uint16_t* p = a.q + (static_cast<int64_t>(row0 + rr) * a.heads + head0 + hh) * a.d;
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        const int c = 8 * (2 * j + lh);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (fine && c < a.d) w = *reinterpret_cast<const uint4*>(p + c);
+        q[j] = __builtin_bit_cast(mfma_half8_t, w);
+      }
+    }
+    float top = kNone, part = 0.0f;
+    f32x16_t o[DB];
+#pragma unroll
+    for (int e = 0; e < DB; ++e) o[e] = f32x16_t{};
+
+    __syncthreads();  // the last tile's buffers and flags
+    if (tid < 16) flags[tid / 4][tid % 4] = 0;
+    __syncthreads();
+    if (step0 < last) {
+      fetch_page(step0);
+      fetch_keys(step0);
+      store_keys(step0);
+      fetch(step0);
+      if (turn) {
+        if (step0 + 1 < last) store_keys(step0 + 1);
+        store_values(step0);
+        fetch(step0 + 1);
+      }
+    }
+    __syncthreads();
+    if (turn) __syncthreads();
+
+    f32x16_t x;
+    uint64_t seen = 0;
+    bool masked = false;
+    for (int s = step0; s <= last; ++s) {
+      // ---- the matrix products' turn: O^T += V^T W^T of unit s - 1, S^T = K Q^T of unit s
+      const bool scores = busy && s < last && s * kWide < pair_end;
+      if (busy && s > step0 && (s - 1) * kWide < pair_end) {
+        const char* vs = values[(s - 1) & 1];
+        mfma_half8_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const mfma_half8_t*>(weights[pair][j][lane]);
+        auto value = [&](int y) {  // columns 32 (y % DB) of the half on of tokens 16 (y / DB) on
+          mfma_half8_t v;
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int t = 16 * (y / DB) + 8 * z + 4 * lh + (lane & 15) / 4;
+            const int c = 16 * half + 4 * (y % DB) + 2 * ((lane >> 4) & 1) + (lane & 3) / 2;
+            const auto v4 = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_short4_t*)(vs + t * (D * 2) + value_piece<D>(t, c) * 16 + (lane & 1) * 8)));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[4 * z + u] = v4[u];
+          }
+          return v;
+        };
+        mfma_half8_t vf[kAhead];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) vf[y] = value(y);
+#pragma unroll
+        for (int y = 0; y < 4 * DB; ++y) {
+          const mfma_half8_t v = vf[y % kAhead];
+          o[y % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[y / DB], o[y % DB], 0, 0, 0);
+          if (y + kAhead < 4 * DB) vf[y % kAhead] = value(y + kAhead);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);  // LDS reads
+#pragma unroll
+        for (int y = 0; y < 4 * DB - kAhead; ++y) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix instructions
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (masked) {
+          // infinities and NaN among values that some rows may not see: added for the rows that do
+          uint64_t wild = flags[(s - 1) & 3][2] | static_cast<uint64_t>(flags[(s - 1) & 3][3]) << 32;
+          while (wild) {
+            const int y = __builtin_ctzll(wild);
+            wild &= wild - 1;
+            const int t = (s - 1) * kWide + y, number = table[static_cast<uint32_t>(t >> a.shift)];
+            const int64_t p = number * page_elements + head_at + (t & page_mask) * a.d;
+            // element (y / 8) * 4 + y % 4 of the lane that holds the token
+            const _Float16* mine = weights[pair][y >> 4][li + 32 * ((y >> 2) & 1)];
+            const float add = static_cast<float>(mine[((y >> 3) & 1) * 4 + (y & 3)]);
+            if (seen >> y & 1) {
+#pragma unroll
+              for (int e = 0; e < DB; ++e)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  f32x4_t part_o = {o[e][4 * z], o[e][4 * z + 1], o[e][4 * z + 2], o[e][4 * z + 3]};
+                  add_wild(part_o, a.v + p, 128 * half + 32 * e + 8 * z + 4 * lh, a.d, add);
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) o[e][4 * z + u] = part_o[u];
+                }
+            }
+          }
+        }
+      }
+      if (scores) {
+        const char* ks = keys[s & 1];
+        auto key = [&](int y) {
+          const int t = 32 * half + li;
+          return *reinterpret_cast<const mfma_half8_t*>(ks + t * (D * 2) + key_piece<D>(t, 2 * y + lh) * 16);
+        };
+        mfma_half8_t kf[kAhead];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) kf[y] = key(y);
+#pragma unroll
+        for (int y = 0; y < KS; ++y) {
+          const mfma_half8_t k = kf[y % kAhead];
+          x = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[y], y == 0 ? f32x16_t{} : x, 0, 0, 0);
+          if (y + kAhead < KS) kf[y % kAhead] = key(y + kAhead);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int y = 0; y < KS - kAhead; ++y) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        const int t0 = s * kWide;
+        const uint64_t gaps = flags[s & 3][0] | static_cast<uint64_t>(flags[s & 3][1]) << 32;
+        masked = t0 + kWide > edge || gaps != 0;
+        if (masked) {
+          __builtin_amdgcn_sched_barrier(0);  // a branch, not a selection in every unit
+          seen = seen_from(t0, r.length, upto, tree) & ~gaps & ones_below(r.tokens - t0);
+          const uint32_t mine = static_cast<uint32_t>(seen >> (32 * half + 4 * lh));
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = seen_or_none(x[e], mine, 8 * (e / 4) + e % 4);
+        }
+        float high = kNone;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) high = fmaxf(high, x[e]);
+        auto both = __builtin_amdgcn_permlane32_swap(as_u32(high), as_u32(high), false, false);
+        if (lh == 0) meet[pair][half][li] = fmaxf(as_f32(both[0]), as_f32(both[1]));
+      }
+      __syncthreads();
+
+      // ---- the other instructions' turn: loads, and the weights of unit s
+      const int next = s + 1 + turn;
+      if (next < last) store_keys(next);
+      if (next - 1 < last) store_values(next - 1);
+      fetch(next);
+      // last read two units before it, written from the next turn on
+      if (tid < 4) flags[(s + 2) & 3][tid] = 0;
+      if (scores) {
+        const float high = fmaxf(meet[pair][0][li], meet[pair][1][li]) * a.scale;
+        if (__any(high > top + kSlack)) {
+          const float now = fmaxf(top, high), keep = weight_of(top, now);
+          top = now;
+          part *= keep;
+#pragma unroll
+          for (int e = 0; e < DB; ++e) o[e] *= keep;
+        }
+        const float less = top == kNone ? 0.0f : top;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float p[8];
+          mfma_half8_t w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            p[e] = exp2_of(__builtin_fmaf(x[8 * j + e], a.scale, -less));
+            w[e] = static_cast<_Float16>(p[e]);
+          }
+          part += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+          *reinterpret_cast<mfma_half8_t*>(weights[pair][2 * half + j][lane]) = w;
+        }
+      }
+      __syncthreads();
+    }
+    if (!turn) __syncthreads();
+
+    auto both = __builtin_amdgcn_permlane32_swap(as_u32(part), as_u32(part), false, false);
+    if (lh == 0) meet[pair][half][li] = as_f32(both[0]) + as_f32(both[1]);
+    __syncthreads();
+    const float sum = meet[pair][0][li] + meet[pair][1][li];
+    const bool starts = here.step == 0, ends = step1 == here.steps;
+    if (fine && starts && ends) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      uint16_t* to = a.out + (static_cast<int64_t>(row0 + rr) * a.heads + head0 + hh) * a.d;
+#pragma unroll
+      for (int e = 0; e < DB; ++e)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int c = 128 * half + 32 * e + 8 * z + 4 * lh;
+          f32x4_t y = {o[e][4 * z], o[e][4 * z + 1], o[e][4 * z + 2], o[e][4 * z + 3]};
+          if (sum == 0.0f) y = f32x4_t{};
+          if (c < a.d) *reinterpret_cast<half4_t*>(to + c) = __builtin_convertvector(y * inv, half4_t);
+        }
+    } else if (fine) {
+      float* state = a.states + (me * 2 + (starts ? 1 : 0)) * kPairRows * (D + 2);
+#pragma unroll
+      for (int e = 0; e < DB; ++e)
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          *reinterpret_cast<f32x4_t*>(state + n * D + 128 * half + 32 * e + 8 * z + 4 * lh) =
+              f32x4_t{o[e][4 * z], o[e][4 * z + 1], o[e][4 * z + 2], o[e][4 * z + 3]};
+      if (lh == 0 && half == 0) {
+        state[kPairRows * D + 2 * n] = top;
+        state[kPairRows * D + 2 * n + 1] = sum;
+      }
+    }
+    if (starts && !ends && tid == 0)
+      a.parts[me] = make_int4(row0, head0, tile_heads << 16 | tile_rows,
+                              static_cast<int>(quotient(at + here.steps - 1, line.share) - me + 1));
+    at += step1 - step0;
+  }
+}
+
 // Joins the pieces of the tiles of R query rows that several of N workgroups had. Every workgroup counts the jobs,
 // four query rows of a tile each, and takes its share of them (a workgroup for each that could be, most of them with
 // nothing to do, took 9 us for 4,096). A wave has 16 lanes a row and merges pieces as they come, the loads of AHEAD
@@ -1183,7 +1547,7 @@ constexpr int kGroups = 1 << few_bits(64, 1);
 constexpr int kWideGroups = 1 << kWideBits;
 constexpr int kJoinGroups = 256;
 
-constexpr int wide_waves(int d) { return d == 256 ? 4 : 8; }
+constexpr int wide_rows(int d) { return d == 256 ? kPairRows : 256; }
 
 // The sizes of tiles of R query rows, and their part of the workspace.
 AttnArgs with_tiles(AttnArgs a, int r, void* ws) {
@@ -1217,7 +1581,7 @@ hipError_t launch_few(const AttnArgs& args, void* ws, hipStream_t stream) {
 // it), nor does one request, nor heads of which more than 16 share a key head.
 template <int D>
 hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
-  constexpr int W = wide_waves(D), R = W * 32, groups = 1 << few_bits(D, 1);
+  constexpr int R = wide_rows(D), groups = 1 << few_bits(D, 1);
   AttnArgs few = with_tiles(args, 16, ws);
   AttnArgs wide = with_tiles(args, R, static_cast<char*>(ws) + workspace_of(groups, 16, D));
   const int ratio = args.heads / args.kv_heads;
@@ -1227,7 +1591,8 @@ hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
     wide.least = few.most + 1;
     hipLaunchKernelGGL((attention_kernel<D, 1>), dim3(groups), dim3(kThreads), 0, stream, few);
   }
-  hipLaunchKernelGGL((attention_wide_kernel<D, 1, W>), dim3(kWideGroups), dim3(W * kWave), 0, stream, wide);
+  if constexpr (D == 256) hipLaunchKernelGGL(attention_pairs_kernel, dim3(kWideGroups), dim3(512), 0, stream, wide);
+  else hipLaunchKernelGGL((attention_wide_kernel<D, 1, 8>), dim3(kWideGroups), dim3(512), 0, stream, wide);
   if (both)
     hipLaunchKernelGGL((attention_join_both_kernel<D, groups, R, kWideGroups>), dim3(groups + 8 * kJoinGroups),
                        dim3(kThreads), 0, stream, few, wide);
@@ -1258,7 +1623,7 @@ int64_t attention_workspace_bytes(int head_dim) {
   int64_t most = 0;
   for (int d = 64; d <= 256 && (d == 64 || d < 2 * head_dim); d *= 2) {
     const int64_t two = d == 256 ? 0 : workspace_of(1 << few_bits(d, 2), 32, d);
-    const int64_t both = workspace_of(1 << few_bits(d, 1), 16, d) + workspace_of(kWideGroups, 32 * wide_waves(d), d);
+    const int64_t both = workspace_of(1 << few_bits(d, 1), 16, d) + workspace_of(kWideGroups, wide_rows(d), d);
     most = most > two ? most : two;
     most = most > both ? most : both;
   }
