@@ -1062,6 +1062,13 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
 // There is room for two buffers of values, so that a wave stores its values one unit after its keys: in the turn behind
 // the products of unit s the waves that come first store K(s + 1) and V(s), the others K(s + 2) and V(s + 1). K(s) is
 // read in turns 2 s and 2 s + 1, V(s) in 2 s + 2 and 2 s + 3.
+// What is made of v is made again in every unit: held over the loop, addresses and masks of the branches alone spill
+// registers, whose loads then wait for the keys and values on their way.
+__device__ __forceinline__ int afresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 constexpr int kPairRows = 128;  // query rows of a tile: four pairs of waves
 
 __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
@@ -1159,6 +1166,7 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
     };
     auto store_keys = [&](int s) {
       char* to = keys[s & 1];
+      const int lane_now = afresh(lane), load_t = lane_now / kChunks, load_c = lane_now % kChunks;
       if (key_page < 0) {
         __builtin_amdgcn_sched_barrier(0);  // a branch
         if (lane == 0) atomicOr(&flags[s & 3][wave / 4], 0xFFu << (wave % 4 * 8));
@@ -1174,6 +1182,7 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
     };
     auto store_values = [&](int s) {
       char* to = values[s & 1];
+      const int lane_now = afresh(lane), load_t = lane_now / kChunks, load_c = lane_now % kChunks;
       const bool edges = (s + 1) * kWide > edge;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
@@ -1243,17 +1252,18 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
       const bool scores = busy && s < last && s * kWide < pair_end;
       if (busy && s > step0 && (s - 1) * kWide < pair_end) {
         const char* vs = values[(s - 1) & 1];
+        const int lane_now = afresh(lane), lh = lane_now >> 5;
         mfma_half8_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const mfma_half8_t*>(weights[pair][j][lane]);
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const mfma_half8_t*>(weights[pair][j][lane_now]);
         auto value = [&](int y) {  // columns 32 (y % DB) of the half on of tokens 16 (y / DB) on
           mfma_half8_t v;
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const int t = 16 * (y / DB) + 8 * z + 4 * lh + (lane & 15) / 4;
-            const int c = 16 * half + 4 * (y % DB) + 2 * ((lane >> 4) & 1) + (lane & 3) / 2;
+            const int t = 16 * (y / DB) + 8 * z + 4 * lh + (lane_now & 15) / 4;
+            const int c = 16 * half + 4 * (y % DB) + 2 * ((lane_now >> 4) & 1) + (lane_now & 3) / 2;
             const auto v4 = __builtin_bit_cast(half4_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_short4_t*)(vs + t * (D * 2) + value_piece<D>(t, c) * 16 + (lane & 1) * 8)));
+                (lds_short4_t*)(vs + t * (D * 2) + value_piece<D>(t, c) * 16 + (lane_now & 1) * 8)));
 #pragma unroll
             for (int u = 0; u < 4; ++u) v[4 * z + u] = v4[u];
           }
@@ -1280,6 +1290,7 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
         if (masked) {
           // infinities and NaN among values that some rows may not see: added for the rows that do
           uint64_t wild = flags[(s - 1) & 3][2] | static_cast<uint64_t>(flags[(s - 1) & 3][3]) << 32;
+          const int li = afresh(lane) & 31, lh = afresh(lane) >> 5;
           while (wild) {
             const int y = __builtin_ctzll(wild);
             wild &= wild - 1;
@@ -1304,6 +1315,7 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
       }
       if (scores) {
         const char* ks = keys[s & 1];
+        const int lane_now = afresh(lane), li = lane_now & 31, lh = lane_now >> 5;
         auto key = [&](int y) {
           const int t = 32 * half + li;
           return *reinterpret_cast<const mfma_half8_t*>(ks + t * (D * 2) + key_piece<D>(t, 2 * y + lh) * 16);
