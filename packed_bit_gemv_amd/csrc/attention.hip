@@ -661,8 +661,9 @@ constexpr int kWideBits = 8;  // one workgroup on each compute unit
 // exponentials and the rest of the vector instructions 1.0 and its LDS reads
 // 0.9, each on units of their own. Without the loads it would be 670, without
 // the exponentials 690.
-template <int D, int NB, int W>
-__global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
+template <int D>
+__global__ __launch_bounds__(512) void attention_wide_kernel(AttnArgs a) {
+  constexpr int W = 8, NB = 1;         // two blocks a wave do not fit the registers
   constexpr int KS = D / 16;           // products of 16 columns in a score
   constexpr int DB = D / 32;           // blocks of 32 columns of the output
   constexpr int kChunks = D / 8;       // 16-byte pieces of a token's keys
@@ -674,8 +675,7 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
   constexpr int kAhead = 4;            // pieces of keys or values read before they are needed
   constexpr int kRows = W * NB * 32;
   constexpr int kTile = kWide * D * 2;
-  constexpr bool kTurns = W > 4;  // two waves on a SIMD: they take turns
-  constexpr int kValueTiles = kTurns ? 3 : 2;
+  constexpr int kValueTiles = 3;
   __shared__ __attribute__((aligned(16))) char keys[2][kTile];
   __shared__ __attribute__((aligned(16))) char values[kValueTiles][kTile];
   __shared__ __attribute__((aligned(16))) _Float16 weights[W][NB][4][kWave][8];  // for the rare path only
@@ -820,7 +820,7 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
       for (int e = 0; e < DB; ++e) o[b][e] = f32x16_t{};
     }
 
-    const int turn = kTurns ? wave / (W / 2) : 0;
+    const int turn = wave / (W / 2);  // a SIMD has a wave of either
     __syncthreads();  // the last tile's buffers and flags
     if (tid < 16) flags[tid / 4][tid % 4] = 0;
     __syncthreads();
@@ -1009,7 +1009,7 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
       }
       __syncthreads();
     }
-    if (kTurns && !turn) __syncthreads();
+    if (!turn) __syncthreads();
 
     const bool starts = here.step == 0, ends = step1 == here.steps;
     float* state = a.states + (me * 2 + (starts ? 1 : 0)) * kRows * (D + 2);
@@ -1053,15 +1053,6 @@ __global__ __launch_bounds__(W * kWave) void attention_wide_kernel(AttnArgs a) {
 
 // ---- many query rows of wide heads
 
-// The same for heads of 256 columns, whose outputs and queries would not fit the registers of two waves on a SIMD
-// (one wave with all of them spills, and nothing runs beside its products: 4,096 rows over 8,192 tokens, 16 heads over
-// 4, take 2,144 us): two waves share 32 query rows. Each makes the scores of half of a unit's tokens and the output of
-// half of the columns, so that both read keys and values once between them. They meet in LDS: each half's largest
-// scores at the end of the products' turn, the weights at the end of the other. Both then raise the same maximum.
-//
-// There is room for two buffers of values, so that a wave stores its values one unit after its keys: in the turn behind
-// the products of unit s the waves that come first store K(s + 1) and V(s), the others K(s + 2) and V(s + 1). K(s) is
-// read in turns 2 s and 2 s + 1, V(s) in 2 s + 2 and 2 s + 3.
 // What is made of v is made again in every unit: held over the loop, addresses and masks of the branches alone spill
 // registers, whose loads then wait for the keys and values on their way.
 __device__ __forceinline__ int afresh(int v) {
@@ -1069,6 +1060,19 @@ __device__ __forceinline__ int afresh(int v) {
   return v;
 }
 
+// The same for heads of 256 columns, whose outputs and queries would not fit the registers of two waves on a SIMD
+// (one wave with all of them spills, and nothing runs beside its products): two waves share 32 query rows. Each
+// makes the scores of half of a unit's tokens and the output of half of the columns, so that both read keys and
+// values once between them. They meet in LDS: each half's largest scores at the end of the products' turn, the
+// weights at the end of the other. Both then raise the same maximum.
+//
+// There is room for two buffers of values, so that a wave stores its values one unit after its keys: in the turn behind
+// the products of unit s the waves that come first store K(s + 1) and V(s), the others K(s + 2) and V(s + 1). K(s) is
+// read in turns 2 s and 2 s + 1, V(s) in 2 s + 2 and 2 s + 3.
+//
+// 4,096 rows over 8,192 tokens and themselves (16 heads over 4) take 877 us, 784 TFLOP/s (one wave with 32 rows of its
+// own 2,144); 16 trees of 31 to 61 rows over 2,050 to 4,100 tokens 104 (266). What the other kernel's unit costs, and
+// the way of the weights through LDS.
 constexpr int kPairRows = 128;  // query rows of a tile: four pairs of waves
 
 __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
@@ -1604,7 +1608,7 @@ hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
     hipLaunchKernelGGL((attention_kernel<D, 1>), dim3(groups), dim3(kThreads), 0, stream, few);
   }
   if constexpr (D == 256) hipLaunchKernelGGL(attention_pairs_kernel, dim3(kWideGroups), dim3(512), 0, stream, wide);
-  else hipLaunchKernelGGL((attention_wide_kernel<D, 1, 8>), dim3(kWideGroups), dim3(512), 0, stream, wide);
+  else hipLaunchKernelGGL((attention_wide_kernel<D>), dim3(kWideGroups), dim3(512), 0, stream, wide);
   if (both)
     hipLaunchKernelGGL((attention_join_both_kernel<D, groups, R, kWideGroups>), dim3(groups + 8 * kJoinGroups),
                        dim3(kThreads), 0, stream, few, wide);
@@ -1618,10 +1622,12 @@ hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
 // at head_dim 128: 20 rows take 74.5 us in tiles of 16, 61.7 in tiles of 32 and 62.5 in the wide kernel; 28 rows
 // 90.1, 62.4 and 63.0; 48 rows 93.9 in tiles of 48, 128.6 in tiles of 64 and 67.4 in the wide kernel. One row each of
 // 64 requests: 217 us in tiles of 16, 291 in tiles of 32, 829 wide. At head_dim 256, where a tile of 32 does not fit
-// the registers, 32 rows take 45 us in tiles of 16, 66 in tiles of 32 and 68 wide.
+// the registers, the kernel of pairs takes over: 16 trees of 24 query rows over 2,050 to 4,100 tokens take 71 us there
+// and 99 in tiles of 16, 40 rows 75 and 143; 8 requests of 32 rows 43.6 and 46.0, one of 32 rows over 2,000 tokens
+// 25.5 and 24.3.
 template <int D>
 hipError_t launch_rows(const AttnArgs& a, int64_t rows, void* ws, hipStream_t stream) {
-  if (rows <= (D == 256 ? 32 : 16)) return launch_few<D, 1>(a, ws, stream);
+  if (rows <= 16) return launch_few<D, 1>(a, ws, stream);
   if constexpr (D < 256) {
     if (rows <= 32) return launch_few<D, 2>(a, ws, stream);
   }

@@ -343,6 +343,35 @@ def test_attention_pages(pbg, page):
     check_attention(pbg, attention_case(page, [9, 257], [30, 64], 8, 2, 128, page, tree=True, width=300))
 
 
+@pytest.mark.parametrize("heads,kv,d,lengths,added,page,tree", [
+    (24, 2, 256, [3000], [96], 16, False),                # several units of a tile in one workgroup
+    (16, 1, 256, [3000, 0, 1500], [96, 200, 33], 64, False),
+    (16, 1, 256, [2000, 0, 700, 64, 1], [40, 1, 64, 3, 64], 8, True),
+    (8, 8, 200, [130, 63, 64, 65, 0], [129, 1, 1, 1, 257], 128, False),  # single tokens beside prompts
+    (40, 2, 136, [900, 5], [17, 70], 8, False),           # 20 query heads a key head: a row and its pair's tail empty
+    (130, 1, 256, [200, 31], [5, 2], 32, True)])          # more heads than a tile has rows
+def test_attention_wide_heads(pbg, heads, kv, d, lengths, added, page, tree):
+    """Two waves a query row: its tokens' halves and the halves of its columns meet."""
+    say(f"attention wide heads {heads}/{kv} x {d} {lengths} {added}")
+    c = attention_case(d + heads, lengths, added, heads, kv, d, page, tree=tree, pad=2)
+    check_attention(pbg, c)
+    # a page in the middle that no request has, and what no row sees is not finite
+    c["table"][0, c["lengths"][0] // page // 2] = -1
+    for cache in (c["k_cache"], c["v_cache"]):
+        free = np.setdiff1d(np.arange(len(cache)), c["table"])
+        cache[free] = np.nan
+        for i in range(len(lengths)):
+            end = int(c["lengths"][i] + added[i])
+            if end % page and c["table"][i, end // page] >= 0:
+                cache[c["table"][i, end // page], :, end % page:] = np.inf
+    # one score far above the others, in either half of a unit, early and late
+    for t in (3, 40, int(c["lengths"][0]) - 1):
+        number = c["table"][0, t // page]
+        if number >= 0:
+            c["k_cache"][number, :, t % page] = c["q"][0, :kv] * 4
+    check_attention(pbg, c)
+
+
 @pytest.mark.parametrize("heads,kv,d", HEADS)
 def test_attention_trees(pbg, heads, kv, d):
     say(f"attention trees {heads}/{kv} x {d}")
