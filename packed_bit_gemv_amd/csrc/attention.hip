@@ -249,6 +249,26 @@ __device__ __forceinline__ int narrow_piece(int token, int piece) {
   else return piece ^ ((token & 7) << 1);
 }
 
+// Scores, in powers of two, from which on their rounding matters. The maximum is a rounded product; a score that is held
+// against it by a product and difference in one has no such rounding, and the difference, up to 2^-25 of the score, is a
+// power of two of its own (at a score of 2^30 the largest weight was anything from 2^-32 to 2^32). Rows whose maximum is
+// that far from 0 have every score rounded first: the branch takes 1 % of the time of many rows (chunk 758 -> 765 us,
+// trees 88 -> 89). The kernel for few rows always rounds, which takes it no longer.
+constexpr float kFar = 0x1p20f;
+
+__device__ __forceinline__ float rounded_product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+
+__device__ __forceinline__ bool is_far(float top) { return fabsf(top) > kFar && top != kNone; }
+
+// Score x of a row whose maximum is far, less that maximum and before the scale; x itself in other rows, whose bits are
+// the same beside any others. (A scale that lets scores get that far has a reciprocal.)
+__device__ __forceinline__ float over_far(float x, float scale, float top) {
+  return is_far(top) ? (rounded_product(x, scale) - top) * __builtin_amdgcn_rcpf(scale) : x;
+}
+
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
 
 // Maximum over the four 16-lane groups of a wave, lane by lane.
@@ -518,8 +538,11 @@ __global__ __launch_bounds__(kThreads, few_blocks(D, QB)) void attention_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) high = fmaxf(high, x[b][h][e]);
-        high = groups_max(high) * a.scale;
+          for (int e = 0; e < 4; ++e) {
+            x[b][h][e] = rounded_product(x[b][h][e], a.scale);
+            high = fmaxf(high, x[b][h][e]);
+          }
+        high = groups_max(high);
         if (__any(high > top[b] + kSlack)) {
           const float now = fmaxf(top[b], high), keep = weight_of(top[b], now);
           top[b] = now;
@@ -532,7 +555,7 @@ __global__ __launch_bounds__(kThreads, few_blocks(D, QB)) void attention_kernel(
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float p = exp2_of(__builtin_fmaf(x[b][h][e], a.scale, -less));
+            const float p = exp2_of(x[b][h][e] - less);
             part[b] += p;
             w[b][4 * h + e] = static_cast<_Float16>(p);
           }
@@ -843,8 +866,9 @@ __global__ __launch_bounds__(512) void attention_wide_kernel(AttnArgs a) {
     f32x16_t x[NB][2];
     uint64_t seen[NB];
     bool masked = false;
+    bool far[NB];  // the maximum of some row of the wave is far from 0
 #pragma unroll
-    for (int b = 0; b < NB; ++b) seen[b] = 0;
+    for (int b = 0; b < NB; ++b) seen[b] = 0, far[b] = false;
     // values of units s - 1 and of the one that is stored next
     int value_read = (kValueTiles - 1) * kTile, value_store = (1 + turn) * kTile;
     for (int s = step0; s <= last; ++s) {
@@ -993,8 +1017,17 @@ __global__ __launch_bounds__(512) void attention_wide_kernel(AttnArgs a) {
             part[b] *= keep;
 #pragma unroll
             for (int e = 0; e < DB; ++e) o[b][e] *= keep;
+            far[b] = __any(is_far(now));
           }
-          const float less = top[b] == kNone ? 0.0f : top[b];
+          float less = top[b] == kNone ? 0.0f : top[b];
+          if (far[b]) {
+            __builtin_amdgcn_sched_barrier(0);  // a branch
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[b][h][e] = over_far(x[b][h][e], a.scale, top[b]);
+            less = is_far(top[b]) ? 0.0f : less;
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float p[8];
@@ -1250,7 +1283,7 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
 
     f32x16_t x;
     uint64_t seen = 0;
-    bool masked = false;
+    bool masked = false, far = false;  // far: the maximum of some row of the pair is far from 0
     for (int s = step0; s <= last; ++s) {
       // ---- the matrix products' turn: O^T += V^T W^T of unit s - 1, S^T = K Q^T of unit s
       const bool scores = busy && s < last && s * kWide < pair_end;
@@ -1375,8 +1408,15 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
           part *= keep;
 #pragma unroll
           for (int e = 0; e < DB; ++e) o[e] *= keep;
+          far = __any(is_far(now));
         }
-        const float less = top == kNone ? 0.0f : top;
+        float less = top == kNone ? 0.0f : top;
+        if (far) {
+          __builtin_amdgcn_sched_barrier(0);  // a branch
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = over_far(x[e], a.scale, top);
+          less = is_far(top) ? 0.0f : less;
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float p[8];

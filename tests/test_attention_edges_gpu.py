@@ -1,0 +1,63 @@
+"""tree_attention on the GPU where its softmax is at its ends: scores of any size, tokens of next to no weight beside one of nearly
+all of it, and requests that many workgroups share, every piece of which has to count once. References in 64 bits."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import oracle
+from helpers import assert_within
+from test_step_gpu import attention_case, dev, host, pbg, say  # noqa: F401 (pbg is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+# heads, kv heads, head_dim, rows of a request: both tile sizes of the kernel for few query rows, the wide one, that for wide heads
+KERNELS = [(4, 1, 128, 1), (8, 2, 64, 1), (2, 1, 256, 3), (6, 1, 128, 4), (8, 8, 128, 40), (4, 2, 64, 130), (2, 1, 256, 40), (3, 1, 200, 70)]
+
+
+def run(pbg, c, scale=None):  # noqa: F811
+    return host(pbg.tree_attention(**{k: dev(v) for k, v in c.items()}, scale=scale))
+
+
+def set_token(c, i, t, key=None, value=None):
+    """Key and value of token t of request i, for every head."""
+    page = c["k_cache"].shape[2]
+    for name, x in (("k_cache", key), ("v_cache", value)):
+        if x is not None:
+            c[name][c["table"][i, t // page], :, t % page] = x
+
+
+@pytest.mark.parametrize("heads,kv,d,rows", KERNELS)
+@pytest.mark.parametrize("scale", [1.0, 9.0, 130.0, 3e4, 1.7e9, 2.3e17, 1e30])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(pbg, heads, kv, d, rows, scale, sign):  # noqa: F811
+    """Scores that are far apart leave one token's value, scores that are equal the mean of two, however large they are.
+
+    Queries and keys are small integers, so that products are exact, and scores differ by at least 100 in powers of two or not at all:
+    one or two equal weights, each off by its own rounding to fp16 (2^-11) above and not below, and the output's rounding. What a score
+    is off by is off in the largest as well.
+    """
+    say(f"attention scores {heads}/{kv} x {d} rows={rows} scale={scale} sign={sign}")
+    lengths = [700, 65, 3]
+    c = attention_case(d + rows, lengths, [rows] * 3, heads, kv, d, 16)
+    rng = np.random.default_rng(1)
+    c["q"][:], c["k_cache"][:] = 0, 0
+    c["q"][..., 0] = 100
+    c["v_cache"][:] = rng.integers(-32, 33, c["v_cache"].shape)
+    most = max(lengths) + rows
+    for i in range(3):
+        # the tokens before the step in any order, the step's own below all of them, those of the step among them by their row
+        order = rng.permutation(lengths[i])
+        for t in range(lengths[i] + rows):
+            key = order[t] + rows if t < lengths[i] else t - lengths[i]
+            set_token(c, i, t, key + 1 if sign > 0 else key - most)
+        # a tie of the two largest
+        a, b = int(np.flatnonzero(order == lengths[i] - 1)[0]), int(np.flatnonzero(order == lengths[i] - 2)[0])
+        if i < 2:
+            set_token(c, i, b, lengths[i] - 1 + rows + 1 if sign > 0 else lengths[i] - 1 + rows - most)
+            assert np.array_equal(c["k_cache"][c["table"][i, a // 16], :, a % 16], c["k_cache"][c["table"][i, b // 16], :, b % 16])
+    ref, size, _ = oracle.tree_attention(**c, scale=scale)
+    bound = 2.0 ** -11 * (size + np.abs(ref)) * 1.01 + 2.0 ** -25
+    assert_within(run(pbg, c, scale), ref, bound)
