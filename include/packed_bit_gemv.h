@@ -649,8 +649,9 @@ int rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, c
  * Heads and head_dim as for rotary_qkv; page_size at least
  * PBG_ATTENTION_MIN_PAGE. Scores, weights' sums and the output's sums are
  * fp32 (a row with a score times scale * log2(e) beyond fp32 is not
- * specified); the weights enter the second product rounded to fp16 relative to
- * the row's largest.
+ * specified). The weights enter the second product rounded to fp16: to 2^-11
+ * of themselves, and light ones to 2^-33 of the row's largest (an infinite
+ * value that a row sees with a weight below that makes the output NaN).
  */
 #define PBG_ATTENTION_MIN_PAGE 8
 

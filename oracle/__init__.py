@@ -572,9 +572,10 @@ def cached_tokens(cache, table_row, count, head):
     return out, held
 
 
-def tree_attention(q, k_cache, v_cache, table, lengths, row_start, ancestors=None, scale=None):
+def tree_attention(q, k_cache, v_cache, table, lengths, row_start, ancestors=None, scale=None, totals=None):
     """(out, size, far) fp64: out[a, e] = sum_t w_t v_t / sum_t w_t over the tokens that row a sees; size the same sum of
-    magnitudes |v_t|, far the largest sum_j |q_j k_j| of a token seen. Rows of no request are NaN."""
+    magnitudes |v_t|, far the largest sum_j |q_j k_j| of a token seen. Rows of no request are NaN. totals [m, heads], if
+    given, takes each row's sum of weights relative to the largest of them."""
     m, heads, d = q.shape
     kv_heads = k_cache.shape[1]
     scale = d ** -0.5 if scale is None else scale
@@ -605,6 +606,8 @@ def tree_attention(q, k_cache, v_cache, table, lengths, row_start, ancestors=Non
                         top = s.max()
                         w = np.exp(s - (top if np.isfinite(top) else 0.0))
                         total = w.sum()
+                        if totals is not None:
+                            totals[a, e] = total
                         out[a, e] = 0.0 if total == 0 else w @ vv / total
                         size[a, e] = 0.0 if total == 0 else w @ np.abs(vv) / total
                         far[a, e] = (np.abs(kk) @ np.abs(qq)).max()

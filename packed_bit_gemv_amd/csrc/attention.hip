@@ -16,13 +16,19 @@ constexpr int kMinPage = 8;  // tokens
 constexpr int kParts = 8;  // of the chip; workgroups go to them in turn
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -__builtin_inff();
-// A running maximum is only raised when a score passes it by this much (in powers of two): weights then reach 2^8,
-// far inside fp16, and the sums are hardly ever scaled. Weights are rounded to fp16 for the second product, to half a
-// step each (2^-11), independent of one another and no more than the output's own rounding: against 64 bits both
-// together are 1.38 times the latter alone (1.07 with a maximum that is always raised, whose largest weights are
-// exactly 1). The sum of the weights is that of the unrounded ones: of the rounded ones the wide kernel is 13 %
-// slower, and 1.30 times.
-constexpr float kSlack = 8.0f;
+// Weights are rounded to fp16 for the second product, to half a step each (2^-11), independent of one another and no
+// more than the output's own rounding; their sum is that of the unrounded ones (of the rounded ones the wide kernel is
+// 13 % slower). They are held relative to 2^-lift of the row's running maximum, so that light ones keep their bits
+// beside a token that has nearly all the weight: what the second product loses of one is 2^-(25 + lift) of the largest
+// at most, 2^-40 in the kernel for few rows and 2^-33 in the others. (Without a lift 3,000 tokens of 2^-25.2 each
+// added to 0 above and not below.)
+// The maximum is raised when a score passes it by more than the slack (in powers of two), and with both the weights
+// reach 2^15, still inside fp16. Without a slack the largest weights are exactly 2^15, and both roundings together are
+// 1.09 times the output's own against 64 bits; with one of 7 or 8 they are 1.38 times. The kernel for few rows, which
+// waits for its reads, has none (64 tokens 218 us either way, 7 rows 43.4 -> 44.2); in the others the sums would be
+// scaled in most units (chunk 778 -> 825 us, trees 90.8 -> 96.1).
+constexpr float kFewLift = 15.0f;
+constexpr float kWideLift = 8.0f, kWideSlack = 7.0f;
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef short short4_t __attribute__((ext_vector_type(4)));
@@ -249,11 +255,11 @@ __device__ __forceinline__ int narrow_piece(int token, int piece) {
   else return piece ^ ((token & 7) << 1);
 }
 
-// Scores, in powers of two, from which on their rounding matters. The maximum is a rounded product; a score that is held
-// against it by a product and difference in one has no such rounding, and the difference, up to 2^-25 of the score, is a
-// power of two of its own (at a score of 2^30 the largest weight was anything from 2^-32 to 2^32). Rows whose maximum is
-// that far from 0 have every score rounded first: the branch takes 1 % of the time of many rows (chunk 758 -> 765 us,
-// trees 88 -> 89). The kernel for few rows always rounds, which takes it no longer.
+// Scores, in powers of two, from which on their rounding matters. The maximum is a rounded product; a score that is
+// held against it by a product and difference in one has no such rounding, and the difference, up to 2^-25 of the
+// score, is a power of two of its own (at a score of 2^30 the largest weight was anything from 2^-32 to 2^32). Rows
+// whose maximum is that far from 0 have every score rounded first, and no lift: the branch takes 1 % of the time of
+// many rows (chunk 758 -> 765 us, trees 88 -> 89). The kernel for few rows always rounds, which takes it no longer.
 constexpr float kFar = 0x1p20f;
 
 __device__ __forceinline__ float rounded_product(float a, float b) {
@@ -543,7 +549,8 @@ __global__ __launch_bounds__(kThreads, few_blocks(D, QB)) void attention_kernel(
             high = fmaxf(high, x[b][h][e]);
           }
         high = groups_max(high);
-        if (__any(high > top[b] + kSlack)) {
+        if (!is_far(high)) high -= kFewLift;
+        if (__any(high > top[b])) {
           const float now = fmaxf(top[b], high), keep = weight_of(top[b], now);
           top[b] = now;
           part[b] *= keep;
@@ -662,6 +669,10 @@ __global__ __launch_bounds__(kThreads, few_blocks(D, QB)) void attention_kernel(
 }
 
 // ---- many query rows
+
+// What scores are held against. Half of the lift is in the maximum already: a whole one there or here takes a constant
+// more, and 1.5 % of the time. Finite where the row has seen nothing, so that its weights are 0.
+__device__ __forceinline__ float lifted(float top) { return fmaxf(top, -__FLT_MAX__) - kWideLift / 2; }
 
 constexpr int kWide = 64;  // tokens of a unit of work
 constexpr int kWideBits = 8;  // one workgroup on each compute unit
@@ -1010,8 +1021,10 @@ __global__ __launch_bounds__(512) void attention_wide_kernel(AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) high = fmaxf(high, x[b][h][e]);
           auto both = __builtin_amdgcn_permlane32_swap(as_u32(high), as_u32(high), false, false);
-          high = fmaxf(as_f32(both[0]), as_f32(both[1])) * a.scale;
-          if (__any(high > top[b] + kSlack)) {
+          const float most = fmaxf(as_f32(both[0]), as_f32(both[1]));
+          high = __builtin_fmaf(most, a.scale, -kWideLift / 2);
+          if (__any(high > top[b] + kWideSlack)) {
+            if (is_far(high)) high = rounded_product(most, a.scale);
             const float now = fmaxf(top[b], high), keep = weight_of(top[b], now);
             top[b] = now;
             part[b] *= keep;
@@ -1019,7 +1032,7 @@ __global__ __launch_bounds__(512) void attention_wide_kernel(AttnArgs a) {
             for (int e = 0; e < DB; ++e) o[b][e] *= keep;
             far[b] = __any(is_far(now));
           }
-          float less = top[b] == kNone ? 0.0f : top[b];
+          float less = lifted(top[b]);
           if (far[b]) {
             __builtin_amdgcn_sched_barrier(0);  // a branch
 #pragma unroll
@@ -1401,8 +1414,10 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
       // last read two units before it, written from the next turn on
       if (tid < 4) flags[(s + 2) & 3][tid] = 0;
       if (scores) {
-        const float high = fmaxf(meet[pair][0][li], meet[pair][1][li]) * a.scale;
-        if (__any(high > top + kSlack)) {
+        const float most = fmaxf(meet[pair][0][li], meet[pair][1][li]);
+        float high = __builtin_fmaf(most, a.scale, -kWideLift / 2);
+        if (__any(high > top + kWideSlack)) {
+          if (is_far(high)) high = rounded_product(most, a.scale);
           const float now = fmaxf(top, high), keep = weight_of(top, now);
           top = now;
           part *= keep;
@@ -1410,7 +1425,7 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
           for (int e = 0; e < DB; ++e) o[e] *= keep;
           far = __any(is_far(now));
         }
-        float less = top == kNone ? 0.0f : top;
+        float less = lifted(top);
         if (far) {
           __builtin_amdgcn_sched_barrier(0);  // a branch
 #pragma unroll

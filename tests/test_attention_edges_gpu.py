@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 import oracle
+from attention_helpers import attention_bound
 from helpers import assert_within
 from test_step_gpu import attention_case, dev, host, pbg, say  # noqa: F401 (pbg is a fixture)
 
@@ -61,3 +62,29 @@ def test_scores_of_any_size(pbg, heads, kv, d, rows, scale, sign):  # noqa: F811
     ref, size, _ = oracle.tree_attention(**c, scale=scale)
     bound = 2.0 ** -11 * (size + np.abs(ref)) * 1.01 + 2.0 ** -25
     assert_within(run(pbg, c, scale), ref, bound)
+
+
+# heads, kv heads, head_dim, requests, tokens, rows: several units of a request in a workgroup, so that many tokens share a maximum
+LIGHT = [(8, 8, 64, 16, 3000, 1), (8, 8, 128, 16, 3000, 1), (8, 4, 128, 16, 3000, 12), (8, 8, 256, 8, 3000, 2), (8, 8, 64, 4, 3000, 70),
+         (8, 8, 128, 4, 3000, 40), (4, 4, 256, 8, 3000, 33)]
+
+
+@pytest.mark.parametrize("heads,kv,d,requests,tokens,rows", LIGHT)
+@pytest.mark.parametrize("light,where", [(12.3, "last"), (21.45, "first"), (25.2, "first")])
+def test_light_tokens_beside_a_heavy_one(pbg, heads, kv, d, requests, tokens, rows, light, where):  # noqa: F811
+    """One token has nearly all the weight and no value, all others 2^-light of it each: they alone are the output."""
+    say(f"attention light {heads}/{kv} x {d} requests={requests} rows={rows} light={light} heavy={where}")
+    c = attention_case(d + rows, [tokens] * requests, [rows] * requests, heads, kv, d, 16)
+    rng = np.random.default_rng(2)
+    c["q"][:], c["k_cache"][:] = 0, 0
+    c["q"][..., 0] = 1
+    c["k_cache"][..., 0] = -light * np.log(2.0)
+    c["v_cache"][:] = rng.uniform(0.5, 1.5, c["v_cache"].shape)
+    for i in range(requests):
+        set_token(c, i, 0 if where == "first" else tokens - 1, 0, 0)
+    total = np.zeros(c["q"].shape[:2])
+    ref, size, far = oracle.tree_attention(**c, scale=1.0, totals=total)
+    bound = attention_bound(c["q"], c["lengths"], c["row_start"], ref, size, far, total, 1.5, 1.0)
+    # what is tested is well above what is allowed
+    assert (bound < 0.02 * ref).all()
+    assert_within(run(pbg, c, 1.0), ref, bound)
