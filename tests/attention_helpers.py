@@ -19,3 +19,22 @@ def attention_bound(q, lengths, row_start, ref, size, far, total, high, scale):
     e = 2 * (d + 4) * U * scale * far + 30 * U + 2.0 ** -11 + (n / 32 + 64) * U
     off = e[:, :, None] * (size + np.abs(ref)) * 1.01 + n * LOST * high / np.maximum(total, 1.0)[:, :, None]
     return off + (np.abs(ref) + off) * 2.0 ** -11 + 2.0 ** -25
+
+BLOCK = 64  # tokens; every unit of work of every kernel is one or more of these
+
+# heads, kv heads, head_dim, rows of each request, tokens of each request: up to 235 units of 128 tokens or 470 of 64, so
+# that every workgroup of a launch has a piece of the same rows
+LONG = [(4, 1, 128, 1, [30001]), (4, 2, 64, 6, [30001]), (2, 1, 256, 3, [30001]), (12, 2, 128, 4, [30001]), (4, 1, 128, 40, [30001]),
+        (2, 1, 64, 33, [30001]), (2, 1, 256, 40, [30001]), (4, 1, 128, 1, [9000, 12, 14001]), (4, 2, 64, 80, [9000, 12, 14001])]
+
+
+def long_case(heads, kv, d, rows, lengths):
+    """Scores of about one, and values that say where they stand: 1 in the column of the token's block, 0 elsewhere."""
+    from test_step_gpu import attention_case
+
+    c = attention_case(d + rows, lengths, [rows] * len(lengths), heads, kv, d, 16, spread=0.25)
+    c["v_cache"][:] = 0
+    for i, n in enumerate(lengths):
+        t = np.arange(n + rows)
+        c["v_cache"][c["table"][i, t // 16], :, t % 16, t // BLOCK % d] = 1
+    return c

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import oracle
-from attention_helpers import attention_bound
+from attention_helpers import LONG, attention_bound, long_case
 from helpers import assert_within
 from test_step_gpu import attention_case, dev, host, pbg, say  # noqa: F401 (pbg is a fixture)
 
@@ -88,3 +88,13 @@ def test_light_tokens_beside_a_heavy_one(pbg, heads, kv, d, requests, tokens, ro
     # what is tested is well above what is allowed
     assert (bound < 0.02 * ref).all()
     assert_within(run(pbg, c, 1.0), ref, bound)
+
+
+@pytest.mark.parametrize("heads,kv,d,rows,lengths", LONG)
+def test_every_block_of_a_long_request_counts_once(pbg, heads, kv, d, rows, lengths):  # noqa: F811
+    """Requests that every workgroup has a piece of. (A block of tokens left out or taken twice is 4 bounds off: test_attention_edges.)"""
+    say(f"attention long {heads}/{kv} x {d} rows={rows} {lengths}")
+    c = long_case(heads, kv, d, rows, lengths)
+    total = np.zeros(c["q"].shape[:2])
+    ref, size, far = oracle.tree_attention(**c, totals=total)
+    assert_within(run(pbg, c), ref, attention_bound(c["q"], c["lengths"], c["row_start"], ref, size, far, total, 1.0, d ** -0.5))
