@@ -651,7 +651,7 @@ int rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, c
  * fp32 (a row with a score times scale * log2(e) beyond fp32 is not
  * specified). The weights enter the second product rounded to fp16: to 2^-11
  * of themselves, and light ones to 2^-33 of the row's largest (an infinite
- * value that a row sees with a weight below that makes the output NaN).
+ * value that a row sees with a weight below that may make the output NaN).
  */
 #define PBG_ATTENTION_MIN_PAGE 8
 
@@ -692,8 +692,9 @@ int tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v
  *              row has none). Both NULL for none.
  *   out        [m][n] fp32 out; may be logits itself
  *   token, top [m] int32 and [m] fp32 out, both NULL if not wanted: the greedy
- *              token (the lowest on ties) and its value; -1 and -infinity where
- *              no value is above -infinity. NaN is never chosen.
+ *              token (the lowest on ties, zeros of either sign being equal)
+ *              and its value, of a zero +0; -1 and -infinity where no value
+ *              is above -infinity. NaN is never chosen.
  *   workspace  [m][ceil(n / PBG_LOGITS_SLICE)] uint64, 8-byte aligned, of any
  *              content; read only if token is wanted
  * m * n is at most PBG_MAX_LOGITS, tokens_width at most 2^24.
