@@ -580,6 +580,13 @@ int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16
  * ancestors. So do, but for their request, the rows of a tree from the 64th
  * on. Calling it again on the same inputs gives the same tables: nothing is
  * taken from the stack until free_count is set to free_left.
+ * Pages are only taken here; giving back is the caller's. A step opens pages
+ * for all of its rows. If request i keeps only L' <= lengths[i] + (its rows)
+ * tokens of them (drafted rows that were rejected), the pages in its entries
+ * ceil(L' / page_size) .. ceil((lengths[i] + rows) / page_size) - 1 are
+ * nobody's, and the next step opens those entries anew: they are pushed onto
+ * the stack (free_pages[free_left], free_pages[free_left + 1], ...) before it.
+ * L' = 0 gives back all pages of a request that ends.
  * table_width * page_size is at most 2^30, pages * page_size below 2^40.
  */
 int cache_plan(const int32_t* lengths, const int32_t* added, int64_t requests, int32_t* table, int64_t table_width,

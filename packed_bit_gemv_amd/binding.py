@@ -731,6 +731,8 @@ def cache_plan(lengths: torch.Tensor, added: torch.Tensor, table: torch.Tensor, 
     makes each request's rows a tree of drafted tokens (of at most 64). The step has as many rows as the outputs that
     are given, or `rows`: request, position int32 [rows], slot int64 [rows] (-1 for rows behind the last request),
     row_start int32 [requests + 1], ancestors int64 [rows] (bit masks over the request's rows; allocated for a tree).
+    Pages are only taken: those that rows which are not kept opened, and those of requests that end, go back onto the
+    stack by the caller before the next step.
     """
     i32, i64 = torch.int32, torch.int64
     requests, width, dev = _matrix(table, "table", i32)
