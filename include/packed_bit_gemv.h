@@ -564,7 +564,10 @@ int lora_add(const float* y, const uint16_t* x, const int32_t* ids, const uint16
  *               int32: the rows of each request form a tree, parents[a] being
  *               the index inside the request (0 is its first row) of the row
  *               that row a follows; a parent that does not come before its
- *               row means that the row follows the cached tokens.
+ *               row means that the row follows the cached tokens. A tree has
+ *               at most PBG_MAX_TREE rows, and so has a prompt (each row the
+ *               parent of the next) in a call with parents: longer ones need
+ *               a call without.
  *   row_start   [requests + 1] int32 out
  *   request     [m] int32 out: the row's request
  *   position    [m] int32 out: the length plus the number of rows between the
@@ -634,8 +637,12 @@ int rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, c
  * a = row_start[i] + c sees: t < lengths[i], and of the rows of its own step
  * the tokens lengths[i] + c' for which bit c' of ancestors[a] is set, or,
  * where ancestors is NULL, those with c' <= c. One decoded token, a tree of
- * drafted tokens and a prompt's rows are all calls of this one, and may stand
- * side by side in one. Tokens in a place without a page are not seen. A row
+ * drafted tokens and a prompt's rows are all calls of this one. Side by side
+ * in one call may stand, with ancestors, trees, tokens and prompts of at most
+ * PBG_MAX_TREE rows each, and without, tokens and prompts of any length. A
+ * step that has both trees and longer prompts is two calls, of cache_plan
+ * and of this one, on the requests of either kind (rotary_qkv takes the rows
+ * of both at once). Tokens in a place without a page are not seen. A row
  * whose weights add to zero (it sees nothing, or only scores of -infinity) is
  * all zeros. What the cache holds in places that a row does not see (NaN
  * included) does not reach it.
@@ -646,7 +653,8 @@ int rotary_qkv(const float* qkv, const int32_t* position, const int64_t* slot, c
  *   row_start  [requests + 1] int32, as from cache_plan. Rows behind the last
  *              request are left as they were.
  *   ancestors  [m] uint64, or NULL; of a request's rows from the 64th on none
- *              is seen
+ *              is seen, so that NULL belongs here wherever a request of rows
+ *              one after another adds more than PBG_MAX_TREE of them
  *   scale      > 0, and finite also times log2(e)
  *   out        [m][heads][head_dim] fp16 bits out, 16-byte aligned
  *   workspace  device, 16-byte aligned, pbg_attention_workspace_bytes(...)
@@ -689,8 +697,9 @@ int tree_attention(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v
  *              of the prompt. Tokens outside [0, n) are passed over.
  *   repetition, frequency, presence  [requests] fp32
  *   drafts, row_start, ancestors  all NULL, or the drafted token of each row [m]
- *              int32 and the tables of cache_plan: the tokens of a row's
- *              ancestors (itself among them) count as output
+ *              int32 (outside [0, n) for rows that are no draft, a prompt's)
+ *              and the tables of cache_plan: the tokens of a row's ancestors
+ *              (itself among them) count as output
  *   bias_start [requests + 1] int32, bias_token, bias_value [bias_entries]:
  *              request i's list is entries bias_start[i] .. bias_start[i + 1] - 1;
  *              of a token listed twice the last entry counts. All NULL for none.

@@ -728,7 +728,8 @@ def cache_plan(lengths: torch.Tensor, added: torch.Tensor, table: torch.Tensor, 
     lengths, added int32 [requests]: the tokens that each request has in the cache and the rows that it adds. table
     int32 [requests, width] is read and, for pages that the step opens, written; free_pages int32 [n] is a stack of
     free pages with free_count int32 [1] of them left, free_left int32 [1] what the step leaves. parents int32 [rows]
-    makes each request's rows a tree of drafted tokens (of at most 64). The step has as many rows as the outputs that
+    makes each request's rows a tree of drafted tokens, of at most 64 (from the 64th on a row has no place: prompts that
+    are longer need a call without parents). The step has as many rows as the outputs that
     are given, or `rows`: request, position int32 [rows], slot int64 [rows] (-1 for rows behind the last request),
     row_start int32 [requests + 1], ancestors int64 [rows] (bit masks over the request's rows; allocated for a tree).
     Pages are only taken: those that rows which are not kept opened, and those of requests that end, go back onto the
@@ -841,7 +842,8 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     q as rotary_qkv leaves it; k_cache, v_cache fp16 [pages, kv_heads, page_size, head_dim], which hold the step's own
     keys and values already; table int32 [requests, width]; lengths int32 [requests], the tokens before the step;
     row_start int32 [requests + 1] and ancestors int64 [m] from cache_plan. Each row sees its request's tokens from
-    before the step, and of the step's own those of its ancestors, or without ancestors those up to itself. scale
+    before the step, and of the step's own those of its ancestors, or without ancestors those up to itself. Ancestors
+    reach over the first 64 rows of a request: leave them out for longer prompts. scale
     defaults to 1 / sqrt(head_dim). A row that sees nothing is zero; rows behind the last request are left as they were.
     """
     pages, kv_heads, page_size, head_dim, dev = _cache(k_cache, v_cache)
