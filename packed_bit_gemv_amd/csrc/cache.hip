@@ -227,10 +227,26 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
     for (int j = 0; j < 4; ++j) sum += y0[j] * y0[j] + y1[j] * y1[j];
 #pragma unroll
     for (int k = LPH / 2; k > 0; k /= 2) sum += __shfl_xor(sum, k);
+    float eps = a.eps;
+    if (__any(sum > __FLT_MAX__)) {
+      // Squares that leave fp32: such a head is taken times 2^-70, which its norm takes out again. (An infinite element
+      // stays infinite.)
+      const bool large = sum > __FLT_MAX__ && weight && !is_v;
+      const float down = large ? 0x1p-70f : 1.0f;
+      y0 *= down;
+      y1 *= down;
+      float less = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) less += y0[j] * y0[j] + y1[j] * y1[j];
+#pragma unroll
+      for (int k = LPH / 2; k > 0; k /= 2) less += __shfl_xor(less, k);
+      if (large) sum = less;
+      eps *= down * down;
+    }
     if (head >= all || !mine) continue;
     if (!is_v) {
       if (weight) {
-        const float norm = 1.0f / sqrtf(sum / static_cast<float>(d) + a.eps);
+        const float norm = 1.0f / sqrtf(sum / static_cast<float>(d) + eps);
         const f32x4_t w0 = *reinterpret_cast<const f32x4_any_t*>(weight + e0);
         const f32x4_t w1 = *reinterpret_cast<const f32x4_any_t*>(weight + e1);
         y0 *= w0 * norm;
