@@ -1024,8 +1024,10 @@ __global__ __launch_bounds__(512) void attention_wide_kernel(AttnArgs a) {
           const float most = fmaxf(as_f32(both[0]), as_f32(both[1]));
           high = __builtin_fmaf(most, a.scale, -kWideLift / 2);
           if (__any(high > top[b] + kWideSlack)) {
+            // of the rows that pass it: what other rows see does not change a row's bits
+            const bool passes = high > top[b] + kWideSlack;
             if (is_far(high)) high = rounded_product(most, a.scale);
-            const float now = fmaxf(top[b], high), keep = weight_of(top[b], now);
+            const float now = passes ? high : top[b], keep = weight_of(top[b], now);
             top[b] = now;
             part[b] *= keep;
 #pragma unroll
@@ -1417,8 +1419,9 @@ __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
         const float most = fmaxf(meet[pair][0][li], meet[pair][1][li]);
         float high = __builtin_fmaf(most, a.scale, -kWideLift / 2);
         if (__any(high > top + kWideSlack)) {
+          const bool passes = high > top + kWideSlack;
           if (is_far(high)) high = rounded_product(most, a.scale);
-          const float now = fmaxf(top, high), keep = weight_of(top, now);
+          const float now = passes ? high : top, keep = weight_of(top, now);
           top = now;
           part *= keep;
 #pragma unroll

@@ -98,3 +98,27 @@ def test_every_block_of_a_long_request_counts_once(pbg, heads, kv, d, rows, leng
     total = np.zeros(c["q"].shape[:2])
     ref, size, far = oracle.tree_attention(**c, totals=total)
     assert_within(run(pbg, c), ref, attention_bound(c["q"], c["lengths"], c["row_start"], ref, size, far, total, 1.0, d ** -0.5))
+
+
+@pytest.mark.parametrize("heads,kv,d,rows", [(4, 1, 128, 4), (2, 1, 256, 6), (8, 1, 64, 4), (32, 32, 128, 12), (32, 32, 64, 60),
+                                              (32, 32, 128, 60), (32, 32, 256, 60)])
+@pytest.mark.parametrize("tree", [True, False])
+def test_scores_that_a_row_does_not_see_do_not_change_it(pbg, heads, kv, d, rows, tree):  # noqa: F811
+    """A row's token with scores far above all others, finite: rows that do not see it keep their bits. (The first lengths: several units in a
+    workgroup, whose maxima are raised between them.)"""
+    say(f"attention unseen scores {heads}/{kv} x {d} rows={rows} tree={tree}")
+    for lengths in ([700, 650], [0, 9], [61, 63]):
+        c = attention_case(d + rows + lengths[0], lengths, [rows, rows], heads, kv, d, 16, tree=tree, spread=1.0)
+        # tokens before the step score lower than its own
+        for t in range(lengths[0]):
+            page, off = c["table"][0, t // 16], t % 16
+            c["k_cache"][page, :, off] *= np.float16(0.1)
+        for times, scale, row in [(x, None, y) for x in (3, 30, 300) for y in (0, rows // 2, rows - 1)] + [(60000, 1.0, rows // 2)]:
+            base = run(pbg, c, scale)
+            bad = {k: None if v is None else v.copy() for k, v in c.items()}
+            q = bad["q"][row, 0].astype(np.float32)
+            set_token(bad, 0, lengths[0] + row, np.clip(q * times, -60000, 60000))
+            got = run(pbg, bad, scale)
+            sees = np.array([(int(c["ancestors"][a]) >> row & 1) if tree else a >= row for a in range(rows)] + [False] * rows, bool)
+            assert sees.any() and np.isfinite(got).all()
+            assert np.array_equal(got[~sees].view(np.uint16), base[~sees].view(np.uint16)), (lengths, times, row)
