@@ -691,8 +691,8 @@ constexpr int kWideBits = 8;  // one workgroup on each compute unit
 // unit's keys and values one turn early; K(s) is read in turns 2 s and 2 s + 1,
 // V(s) in 2 s + 2 and 2 s + 3, so keys need two buffers and values three.
 //
-// 4,096 rows over 8,192 tokens and themselves (32 heads over 8 of 128) take 750
-// us, 916 TFLOP/s: a unit takes 2.3 us, of which its products are 0.9, its
+// 4,096 rows over 8,192 tokens and themselves (32 heads over 8 of 128) take 752
+// us, 914 TFLOP/s: a unit takes 2.3 us, of which its products are 0.9, its
 // exponentials and the rest of the vector instructions 1.0 and its LDS reads
 // 0.9, each on units of their own. Without the loads it would be 670, without
 // the exponentials 690.
@@ -729,7 +729,7 @@ __global__ __launch_bounds__(512) void attention_wide_kernel(AttnArgs a) {
   int64_t base = line.base;
 
   // The end of a tile that another workgroup began comes last: all then walk the tokens from the first on at about the
-  // same time, and find the keys that they share in the cache (750 us of the above; in the line's order 771).
+  // same time, and find the keys that they share in the cache (771 -> 750 us of the above when it was done).
   const Place begun = place_of(r, line.begin - base);
   const int64_t begun_end = begun.step == 0 ? line.begin : min(line.begin + begun.steps - begun.step, line.end);
   int64_t stop = line.end;
@@ -1119,9 +1119,10 @@ __device__ __forceinline__ int afresh(int v) {
 // the products of unit s the waves that come first store K(s + 1) and V(s), the others K(s + 2) and V(s + 1). K(s) is
 // read in turns 2 s and 2 s + 1, V(s) in 2 s + 2 and 2 s + 3.
 //
-// 4,096 rows over 8,192 tokens and themselves (16 heads over 4) take 877 us, 784 TFLOP/s (one wave with 32 rows of its
-// own 2,144); 16 trees of 31 to 61 rows over 2,050 to 4,100 tokens 104 (266). What the other kernel's unit costs, and
-// the way of the weights through LDS.
+// 4,096 rows over 8,192 tokens and themselves (16 heads over 4) take 900 us, 764 TFLOP/s (one wave with 32 rows of its
+// own 2,144); 16 trees of 31 to 61 rows over 2,050 to 4,100 tokens 105 (266). Matrix cores busy 34 % of the cycles,
+// vector units 42 %, LDS 31 %, where the other kernel has 44, 48 and 28: the weights' way through LDS and the addresses
+// made again are what is longer.
 constexpr int kPairRows = 128;  // query rows of a tile: four pairs of waves
 
 __global__ __launch_bounds__(512) void attention_pairs_kernel(AttnArgs a) {
@@ -1652,8 +1653,8 @@ hipError_t launch_few(const AttnArgs& args, void* ws, hipStream_t stream) {
 // Without a tree, requests with at most 16 query rows a key head go through the kernel for few rows, also here:
 // single tokens beside a prompt. 63 tokens of requests of 4,096 beside a prompt of 1,024 rows take 256 us, all
 // through the wide kernel 422. Where there are none the launch costs 7 us with its part of the join (of 771 for 4,096
-// rows over 8,192 tokens), which trees, whose sizes are alike, do not pay (16 trees of 30 to 61 rows: 87 us, 94 with
-// it), nor does one request, nor heads of which more than 16 share a key head.
+// rows over 8,192 tokens), which calls with a tree do not pay (16 trees of 30 to 61 rows: 87 us, 94 with it; single
+// tokens among them take the wide kernel), nor does one request, nor heads of which more than 16 share a key head.
 template <int D>
 hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
   constexpr int R = wide_rows(D), groups = 1 << few_bits(D, 1);
@@ -1677,7 +1678,10 @@ hipError_t launch_wide(const AttnArgs& args, void* ws, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Which kernel, by the query rows of a key head that a request has on average. Eight requests of up to 8,192 tokens
+// Which kernel, by the query rows of a key head that a request has on average, which is what the host knows; rows
+// behind the last request and requests without rows count like others. It suits requests that are alike, and a prompt
+// that an average hides among many tokens is slow in small tiles: 255 tokens over 1,000 with a prompt of 512 rows over
+// 8,192 take 724 us, in calls of their own 197 and 108. Eight requests of up to 8,192 tokens
 // at head_dim 128: 20 rows take 74.5 us in tiles of 16, 61.7 in tiles of 32 and 62.5 in the wide kernel; 28 rows
 // 90.1, 62.4 and 63.0; 48 rows 93.9 in tiles of 48, 128.6 in tiles of 64 and 67.4 in the wide kernel. One row each of
 // 64 requests: 217 us in tiles of 16, 291 in tiles of 32, 829 wide. At head_dim 256, where a tile of 32 does not fit
